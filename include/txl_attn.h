@@ -14,7 +14,8 @@
  *
  * Conventions shared by every entry point
  *   - All tensors are dense, contiguous, row-major, on the current CUDA
- *     device; every pointer argument is a DEVICE pointer.  The caller owns
+ *     device; every pointer argument is a DEVICE pointer unless the call says
+ *     otherwise.  The caller owns
  *     every buffer; the library never allocates, frees or retains them.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream) and never synchronise the host, except
@@ -338,6 +339,86 @@ int txl_linear(const void* x, int x_layout, int B, int T, int K, const void* w, 
                const void* bias, const void* resid, int relu, void* out, void* stream);
 int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
                    int d, float eps, void* out, void* stream);
+
+/*
+ * LayerNorm for training: txl_layer_norm's forward that also keeps each row's
+ * statistics, and its gradients.  Any row length 1 <= d <= 16384
+ * (TXL_ERR_UNSUPPORTED beyond), any number of rows (0 too), dtype TXL_BF16 or
+ * TXL_F32 for x, y, gamma, beta, out, dout, dres and dx; statistics and
+ * parameter gradients fp32.
+ *
+ * txl_layer_norm_fwd: with z = x + y (y may be null),
+ *   mean[r] = sum z / d, rstd[r] = (sum (z - mean)^2 / d + eps)^(-1/2),
+ *   out = (z - mean) rstd gamma + beta.  mean, rstd: [rows].
+ * txl_layer_norm_bwd: from dout, the gradient of out, and the forward's inputs
+ *   and statistics: dx [rows, d], the gradient of x and of y alike, plus dres
+ *   (may be null: the gradient that reaches z along a residual path);
+ *   dgamma, dbeta [d], summed over the rows in a fixed order (the same inputs
+ *   give the same bits; zeros when rows = 0).
+ *
+ * All pointers 16-byte aligned (TXL_ERR_MISALIGNED; with rows = 0 those of
+ * row data are not looked at).  Outputs overlap neither inputs nor each other
+ * (TXL_ERR_ALIAS).  workspace: device memory, 256-byte aligned, at least
+ * txl_layer_norm_bwd_workspace_bytes(...) bytes (TXL_ERR_WORKSPACE), overlapping
+ * no other argument (TXL_ERR_ALIAS); concurrent calls use distinct ones.
+ */
+int txl_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
+                       int d, float eps, void* out, float* mean, float* rstd, int dtype, void* stream);
+size_t txl_layer_norm_bwd_workspace_bytes(long long rows, int d, int dtype);
+int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
+                       const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
+                       float* dbeta, int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * txl_adamw_step: one AdamW step over n_tensors tensors.  `tensors` is an array
+ * in HOST memory, read during the call; tensor i has n elements (0: skipped),
+ * a parameter, a gradient and a weight decay of its own.  With g the gradient
+ * times the clip factor and t the step's number (the first step is 1),
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p - lr (weight_decay p + m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)),
+ * in fp32.  param_dtype TXL_F32: p is the parameter (master null).  TXL_BF16: p
+ * is the fp32 copy in `master`, and the parameter is written as its rounding.
+ * grad_dtype: TXL_F32 or TXL_BF16.
+ *
+ * Flat state: tensor i's state starts at element 256 * (sum over j < i of
+ * ceil(n_j / 256)) of master, exp_avg and exp_avg_sq; the elements between a
+ * tensor's end and the next start are the library's (start them at zero).
+ * txl_adamw_state_elements gives the length (-1: invalid or above 2^38).
+ *   state_bits 32: exp_avg, exp_avg_sq hold m and v in fp32 (the scales null).
+ *   state_bits 8: exp_avg holds e4m3 codes of m, exp_avg_sq of sqrt(v), each
+ *     block of 256 elements with one fp32 scale in exp_avg_scale and
+ *     exp_avg_sq_scale (value = code * scale); codes are rounded up or down at
+ *     random, the mean kept, from `seed`, the step's number and the element's index.
+ * All of it starts at zero, master at the parameters' values.
+ *
+ * steps (device): number of steps done, advanced by the call.  lr (device): the
+ * learning rate.  Both are read when the step runs, so a captured step can be
+ * replayed and lr changed between replays.  max_norm > 0: gradients are scaled
+ * by min(1, max_norm / norm) with norm the 2-norm of all gradients (their sum of
+ * squares must stay in fp32's range), written to grad_norm (device, may be
+ * null); a norm that is not finite leaves parameters, states and steps as
+ * they were.  max_norm = 0: no clipping, grad_norm untouched.
+ *
+ * Parameters, gradients and flat buffers 16-byte aligned, steps 8-byte
+ * (TXL_ERR_MISALIGNED).  What is written overlaps nothing else
+ * (TXL_ERR_ALIAS); gradients may share memory.  workspace as for
+ * txl_layer_norm_bwd, of txl_adamw_workspace_bytes(...) bytes.  betas in
+ * [0, 1), eps >= 0, max_norm >= 0 and finite (TXL_ERR_INVALID_ARG).
+ */
+typedef struct txl_adamw_tensor {
+    void* param;
+    const void* grad;
+    long long n;
+    float weight_decay;
+    int reserved; /* 0 */
+} txl_adamw_tensor;
+long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors);
+size_t txl_adamw_workspace_bytes(const txl_adamw_tensor* tensors, int n_tensors);
+int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dtype, int grad_dtype,
+                   int state_bits, float* master, void* exp_avg, float* exp_avg_scale, void* exp_avg_sq,
+                   float* exp_avg_sq_scale, long long* steps, const float* lr, double beta1, double beta2,
+                   double eps, double max_norm, unsigned seed, float* grad_norm, void* workspace,
+                   size_t ws_bytes, void* stream);
 
 /*
  * Tail_M memory roll, in place ("Transformer-XL" notes, section

@@ -11,6 +11,9 @@ Public API (all computation runs in libtxl.so's CUDA kernels):
     qkv_proj, r_proj                              head-split input projections (tensor cores)
     qkvr_proj                                     both in one launch
     linear, layer_norm                            o_net / feed-forward GEMMs, fused residual LayerNorm
+    layer_norm_fwd, layer_norm_bwd                LayerNorm keeping its row statistics, and its gradients
+    layer_norm_bwd_workspace_bytes                scratch of the latter
+    AdamW                                         AdamW over many tensors, 32-bit or 8-bit states
     sync_status, check_status                     device status word
     bounds_status                                 first out-of-range access (bounds-checked build)
     SegmentDriver                                 multi-segment, multi-layer driver (caller's projections)
@@ -23,8 +26,10 @@ from ._lib import (TXL_BF16, TXL_F32, TxlError, attn_bwd, attn_bwd_workspace_byt
                    status_string,
                    sync_status, version, LIB_PATH)
 from .driver import AttnStack, DecoderStack, SegmentDriver
+from .train import AdamW, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd
 
 __all__ = ["TXL_BF16", "TXL_F32", "TxlError", "attn_bwd", "attn_bwd_workspace_bytes", "attn_fwd", "attn_fwd_lse", "attn_fwd_noalloc", "attn_fwd_ws",
            "attn_workspace_bytes", "bounds_status",
            "check_status", "debug_inject", "header_functions", "layer_norm", "linear", "load", "mem_reset", "mem_ring_push", "mem_update", "qkv_proj", "qkvr_proj", "r_proj",
-           "status_string", "sync_status", "version", "SegmentDriver", "AttnStack", "DecoderStack", "LIB_PATH"]
+           "status_string", "sync_status", "version", "SegmentDriver", "AttnStack", "DecoderStack", "AdamW", "layer_norm_fwd",
+           "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "LIB_PATH"]

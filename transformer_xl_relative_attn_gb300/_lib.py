@@ -33,6 +33,13 @@ STATUS = {
     -10: "TXL_ERR_OUT_OF_BOUNDS",
 }
 
+
+class AdamwTensor(ctypes.Structure):
+    """txl_adamw_tensor: one tensor of txl_adamw_step's table."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("n", ctypes.c_longlong),
+                ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -94,6 +101,20 @@ def load() -> ctypes.CDLL:
         lib.txl_linear.restype = i
         lib.txl_layer_norm.argtypes = [vp, vp, vp, vp, ctypes.c_longlong, i, f, vp, vp]
         lib.txl_layer_norm.restype = i
+        ll, dbl, table = ctypes.c_longlong, ctypes.c_double, ctypes.POINTER(AdamwTensor)
+        lib.txl_layer_norm_fwd.argtypes = [vp] * 4 + [ll, i, f] + [vp] * 3 + [i, vp]
+        lib.txl_layer_norm_fwd.restype = i
+        lib.txl_layer_norm_bwd_workspace_bytes.argtypes = [ll, i, i]
+        lib.txl_layer_norm_bwd_workspace_bytes.restype = sz
+        lib.txl_layer_norm_bwd.argtypes = [vp] * 7 + [ll, i] + [vp] * 3 + [i, vp, sz, vp]
+        lib.txl_layer_norm_bwd.restype = i
+        lib.txl_adamw_state_elements.argtypes = [table, i]
+        lib.txl_adamw_state_elements.restype = ll
+        lib.txl_adamw_workspace_bytes.argtypes = [table, i]
+        lib.txl_adamw_workspace_bytes.restype = sz
+        lib.txl_adamw_step.argtypes = ([table] + [i] * 4 + [vp] * 7 + [dbl] * 4 + [ctypes.c_uint] +
+                                       [vp, vp, sz, vp])
+        lib.txl_adamw_step.restype = i
         lib.txl_mem_update_ext.argtypes = [vp, vp] + [i] * 6 + [vp]
         lib.txl_mem_update_ext.restype = i
         lib.txl_mem_reset.argtypes = [vp, vp] + [i] * 4 + [vp]
@@ -117,7 +138,7 @@ def header_functions() -> list[str]:
     with open(HEADER, encoding="utf-8") as fh:
         text = fh.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(txl_\w+)\s*\(", text, flags=re.M)
+    return re.findall(r"^\s*(?:const\s+)?(?:long\s+)?\w+\s*\*?\s*(txl_\w+)\s*\(", text, flags=re.M)
 
 
 def status_string(code: int) -> str:

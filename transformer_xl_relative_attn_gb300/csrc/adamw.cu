@@ -1,0 +1,486 @@
+// One AdamW step over many tensors.  With g the gradient (times the clip
+// factor c = min(1, max_norm / |all gradients|) where max_norm is given), t
+// the step's number and every product and sum in fp32,
+//
+//   m = b1 m + (1 - b1) g        v = b2 v + (1 - b2) g g
+//   p = p - (lr wd p + lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps))
+//
+// p is an fp32 parameter, or the fp32 master copy of a bf16 one (which is
+// written as the master's rounding).  The decay is subtracted as lr wd p, not
+// as a factor 1 - lr wd: with lr wd = 1e-6 that factor would be 6 % off in fp32.
+//
+// States.  The tensors' states lie one behind the other in flat buffers, each
+// tensor starting at a multiple of 256 elements.  One warp owns one such block
+// of 256 (8 elements per lane), so a block's scale in the 8-bit form needs one
+// warp reduction and no shared memory.  In 32 bits the buffers hold m and v.
+// In 8 bits they hold e4m3 codes of m / s and sqrt(v) / s', with s the block's
+// largest magnitude / 448.  sqrt(v) rather than v because its range is half as
+// many octaves, and e4m3 covers 18 of them.  Codes are rounded up or down at
+// random with the value kept in the mean: under round-to-nearest, a moving
+// average that changes by 0.1 % a step would never leave a code 3 mantissa bits
+// wide.  The 32 random bits of an element are a hash of (seed, step, its index):
+// the same inputs give the same bits.  A non-zero sqrt(v) is never rounded to 0,
+// which bounds m / sqrt(v) of the next step.  A block whose largest magnitude is
+// not above 2^-110 is stored as zeros; one that is not finite gets a scale that
+// is not finite.
+//
+// The step's number, the learning rate and the clip factor are device values:
+// a step can be captured in a graph and replayed.  A first launch sums g g
+// (only with max_norm), a one-CTA launch turns it into the step's coefficients
+// and advances the step, and the third launch updates.  A norm that is not finite
+// leaves everything as it was.
+//
+// The tensor table travels in the kernel's parameters (32 bytes per tensor):
+// no table in device memory to keep in step with the host's.
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "adamw.h"
+#include "txl_device.cuh"
+
+namespace txl {
+
+namespace {
+
+constexpr int kPerCta = 32;  // blocks per CTA (4 per warp)
+
+// What the update launch needs of this step, written by adamw_coef_kernel.
+struct AdamwCoef {
+    float clip;       // factor of the gradients
+    float step_size;  // lr / (1 - b1^t)
+    float root_corr;  // 1 / sqrt(1 - b2^t)
+    float lr;
+    unsigned key;  // hash key of the step
+    int skip;      // the gradient norm is not finite
+};
+
+struct AdamwEntry {
+    void* p;
+    const void* g;
+    long long n;
+    unsigned start;  // first block, relative to the launch's first
+    float wd;
+};
+
+// Tables of two sizes: a launch copies its parameters, so a short list should
+// not pay for a long one.
+template <int CAP>
+struct AdamwTable {
+    int n;
+    AdamwEntry e[CAP];
+};
+
+struct AdamwFlat {
+    float* master;
+    void* m;
+    float* ms;
+    void* v;
+    float* vs;
+};
+
+// 32-bit integer hash: xor-shifts and odd multipliers, every input bit reaching
+// every output bit.
+__host__ __device__ __forceinline__ unsigned mix32(unsigned h) {
+    h ^= h >> 16;
+    h *= 0x6C8E9CF5u;
+    h ^= h >> 15;
+    h *= 0x2B7E1517u;
+    return h ^ (h >> 16);
+}
+
+// The larger of two magnitudes, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max_nan(float a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// q >= 0 to a neighbouring e4m3 value, up with the probability of the fraction
+// by 16 random bits.  e4m3 keeps 3 mantissa bits, so 20 bits of the fp32
+// pattern are cut off after the random bits were added below the cut; its
+// subnormals (below 2^-6) step by 2^-9, which are the steps of the numbers
+// from 2^-6 on, so they are moved there and back.
+__device__ __forceinline__ float round_e4m3(float q, unsigned r16) {
+    const bool low = q < 0x1p-6f;
+    const float t = low ? __fadd_rn(q, 0x1p-6f) : q;
+    const float c = __uint_as_float((__float_as_uint(t) + (r16 << 4)) & 0xFFF00000u);
+    return fminf(low ? __fadd_rn(c, -0x1p-6f) : c, 448.f);
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&f)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+template <typename T>
+__device__ __forceinline__ float load1(const T* p) {
+    return static_cast<float>(*p);
+}
+__device__ __forceinline__ void store1(float* p, float f) { *p = f; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
+
+// Elements i .. i+3 of a tensor of n (0 behind its end).
+template <typename T>
+__device__ __forceinline__ void load4_tail(const T* p, long long i, long long n, float (&f)[4]) {
+    if (i + 4 <= n) {
+        load4(p + i, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = i + k < n ? load1(p + i + k) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4_tail(T* p, long long i, long long n, const float (&f)[4]) {
+    if (i + 4 <= n) {
+        store4(p + i, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n) store1(p + i + k, f[k]);
+    }
+}
+
+// The entry that block b lies in: the last whose start is not behind it.
+template <int CAP>
+__device__ __forceinline__ int find_entry(const AdamwTable<CAP>& t, unsigned b) {
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.e[mid].start <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Sum of g g over each CTA's blocks: part[blockIdx.x].
+template <typename G, int CAP>
+__global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__ AdamwTable<CAP> t,
+                                                         unsigned n_blocks, float* __restrict__ part) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float sh[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned b0 = blockIdx.x * kPerCta;
+    int e = find_entry(t, b0);
+    float s = 0.f;
+    for (int k = warp; k < kPerCta && b0 + k < n_blocks; k += 8) {
+        const unsigned b = b0 + k;
+        while (e + 1 < t.n && t.e[e + 1].start <= b) ++e;
+        const long long i = (long long)(b - t.e[e].start) * kAdamwBlock + lane * 4;
+        float g[2][4];
+        load4_tail(static_cast<const G*>(t.e[e].g), i, t.e[e].n, g[0]);
+        load4_tail(static_cast<const G*>(t.e[e].g), i + 128, t.e[e].n, g[1]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s = fmaf(g[x >> 2][x & 3], g[x >> 2][x & 3], s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) sh[warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float a = 0.f;
+        for (int w = 0; w < 8; ++w) a += sh[w];
+        part[blockIdx.x] = a;
+    }
+}
+
+// The step's coefficients, from the partial sums of g g (max_norm = 0: no clipping).
+__global__ void __launch_bounds__(1024) adamw_coef_kernel(const float* __restrict__ part, unsigned n_part,
+                                                          double beta1, double beta2, double max_norm, unsigned seed,
+                                                          const float* lr, long long* steps, float* grad_norm,
+                                                          AdamwCoef* coef) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ double sh[32];
+    __shared__ double corr[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double s = 0.0;
+    for (unsigned i = threadIdx.x; i < n_part; i += blockDim.x) s += part[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) sh[warp] = s;
+    const long long t = *steps + 1;
+    if (threadIdx.x < 2) corr[threadIdx.x] = 1.0 - pow(threadIdx.x ? beta2 : beta1, (double)t);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    AdamwCoef c = {1.f, 0.f, 0.f, *lr, mix32(seed + (unsigned)t * 0x9E3779B1u), 0};
+    if (max_norm > 0.0) {
+        double a = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) a += sh[w];
+        const double norm = sqrt(a);
+        if (grad_norm) *grad_norm = (float)norm;
+        c.skip = !(norm < (double)INFINITY);
+        c.clip = norm > max_norm ? (float)(max_norm / norm) : 1.f;
+    }
+    c.step_size = (float)((double)c.lr / corr[0]);
+    c.root_corr = (float)(1.0 / sqrt(corr[1]));
+    if (!c.skip) *steps = t;
+    *coef = c;
+}
+
+// One block's state in 8 bits: codes (4 per 32-bit word) and scale of x.
+// keep: what is not zero stays so.
+template <bool KEEP>
+__device__ __forceinline__ float quantize(const float (&x)[8], const unsigned (&r16)[8], unsigned (&code)[2]) {
+    float a = fabsf(x[0]);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) a = max_nan(a, fabsf(x[k]));
+    a = warp_max_nan(a);
+    const bool fine = a > 0x1p-110f && a < INFINITY;
+    const float inv = fine ? __fmul_rn(__frcp_rn(a), 448.f) : 0.f;
+    float q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float t = fine ? __fmul_rn(fabsf(x[k]), inv) : 0.f;
+        q[k] = round_e4m3(t, r16[k]);
+        if (KEEP && t > 0.f) q[k] = fmaxf(q[k], 0x1p-9f);
+        q[k] = copysignf(q[k], x[k]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+        const unsigned hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+        code[h] = lo | (hi << 16);
+    }
+    // a NaN is not above the limit, and stays
+    return a <= 0x1p-110f ? 0.f : __fmul_rn(a, 1.f / 448.f);
+}
+
+__device__ __forceinline__ void codes_to_float(unsigned w, float s, float* f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * h)), __NV_E4M3);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
+        f[2 * h] = __fmul_rn(v.x, s);
+        f[2 * h + 1] = __fmul_rn(v.y, s);
+    }
+}
+
+// The update.  P: type of the parameters (bf16 with a master copy), G: of the
+// gradients.  `first`: the launch's first block in the flat buffers.
+template <typename P, typename G, bool EIGHT, int CAP>
+__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks,
+                                                    unsigned first, const AdamwFlat flat, float b1, float b1c,
+                                                    float b2, float b2c, float eps,
+                                                    const AdamwCoef* __restrict__ coef) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr bool MASTER = sizeof(P) == 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned b0 = blockIdx.x * kPerCta;
+    const AdamwCoef c = *coef;
+    if (c.skip) return;
+    int e = find_entry(t, b0);
+    for (int k = warp; k < kPerCta && b0 + k < n_blocks; k += 8) {
+        const unsigned b = b0 + k;
+        while (e + 1 < t.n && t.e[e + 1].start <= b) ++e;
+        const long long n = t.e[e].n;
+        const long long i = (long long)(b - t.e[e].start) * kAdamwBlock + lane * 4;
+        P* const pp = static_cast<P*>(t.e[e].p);
+        const G* const gp = static_cast<const G*>(t.e[e].g);
+        const float decay = t.e[e].wd * c.lr;
+        const size_t blk = (size_t)first + b, at = blk * kAdamwBlock + lane * 4;
+        float g[8], p[8], m[8], v[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            load4_tail(gp, i + 128 * h, n, *reinterpret_cast<float(*)[4]>(g + 4 * h));
+            if (MASTER)
+                load4(flat.master + at + 128 * h, *reinterpret_cast<float(*)[4]>(p + 4 * h));
+            else
+                load4_tail(reinterpret_cast<const float*>(pp), i + 128 * h, n, *reinterpret_cast<float(*)[4]>(p + 4 * h));
+        }
+        if (EIGHT) {
+            const uint8_t* mc = static_cast<const uint8_t*>(flat.m) + at;
+            const uint8_t* vc = static_cast<const uint8_t*>(flat.v) + at;
+            const float ms = flat.ms[blk], vs = flat.vs[blk];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                codes_to_float(*reinterpret_cast<const unsigned*>(mc + 128 * h), ms, m + 4 * h);
+                codes_to_float(*reinterpret_cast<const unsigned*>(vc + 128 * h), vs, v + 4 * h);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = __fmul_rn(v[x], v[x]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load4(static_cast<const float*>(flat.m) + at + 128 * h, *reinterpret_cast<float(*)[4]>(m + 4 * h));
+                load4(static_cast<const float*>(flat.v) + at + 128 * h, *reinterpret_cast<float(*)[4]>(v + 4 * h));
+            }
+        }
+        float root[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            // each product and sum rounded by itself: what the states become does not hang on
+            // how the compiler fuses them
+            const float gs = __fmul_rn(g[x], c.clip);
+            m[x] = __fadd_rn(__fmul_rn(m[x], b1), __fmul_rn(gs, b1c));
+            v[x] = __fadd_rn(__fmul_rn(v[x], b2), __fmul_rn(__fmul_rn(gs, gs), b2c));
+            root[x] = __fsqrt_rn(v[x]);
+            // the quotient to 2 ulp: it is added to p scaled by the step size
+            const float u = __fdividef(m[x], fmaf(root[x], c.root_corr, eps));
+            p[x] -= fmaf(p[x], decay, u * c.step_size);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float(&p4)[4] = *reinterpret_cast<const float(*)[4]>(p + 4 * h);
+            store4_tail(pp, i + 128 * h, n, p4);
+            if (MASTER) store4(flat.master + at + 128 * h, p4);
+        }
+        if (EIGHT) {
+            unsigned lo[8], hi[8], code[2];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const unsigned h = mix32((unsigned)at + 128u * (x >> 2) + (x & 3) + c.key);
+                lo[x] = h & 0xFFFFu;
+                hi[x] = h >> 16;
+            }
+            uint8_t* mc = static_cast<uint8_t*>(flat.m) + at;
+            uint8_t* vc = static_cast<uint8_t*>(flat.v) + at;
+            const float ms = quantize<false>(m, lo, code);
+            *reinterpret_cast<unsigned*>(mc) = code[0];
+            *reinterpret_cast<unsigned*>(mc + 128) = code[1];
+            const float vs = quantize<true>(root, hi, code);
+            *reinterpret_cast<unsigned*>(vc) = code[0];
+            *reinterpret_cast<unsigned*>(vc + 128) = code[1];
+            if (lane == 0) {
+                flat.ms[blk] = ms;
+                flat.vs[blk] = vs;
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                store4(static_cast<float*>(flat.m) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(m + 4 * h));
+                store4(static_cast<float*>(flat.v) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(v + 4 * h));
+            }
+        }
+    }
+}
+
+unsigned ctas(unsigned blocks) { return (blocks + kPerCta - 1) / kPerCta; }
+
+// Launch with programmatic stream serialisation (every kernel here waits for
+// the one before it before its first global access).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+size_t coef_bytes() { return 256; }
+
+// Fills the table with the next tensors (at most CAP) and calls f(table, blocks, first block).
+template <int CAP, typename F>
+cudaError_t each_group(const AdamwArgs& a, F f) {
+    AdamwTable<CAP> t;
+    long long first = 0, at = 0;
+    t.n = 0;
+    cudaError_t err = cudaSuccess;
+    auto flush = [&] {
+        if (t.n && err == cudaSuccess) err = f(t, (unsigned)(at - first), (unsigned)first);
+        first = at;
+        t.n = 0;
+    };
+    for (int i = 0; i < a.n_tensors; ++i) {
+        const txl_adamw_tensor& x = a.tensors[i];
+        if (x.n <= 0) continue;
+        t.e[t.n++] = {x.param, x.grad, x.n, (unsigned)(at - first), x.weight_decay};
+        at += (x.n + kAdamwBlock - 1) / kAdamwBlock;
+        if (t.n == CAP) flush();
+    }
+    flush();
+    return err;
+}
+
+template <int CAP>
+cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
+    AdamwCoef* coef = static_cast<AdamwCoef*>(a.workspace);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + coef_bytes());
+    unsigned n_part = 0;
+    cudaError_t e = cudaSuccess;
+    if (a.max_norm > 0) {
+        e = each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned) {
+            float* to = part + n_part;
+            n_part += ctas(n);
+            return a.bf16_grad ? launch_pdl(adamw_norm_kernel<__nv_bfloat16, CAP>, ctas(n), 256u, stream, t, n, to)
+                               : launch_pdl(adamw_norm_kernel<float, CAP>, ctas(n), 256u, stream, t, n, to);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(adamw_coef_kernel, 1, n_part ? 1024u : 32u, stream, part, n_part, a.beta1, a.beta2, a.max_norm, a.seed,
+                   a.lr, a.steps, a.grad_norm, coef);
+    if (e != cudaSuccess) return e;
+    const AdamwFlat flat = {a.master, a.exp_avg, a.exp_avg_scale, a.exp_avg_sq, a.exp_avg_sq_scale};
+    const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
+    return each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned first) {
+        auto go = [&](auto kern) {
+            return launch_pdl(kern, ctas(n), 256u, stream, t, n, first, flat, b1, b1c, b2, b2c, (float)a.eps, coef);
+        };
+        using B = __nv_bfloat16;
+        if (a.eight_bit) {
+            if (a.bf16_param) return a.bf16_grad ? go(adamw_kernel<B, B, true, CAP>) : go(adamw_kernel<B, float, true, CAP>);
+            return a.bf16_grad ? go(adamw_kernel<float, B, true, CAP>) : go(adamw_kernel<float, float, true, CAP>);
+        }
+        if (a.bf16_param) return a.bf16_grad ? go(adamw_kernel<B, B, false, CAP>) : go(adamw_kernel<B, float, false, CAP>);
+        return a.bf16_grad ? go(adamw_kernel<float, B, false, CAP>) : go(adamw_kernel<float, float, false, CAP>);
+    });
+}
+
+constexpr int kSmallTable = 32, kLargeTable = 480;
+
+}  // namespace
+
+long long adamw_blocks(const txl_adamw_tensor* tensors, int n_tensors) {
+    long long b = 0;
+    for (int i = 0; i < n_tensors; ++i)
+        if (tensors[i].n > 0) b += (tensors[i].n + kAdamwBlock - 1) / kAdamwBlock;
+    return b;
+}
+
+// Coefficients, and one partial sum per CTA of each group of tensors (a group's
+// last CTA may be partly filled: one more per group at most).
+size_t adamw_workspace_bytes(long long blocks) {
+    return coef_bytes() + (size_t)(blocks / kPerCta + blocks / kSmallTable + 2) * sizeof(float);
+}
+
+cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream) {
+    const long long blocks = adamw_blocks(a.tensors, a.n_tensors);
+    return a.n_tensors <= kSmallTable ? run<kSmallTable>(a, blocks, stream) : run<kLargeTable>(a, blocks, stream);
+}
+
+TXL_BOUNDS_READER(bounds_word_adamw)
+
+}  // namespace txl

@@ -1,11 +1,16 @@
 // extern "C" entry points of libtxl.so (declared in include/txl_attn.h):
 // argument validation on the host, then one asynchronous launch on the
 // caller's stream.  Nothing here allocates device memory.
+#include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
+#include <new>
+#include <vector>
 #include <cuda_runtime.h>
 
+#include "adamw.h"
 #include "proj_gemm.h"
 #include "txl_attn.h"
 #include "txl_device.cuh"
@@ -26,6 +31,14 @@ cudaError_t launch_attn_bwd_simt(const void* q, const void* k, const void* v, co
                                  cudaStream_t stream);
 cudaError_t launch_layer_norm(const void* x, const void* y, const void* gamma, const void* beta,
                               long long rows, int d, float eps, void* out, cudaStream_t stream);
+cudaError_t launch_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta,
+                                  long long rows, int d, float eps, void* out, float* mean, float* rstd,
+                                  int bf16, cudaStream_t stream);
+size_t layer_norm_bwd_workspace_bytes(long long rows, int d);
+cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
+                                  const float* mean, const float* rstd, const void* dres, long long rows,
+                                  int d, void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
+                                  cudaStream_t stream);
 cudaError_t launch_attn_simt_f32(const float* q, const float* k, const float* v, const float* r,
                                  const float* ub, const float* vb, int B, int H, int L, int M,
                                  int dh, float scale, int lo_shift, float* out, cudaStream_t stream);
@@ -52,6 +65,8 @@ unsigned long long bounds_word_attn_bwd_tc();
 unsigned long long bounds_word_mem_update();
 unsigned long long bounds_word_layer_norm();
 unsigned long long bounds_word_proj_gemm();
+unsigned long long bounds_word_layer_norm_train();
+unsigned long long bounds_word_adamw();
 
 }  // namespace txl
 
@@ -615,6 +630,168 @@ int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* 
     return e == cudaSuccess ? TXL_OK : TXL_ERR_LAUNCH;
 }
 
+}  // extern "C"
+
+namespace {
+
+// A byte range of a call's arguments, for overlap checks over many of them.
+struct Range {
+    uintptr_t at, end;
+    bool written;
+};
+
+Range range_of(const void* p, size_t n, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, a + n, written};
+}
+
+// Whether a written range overlaps any other.  Sorts the ranges.
+bool any_written_overlap(Range* r, size_t n) {
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.at < b.at; });
+    uintptr_t end = 0, written_end = 0;  // how far the ranges before this one reach
+    for (size_t i = 0; i < n; ++i) {
+        if (!r[i].at || r[i].at == r[i].end) continue;
+        if (r[i].at < written_end || (r[i].written && r[i].at < end)) return true;
+        end = std::max(end, r[i].end);
+        if (r[i].written) written_end = std::max(written_end, r[i].end);
+    }
+    return false;
+}
+
+constexpr int kLayerNormMaxD = 16384;
+
+// rows * d below 2^40, so that byte offsets stay far inside 64 bits.
+bool row_data_too_large(long long rows, int d) { return rows > (1ll << 40) / d; }
+
+bool bad_workspace(const void* workspace, size_t bytes, size_t need) {
+    return need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || bytes < need);
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+int txl_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
+                       int d, float eps, void* out, float* mean, float* rstd, int dtype, void* stream) {
+    const int es = elem_size(dtype);
+    if (!es || rows < 0 || d <= 0 || !(eps >= 0.f)) return TXL_ERR_INVALID_ARG;
+    if (d > kLayerNormMaxD || row_data_too_large(rows, d)) return TXL_ERR_UNSUPPORTED;
+    if (rows == 0) return TXL_OK;
+    if (!x || !gamma || !beta || !out || !mean || !rstd) return TXL_ERR_INVALID_ARG;
+    for (const void* p : {x, y, gamma, beta, (const void*)out, (const void*)mean, (const void*)rstd})
+        if (!aligned16(p)) return TXL_ERR_MISALIGNED;
+    const size_t n = (size_t)rows * d * es, nd = (size_t)d * es, nr = (size_t)rows * sizeof(float);
+    Range r[] = {range_of(x, n, false),    range_of(y, n, false),  range_of(gamma, nd, false),
+                 range_of(beta, nd, false), range_of(out, n, true), range_of(mean, nr, true),
+                 range_of(rstd, nr, true)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    return cuda_status(txl::launch_layer_norm_fwd(x, y, gamma, beta, rows, d, eps, out, mean, rstd,
+                                                  dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t txl_layer_norm_bwd_workspace_bytes(long long rows, int d, int dtype) {
+    if (!elem_size(dtype) || rows < 0 || d <= 0 || d > kLayerNormMaxD || row_data_too_large(rows, d)) return 0;
+    return txl::layer_norm_bwd_workspace_bytes(rows, d);
+}
+
+int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
+                       const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
+                       float* dbeta, int dtype, void* workspace, size_t ws_bytes, void* stream) {
+    const int es = elem_size(dtype);
+    if (!es || rows < 0 || d <= 0 || !dgamma || !dbeta) return TXL_ERR_INVALID_ARG;
+    if (rows > 0 && (!dout || !x || !gamma || !mean || !rstd || !dx)) return TXL_ERR_INVALID_ARG;
+    if (d > kLayerNormMaxD || row_data_too_large(rows, d)) return TXL_ERR_UNSUPPORTED;
+    if (!aligned16(dgamma) || !aligned16(dbeta)) return TXL_ERR_MISALIGNED;
+    if (rows > 0)
+        for (const void* p : {dout, x, y, gamma, (const void*)mean, (const void*)rstd, dres, (const void*)dx})
+            if (!aligned16(p)) return TXL_ERR_MISALIGNED;
+    const size_t need = txl_layer_norm_bwd_workspace_bytes(rows, d, dtype);
+    if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
+    const size_t n = (size_t)rows * d * es, nd = (size_t)d * sizeof(float), nr = (size_t)rows * sizeof(float);
+    Range r[] = {range_of(dout, n, false),  range_of(x, n, false),      range_of(y, n, false),
+                 range_of(gamma, rows > 0 ? (size_t)d * es : 0, false), range_of(mean, nr, false),
+                 range_of(rstd, nr, false), range_of(dres, n, false),   range_of(dx, n, true),
+                 range_of(dgamma, nd, true), range_of(dbeta, nd, true), range_of(workspace, need, true)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    return cuda_status(txl::launch_layer_norm_bwd(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta,
+                                                  workspace, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors) {
+    if (!tensors || n_tensors <= 0) return -1;
+    long long blocks = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        if (tensors[i].n < 0 || tensors[i].n > (1ll << 38)) return -1;
+        blocks += (tensors[i].n + txl::kAdamwBlock - 1) / txl::kAdamwBlock;
+        if (blocks > (1ll << 30)) return -1;
+    }
+    return blocks * txl::kAdamwBlock;
+}
+
+size_t txl_adamw_workspace_bytes(const txl_adamw_tensor* tensors, int n_tensors) {
+    const long long n = txl_adamw_state_elements(tensors, n_tensors);
+    return n < 0 ? 0 : txl::adamw_workspace_bytes(n / txl::kAdamwBlock);
+}
+
+int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dtype, int grad_dtype,
+                   int state_bits, float* master, void* exp_avg, float* exp_avg_scale, void* exp_avg_sq,
+                   float* exp_avg_sq_scale, long long* steps, const float* lr, double beta1, double beta2,
+                   double eps, double max_norm, unsigned seed, float* grad_norm, void* workspace,
+                   size_t ws_bytes, void* stream) {
+    const int ep = elem_size(param_dtype), eg = elem_size(grad_dtype);
+    if (!ep || !eg || (state_bits != 8 && state_bits != 32)) return TXL_ERR_INVALID_ARG;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
+        !(max_norm >= 0.0) || !std::isfinite(max_norm))
+        return TXL_ERR_INVALID_ARG;
+    const long long total = txl_adamw_state_elements(tensors, n_tensors);
+    if (total < 0 || !steps || !lr) return TXL_ERR_INVALID_ARG;
+    const bool eight = state_bits == 8, bf16 = param_dtype == TXL_BF16;
+    if ((master != nullptr) != bf16 || (exp_avg_scale != nullptr) != eight || (exp_avg_sq_scale != nullptr) != eight ||
+        (total && (!exp_avg || !exp_avg_sq)))
+        return TXL_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)master, (const void*)exp_avg, (const void*)exp_avg_scale,
+                          (const void*)exp_avg_sq, (const void*)exp_avg_sq_scale})
+        if (!aligned16(p)) return TXL_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(steps) & 7u) || (reinterpret_cast<uintptr_t>(lr) & 3u) ||
+        (reinterpret_cast<uintptr_t>(grad_norm) & 3u))
+        return TXL_ERR_MISALIGNED;
+    const size_t need = txl_adamw_workspace_bytes(tensors, n_tensors);
+    if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
+    // (no exception leaves a C entry point)
+    std::vector<Range> r;
+    try {
+        r.reserve(2 * (size_t)n_tensors + 9);
+    } catch (const std::bad_alloc&) {
+        return TXL_ERR_UNSUPPORTED;
+    }
+    for (int i = 0; i < n_tensors; ++i) {
+        const txl_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad) return TXL_ERR_INVALID_ARG;
+        if (!aligned16(t.param) || !aligned16(t.grad)) return TXL_ERR_MISALIGNED;
+        r.push_back(range_of(t.param, (size_t)t.n * ep, true));
+        r.push_back(range_of(t.grad, (size_t)t.n * eg, false));
+    }
+    const size_t state = (size_t)total * (eight ? 1 : 4), scales = (size_t)total / txl::kAdamwBlock * sizeof(float);
+    r.push_back(range_of(master, (size_t)total * 4, true));
+    r.push_back(range_of(exp_avg, state, true));
+    r.push_back(range_of(exp_avg_sq, state, true));
+    r.push_back(range_of(exp_avg_scale, scales, true));
+    r.push_back(range_of(exp_avg_sq_scale, scales, true));
+    r.push_back(range_of(steps, sizeof(long long), true));
+    r.push_back(range_of(lr, sizeof(float), false));
+    r.push_back(range_of(grad_norm, sizeof(float), true));
+    r.push_back(range_of(workspace, need, true));
+    if (any_written_overlap(r.data(), r.size())) return TXL_ERR_ALIAS;
+    const txl::AdamwArgs a = {tensors,       n_tensors, bf16, grad_dtype == TXL_BF16, eight, master,
+                              exp_avg,       exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, steps, lr,
+                              beta1,         beta2,     eps,  max_norm, seed, grad_norm,
+                              workspace};
+    return cuda_status(txl::launch_adamw(a, static_cast<cudaStream_t>(stream)));
+}
+
 const char* txl_status_string(int status) {
     switch (status) {
         case TXL_OK: return "ok";
@@ -640,10 +817,11 @@ int txl_bounds_status(unsigned long long* first) {
     return TXL_ERR_UNSUPPORTED;  // this library was built without bounds checks
 #else
     if (cudaDeviceSynchronize() != cudaSuccess) return TXL_ERR_CUDA;
-    const unsigned long long words[7] = {txl::bounds_word_attn_simt(),   txl::bounds_word_attn_tc(),
+    const unsigned long long words[] = {txl::bounds_word_attn_simt(),   txl::bounds_word_attn_tc(),
                                          txl::bounds_word_attn_bwd(),    txl::bounds_word_attn_bwd_tc(),
                                          txl::bounds_word_mem_update(),  txl::bounds_word_layer_norm(),
-                                         txl::bounds_word_proj_gemm()};
+                                         txl::bounds_word_proj_gemm(),   txl::bounds_word_layer_norm_train(),
+                                         txl::bounds_word_adamw()};
     unsigned long long w = 0;
     for (unsigned long long x : words) {
         if (x == ~0ull) return TXL_ERR_CUDA;

@@ -1,0 +1,247 @@
+"""Training operators of a decoder layer: LayerNorm's forward with its row
+statistics and its gradients, and the AdamW step that applies gradients to the
+weights the forward kernels read.  Argument marshalling and buffers only: every
+step of the computation runs in libtxl.so's CUDA kernels."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Sequence
+
+import torch
+
+from . import _lib
+from ._lib import TXL_BF16, TXL_F32, AdamwTensor, TxlError, _dtype_code, _invoke, _need, _stream
+
+STATE_BLOCK = 256  # elements of one block of a flat optimizer state
+
+
+def _on(stream, device):
+    """Context in which buffers for a call on ``stream`` are allocated: torch
+    hands freed memory out again in the order of the stream it was allocated
+    on, so a call's buffers belong to the call's stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(workspace, need: int, device) -> int:
+    """Address of a call's workspace (the C call checks address and size)."""
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace.numel() * workspace.element_size() < need:
+        raise TxlError(-7, "workspace")
+    return workspace.data_ptr()
+
+
+def _row_args(x, y, gamma, beta, extra):
+    """Checks the tensors of a LayerNorm call; returns (rows, d)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a tensor [..., d]")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {x.dtype}: bf16 or fp32 only")
+    d = x.shape[-1]
+    shape, dt, dev = x.shape, x.dtype, x.device
+    if d == 0:
+        raise ValueError("x must have a last axis of at least one element")
+    _need(x, "x", shape, dt)
+    if y is not None:
+        _need(y, "y", shape, dt, dev)
+    _need(gamma, "gamma", (d,), dt, dev)
+    if beta is not None:
+        _need(beta, "beta", (d,), dt, dev)
+    for name, t in extra:
+        if t is not None:
+            _need(t, name, shape, dt, dev)
+    return x.numel() // d, d
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def layer_norm_fwd(x, gamma, beta, y=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """txl_layer_norm_fwd: LayerNorm(x + y) * gamma + beta over the last axis
+    (y optional), keeping the statistics that layer_norm_bwd takes.  x [..., d]
+    bf16 or fp32 with 1 <= d <= 16384; mean, rstd fp32 [...].  Returns
+    (out, mean, rstd); out overlaps no input."""
+    rows, d = _row_args(x, y, gamma, beta, (("out", out),))
+    dev, st = x.device, x.shape[:-1]
+    with _on(stream, dev):
+        if out is None:
+            out = torch.empty_like(x)
+        if mean is None:
+            mean = torch.empty(st, dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(st, dtype=torch.float32, device=dev)
+    _need(mean, "mean", st, torch.float32, dev)
+    _need(rstd, "rstd", st, torch.float32, dev)
+    rc = _invoke(dev, "txl_layer_norm_fwd", x.data_ptr(), _ptr(y), gamma.data_ptr(), beta.data_ptr(), rows, d,
+                 float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _dtype_code(x), _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace_bytes(rows, d, dtype=torch.bfloat16, device=None) -> int:
+    """txl_layer_norm_bwd_workspace_bytes for a call on ``device`` (default: the
+    current one)."""
+    code = TXL_BF16 if dtype == torch.bfloat16 else TXL_F32
+    dev = device if device is not None else torch.cuda.current_device()
+    return int(_invoke(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, code))
+
+
+def layer_norm_bwd(dout, x, gamma, mean, rstd, y=None, dres=None, stream=None, workspace=None, grads=None):
+    """txl_layer_norm_bwd: gradients of layer_norm_fwd's output.  dout, x, y as
+    its out, x, y; mean, rstd as it returned them; dres [..., d] (optional) is
+    added to dx: the gradient that reaches x + y along a residual path.
+    Returns a dict dx (x's type; the gradient of x and of y), dgamma, dbeta
+    (fp32 [d], summed in a fixed order).  grads: a dict of preallocated tensors
+    to fill; workspace: a uint8 tensor of at least
+    layer_norm_bwd_workspace_bytes(...) bytes (allocated here when None)."""
+    rows, d = _row_args(x, y, gamma, None, (("dout", dout), ("dres", dres)))
+    if dout is None:
+        raise TypeError("dout must be a torch.Tensor")
+    dev, st = x.device, x.shape[:-1]
+    _need(mean, "mean", st, torch.float32, dev)
+    _need(rstd, "rstd", st, torch.float32, dev)
+    need = int(_invoke(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, _dtype_code(x)))
+    with _on(stream, dev):
+        if grads is None:
+            g = {"dx": torch.empty_like(x), "dgamma": torch.empty(d, dtype=torch.float32, device=dev),
+                 "dbeta": torch.empty(d, dtype=torch.float32, device=dev)}
+        else:
+            g = grads
+            _need(g["dx"], "dx", x.shape, x.dtype, dev)
+            _need(g["dgamma"], "dgamma", (d,), torch.float32, dev)
+            _need(g["dbeta"], "dbeta", (d,), torch.float32, dev)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    rc = _invoke(dev, "txl_layer_norm_bwd", dout.data_ptr(), x.data_ptr(), _ptr(y), gamma.data_ptr(),
+                 mean.data_ptr(), rstd.data_ptr(), _ptr(dres), rows, d, g["dx"].data_ptr(), g["dgamma"].data_ptr(),
+                 g["dbeta"].data_ptr(), _dtype_code(x), _scratch(workspace, need, dev), need, _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_layer_norm_bwd")
+    return g
+
+
+class AdamW:
+    """AdamW over a list of parameters in one launch sequence (txl_adamw_step),
+    with the moments in fp32 or in 8 bits.
+
+    ``params``: contiguous CUDA tensors of one type, fp32 or bf16 (bf16
+    parameters get an fp32 master copy, which the steps update and round into
+    them: the forward kernels keep reading the same tensors); ``grads``: one
+    gradient per parameter, fp32 or bf16, the buffers that the backward calls
+    fill.  Both are bound here: step() reads the gradients from these buffers and
+    updates these parameters in place.  ``weight_decay``: one number, or one per
+    parameter.  ``max_norm``: gradients are scaled by min(1, max_norm / norm), norm
+    the 2-norm of all of them, kept in ``grad_norm`` [1]; a norm that is not finite
+    makes the step change nothing.  ``state_bits`` 8: the moments as e4m3 codes
+    with one scale per 256 elements, rounded at random from ``seed``.
+
+    Device values: ``lr`` [1] fp32 (set_lr), ``steps`` [1] int64 (steps done), the
+    flat ``master`` (None for fp32 parameters) and states(); parameter i's part of
+    the flat buffers starts at ``starts[i]``.  A step reads all of them when it
+    runs: captured in a graph it can be replayed."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], lr: float,
+                 betas: tuple = (0.9, 0.999), eps: float = 1e-8, weight_decay: float | Sequence[float] = 0.0,
+                 state_bits: int = 32, max_norm: float | None = None, seed: int = 0,
+                 stream: torch.cuda.Stream | None = None):
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        if n == 0 or len(self.grads) != n:
+            raise ValueError("need one gradient per parameter, and at least one parameter")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be positive, or None")
+        decay = [float(weight_decay)] * n if not isinstance(weight_decay, (list, tuple)) else list(map(float, weight_decay))
+        if len(decay) != n:
+            raise ValueError("need one weight_decay, or one per parameter")
+        p0, g0 = self.params[0], self.grads[0]
+        for t in (p0, g0):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("params and grads must be torch.Tensors")
+        self.device = dev = p0.device
+        self._param_dtype, self._grad_dtype = _dtype_code(p0), _dtype_code(g0)
+        self._table = (AdamwTensor * n)()
+        self.starts, total = [], 0
+        for i, (p, g) in enumerate(zip(self.params, self.grads)):
+            _need(p, f"params[{i}]", p.shape, p0.dtype, dev)
+            _need(g, f"grads[{i}]", p.shape, g0.dtype, dev)
+            self._table[i] = AdamwTensor(p.data_ptr(), g.data_ptr(), p.numel(), decay[i], 0)
+            self.starts.append(total)
+            total += -(-p.numel() // STATE_BLOCK) * STATE_BLOCK
+        self.betas, self.eps, self.weight_decay = tuple(map(float, betas)), float(eps), decay
+        self.state_bits, self.max_norm, self.seed = state_bits, max_norm, int(seed) & 0xFFFFFFFF
+        self._fixed_stream = stream
+        if _invoke(dev, "txl_adamw_state_elements", self._table, n) != total:
+            raise TxlError(-1, "txl_adamw_state_elements")
+        need = int(_invoke(dev, "txl_adamw_workspace_bytes", self._table, n))
+        f32 = dict(dtype=torch.float32, device=dev)
+        with _on(stream, dev):
+            self.lr = torch.full((1,), float(lr), **f32)
+            self.steps = torch.zeros(1, dtype=torch.int64, device=dev)
+            self.grad_norm = torch.zeros(1, **f32) if max_norm is not None else None
+            self.master = None
+            if p0.dtype == torch.bfloat16:
+                self.master = torch.zeros(total, **f32)
+                self._copy_masters()
+            code = torch.float8_e4m3fn if state_bits == 8 else torch.float32
+            self.exp_avg = torch.zeros(total, **f32).to(code)
+            self.exp_avg_sq = torch.zeros(total, **f32).to(code)
+            blocks = total // STATE_BLOCK
+            self.exp_avg_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
+            self.exp_avg_sq_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self._args = (self._table, n, self._param_dtype, self._grad_dtype, state_bits, _ptr(self.master),
+                      self.exp_avg.data_ptr(), _ptr(self.exp_avg_scale), self.exp_avg_sq.data_ptr(),
+                      _ptr(self.exp_avg_sq_scale), self.steps.data_ptr(), self.lr.data_ptr(), *self.betas, self.eps,
+                      float(max_norm or 0.0), self.seed, _ptr(self.grad_norm), self._workspace.data_ptr(), need)
+
+    def _copy_masters(self) -> None:
+        for p, a in zip(self.params, self.starts):
+            self.master[a:a + p.numel()].copy_(p.reshape(-1))
+
+    def step(self, stream=None) -> None:
+        """One step from the gradients as they stand, on ``stream`` (default:
+        the constructor's, else the current one)."""
+        st = stream if stream is not None else self._fixed_stream
+        rc = _invoke(self.device, "txl_adamw_step", *self._args, _stream(st, self.device))
+        if rc != 0:
+            raise TxlError(rc, "txl_adamw_step")
+
+    def set_lr(self, lr: float) -> None:
+        """Learning rate of the steps that follow on the current stream."""
+        self.lr.fill_(float(lr))
+
+    def states(self) -> list:
+        """The flat moments: [exp_avg, exp_avg_sq] in fp32, or with 8 bits
+        [codes of exp_avg, scales, codes of sqrt(exp_avg_sq), scales]."""
+        if self.state_bits == 32:
+            return [self.exp_avg, self.exp_avg_sq]
+        return [self.exp_avg, self.exp_avg_scale, self.exp_avg_sq, self.exp_avg_sq_scale]
+
+    def state_dict(self) -> dict:
+        """Step count, moments and master copy (checkpoint/resume; the
+        parameters are the caller's)."""
+        return {"steps": self.steps.clone(), "lr": self.lr.clone(), "states": [s.clone() for s in self.states()],
+                "master": None if self.master is None else self.master.clone()}
+
+    def load_state_dict(self, sd: dict) -> None:
+        """Restores state_dict's values.  bf16 parameters are set to the
+        rounding of the restored master copy."""
+        if len(sd["states"]) != len(self.states()) or (sd["master"] is None) != (self.master is None):
+            raise ValueError("state of another state_bits or parameter type")
+        for mine, given in zip(self.states() + [self.steps, self.lr], list(sd["states"]) + [sd["steps"], sd["lr"]]):
+            if mine.shape != given.shape:
+                raise ValueError(f"state has shape {tuple(given.shape)}, expected {tuple(mine.shape)}")
+            mine.copy_(given)
+        if self.master is not None:
+            self.master.copy_(sd["master"])
+            for p, a in zip(self.params, self.starts):
+                p.copy_(self.master[a:a + p.numel()].view(p.shape))
