@@ -370,6 +370,29 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
                        float* dbeta, int dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * txl_linear_bwd: gradients of txl_linear's out = x W^T + bias, bf16 with fp32
+ * accumulation on the tensor cores.  dy [B, T, N] is the gradient of out, x
+ * [B, T, K] (TXL_LAYOUT_ROWS) or [B, K/64, T, 64] (TXL_LAYOUT_HEADS), w [N, K]:
+ *   dx = dy W, bf16 in x's layout (an attention output's gradient comes out in
+ *        the layout txl_attn_bwd takes as dout); with relu_in, where x is the
+ *        output of a ReLU, times [x > 0]: the gradient of the ReLU's input
+ *   dw = dy^T x, fp32 [N, K];  db = sum of dy over the rows, fp32 [N]
+ * dx may be null, db may be null, dw may be null if db is (TXL_ERR_INVALID_ARG:
+ * db without dw, or nothing asked for).  Sums over rows are added in a fixed
+ * order: the same inputs give the same bits.
+ *
+ * Any B, T >= 1; K and N multiples of 8, K of 64 in the heads layout
+ * (TXL_ERR_UNSUPPORTED; as are B T above 2^28, K or N above 2^20 and more than
+ * 2^30 output tiles of 128 x 128).  Pointers 16-byte aligned
+ * (TXL_ERR_MISALIGNED); outputs overlap neither inputs nor each other
+ * (TXL_ERR_ALIAS).  workspace as for txl_layer_norm_bwd, of
+ * txl_linear_bwd_workspace_bytes(...) bytes (0: none needed, not touched).
+ */
+size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw);
+int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, int K, const void* w, int N,
+                   int relu_in, void* dx, float* dw, float* db, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * txl_adamw_step: one AdamW step over n_tensors tensors.  `tensors` is an array
  * in HOST memory, read during the call; tensor i has n elements (0: skipped),
  * a parameter, a gradient and a weight decay of its own.  With g the gradient

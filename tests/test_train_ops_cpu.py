@@ -59,6 +59,22 @@ def test_layer_norm_bwd_rejects_bad_arguments(lib):
     assert lib.txl_layer_norm_bwd_workspace_bytes(-1, 500, BF) == 0
 
 
+def test_linear_bwd_rejects_bad_arguments(lib):
+    def call(dy=addr(0), x=addr(1), layout=0, B=2, T=100, K=128, w=addr(2), N=136, relu=0, dx=addr(3), dw=addr(4),
+             db=addr(5), ws=addr(6), ws_bytes=1 << 28):
+        return lib.txl_linear_bwd(dy, x, layout, B, T, K, w, N, relu, dx, dw, db, ws, ws_bytes, None)
+    for name in ("dy", "x", "w"):
+        assert call(**{name: None}) == -1, name
+    assert call(dx=None, dw=None, db=None) == -1 and call(dw=None) == -1      # nothing, or db without dw
+    for name in ("dy", "x", "w", "dx", "dw", "db"):
+        assert call(**{name: addr(9) + 8}) == -3, name
+    assert call(layout=2) == -1 and call(B=0) == -1 and call(T=-1) == -1 and call(K=0) == -1 and call(N=-8) == -1
+    assert call(K=132) == -2 and call(N=100) == -2 and call(layout=1, K=72) == -2
+    assert call(B=1 << 20, T=1 << 10) == -2 and call(K=1 << 21) == -2
+    assert call(dx=addr(1)) == -4 and call(dw=addr(4), db=addr(4) + 64) == -4 and call(dw=addr(2)) == -4
+    assert lib.txl_linear_bwd_workspace_bytes(0, 2, 100, 132, 136, 1, 1) == 0
+
+
 def table(*entries):
     t = (_lib.AdamwTensor * max(1, len(entries)))()
     for i, e in enumerate(entries):
@@ -115,6 +131,13 @@ def test_binding_refuses_what_it_can_see():
         txl.layer_norm_fwd(torch.zeros(4, 0), w, w)
     with pytest.raises(ValueError, match="CUDA"):
         txl.layer_norm_bwd(x, x, w, w, w)
+    b = torch.zeros(1, 4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        txl.linear_bwd(b, b, torch.zeros(8, 8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="want"):
+        txl.linear_bwd(b, b, torch.zeros(8, 8, dtype=torch.bfloat16), want=("dz",))
+    with pytest.raises(ValueError, match="x must be"):
+        txl.linear_bwd(b, b[0], torch.zeros(8, 8, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA"):
         txl.AdamW([x], [x], lr=1e-3)
     with pytest.raises(ValueError, match="gradient"):

@@ -13,6 +13,7 @@ Public API (all computation runs in libtxl.so's CUDA kernels):
     linear, layer_norm                            o_net / feed-forward GEMMs, fused residual LayerNorm
     layer_norm_fwd, layer_norm_bwd                LayerNorm keeping its row statistics, and its gradients
     layer_norm_bwd_workspace_bytes                scratch of the latter
+    linear_bwd, linear_bwd_workspace_bytes        gradients of linear (tensor cores), ReLU mask and bias sum fused
     AdamW                                         AdamW over many tensors, 32-bit or 8-bit states
     sync_status, check_status                     device status word
     bounds_status                                 first out-of-range access (bounds-checked build)
@@ -26,10 +27,11 @@ from ._lib import (TXL_BF16, TXL_F32, TxlError, attn_bwd, attn_bwd_workspace_byt
                    status_string,
                    sync_status, version, LIB_PATH)
 from .driver import AttnStack, DecoderStack, SegmentDriver
-from .train import AdamW, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd
+from .train import AdamW, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd, linear_bwd, linear_bwd_workspace_bytes
 
 __all__ = ["TXL_BF16", "TXL_F32", "TxlError", "attn_bwd", "attn_bwd_workspace_bytes", "attn_fwd", "attn_fwd_lse", "attn_fwd_noalloc", "attn_fwd_ws",
            "attn_workspace_bytes", "bounds_status",
            "check_status", "debug_inject", "header_functions", "layer_norm", "linear", "load", "mem_reset", "mem_ring_push", "mem_update", "qkv_proj", "qkvr_proj", "r_proj",
            "status_string", "sync_status", "version", "SegmentDriver", "AttnStack", "DecoderStack", "AdamW", "layer_norm_fwd",
-           "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "LIB_PATH"]
+           "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+           "linear_bwd", "linear_bwd_workspace_bytes", "LIB_PATH"]

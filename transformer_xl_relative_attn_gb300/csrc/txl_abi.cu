@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "adamw.h"
+#include "linear_bwd.h"
 #include "proj_gemm.h"
 #include "txl_attn.h"
 #include "txl_device.cuh"
@@ -67,6 +68,7 @@ unsigned long long bounds_word_layer_norm();
 unsigned long long bounds_word_proj_gemm();
 unsigned long long bounds_word_layer_norm_train();
 unsigned long long bounds_word_adamw();
+unsigned long long bounds_word_linear_bwd();
 
 }  // namespace txl
 
@@ -667,6 +669,18 @@ bool bad_workspace(const void* workspace, size_t bytes, size_t need) {
     return need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || bytes < need);
 }
 
+int linear_bwd_sizes(int x_layout, int B, int T, int K, int N) {
+    if (x_layout != TXL_LAYOUT_ROWS && x_layout != TXL_LAYOUT_HEADS) return TXL_ERR_INVALID_ARG;
+    if (B <= 0 || T <= 0 || K <= 0 || N <= 0) return TXL_ERR_INVALID_ARG;
+    if (K % 8 != 0 || N % 8 != 0 || (x_layout == TXL_LAYOUT_HEADS && K % 64 != 0)) return TXL_ERR_UNSUPPORTED;
+    const long long rows = (long long)B * T;
+    if (rows > (1ll << 28) || K > (1 << 20) || N > (1 << 20)) return TXL_ERR_UNSUPPORTED;
+    const long long row_tiles = (x_layout == TXL_LAYOUT_HEADS ? B * ((T + 127ll) / 128) : (rows + 127) / 128) +
+                                (N + 127ll) / 128 * 32;  // dw's tiles, over at most 32 splits
+    if (row_tiles * ((K + 127ll) / 128) > (1ll << 30)) return TXL_ERR_UNSUPPORTED;
+    return TXL_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_LAUNCH; }
 
 }  // namespace
@@ -717,6 +731,32 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
     if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
     return cuda_status(txl::launch_layer_norm_bwd(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta,
                                                   workspace, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw) {
+    if (linear_bwd_sizes(x_layout, B, T, K, N) != TXL_OK) return 0;
+    return txl::linear_bwd_workspace_bytes(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0);
+}
+
+int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, int K, const void* w, int N,
+                   int relu_in, void* dx, float* dw, float* db, void* workspace, size_t ws_bytes, void* stream) {
+    if (!dy || !x || !w || (!dx && !dw) || (db && !dw)) return TXL_ERR_INVALID_ARG;
+    const int rc = linear_bwd_sizes(x_layout, B, T, K, N);
+    if (rc != TXL_OK) return rc;
+    for (const void* p : {dy, x, w, (const void*)dx, (const void*)dw, (const void*)db})
+        if (!aligned16(p)) return TXL_ERR_MISALIGNED;
+    const size_t need = txl_linear_bwd_workspace_bytes(x_layout, B, T, K, N, dx != nullptr, dw != nullptr);
+    if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
+    const size_t rows = (size_t)B * T, nx = rows * K * 2, nw = (size_t)N * K;
+    Range r[] = {range_of(dy, rows * N * 2, false),     range_of(x, nx, false),
+                 range_of(w, nw * 2, false),            range_of(dx, nx, true),
+                 range_of(dw, nw * 4, true),            range_of(db, (size_t)N * 4, true),
+                 range_of(need ? workspace : nullptr, need, true)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    int* status = dev_status_ptr();
+    if (!status) return TXL_ERR_CUDA;
+    return launch_status(txl::launch_linear_bwd(dy, x, x_layout == TXL_LAYOUT_HEADS, B, T, K, w, N, relu_in != 0, dx,
+                                                dw, db, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
 long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors) {
@@ -821,7 +861,7 @@ int txl_bounds_status(unsigned long long* first) {
                                          txl::bounds_word_attn_bwd(),    txl::bounds_word_attn_bwd_tc(),
                                          txl::bounds_word_mem_update(),  txl::bounds_word_layer_norm(),
                                          txl::bounds_word_proj_gemm(),   txl::bounds_word_layer_norm_train(),
-                                         txl::bounds_word_adamw()};
+                                         txl::bounds_word_adamw(),       txl::bounds_word_linear_bwd()};
     unsigned long long w = 0;
     for (unsigned long long x : words) {
         if (x == ~0ull) return TXL_ERR_CUDA;

@@ -127,6 +127,65 @@ def layer_norm_bwd(dout, x, gamma, mean, rstd, y=None, dres=None, stream=None, w
     return g
 
 
+def _linear_shape(x):
+    """(layout, B, T, K) of a Linear input: [B, T, K] rows or [B, K/64, T, 64] heads."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() == 3:
+        return (0, *x.shape)
+    if x.dim() == 4 and x.shape[3] == 64:
+        B, H, T, _ = x.shape
+        return 1, B, T, H * 64
+    raise ValueError("x must be [B, T, K] or [B, K/64, T, 64]")
+
+
+def linear_bwd_workspace_bytes(x_shape, N, want=("dx", "dw", "db"), device=None) -> int:
+    """txl_linear_bwd_workspace_bytes for x of shape [B, T, K] or
+    [B, K/64, T, 64] and N output columns, on ``device`` (default: the current
+    one; the split depends on its SM count)."""
+    layout, B, T, K = _linear_shape(torch.empty(x_shape, device="meta"))
+    dev = device if device is not None else torch.cuda.current_device()
+    return int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want)))
+
+
+def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, workspace=None, grads=None):
+    """txl_linear_bwd: gradients of linear's out = x w^T + bias from dy
+    [B, T, N], the gradient of out.  x [B, T, K] or heads [B, K/64, T, 64], w
+    [N, K], all bf16.  Returns a dict of what ``want`` names: dx (bf16, x's
+    layout), dw (fp32 [N, K]), db (fp32 [N], only along with dw).  relu_in: x is
+    the output of a ReLU, and dx becomes the gradient of the ReLU's input.
+    grads: a dict of preallocated tensors to fill; workspace: a uint8 tensor of
+    at least linear_bwd_workspace_bytes(...) bytes (allocated here when None)."""
+    layout, B, T, K = _linear_shape(x)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    bad = [n for n in want if n not in ("dx", "dw", "db")]
+    if bad or not want:
+        raise ValueError(f"want names gradients out of dx, dw, db: got {want}")
+    N, dev, bf = w.shape[0], x.device, torch.bfloat16
+    _need(x, "x", x.shape, bf)
+    _need(w, "w", (N, K), bf, dev)
+    _need(dy, "dy", (B, T, N), bf, dev)
+    need = int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want)))
+    f32 = torch.float32
+    spec = {"dx": (x.shape, bf), "dw": ((N, K), f32), "db": ((N,), f32)}
+    with _on(stream, dev):
+        if grads is None:
+            g = {n: torch.empty(spec[n][0], dtype=spec[n][1], device=dev) for n in want}
+        else:
+            g = grads
+            for n in want:
+                _need(g[n], n, spec[n][0], spec[n][1], dev)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = _invoke(dev, "txl_linear_bwd", dy.data_ptr(), x.data_ptr(), layout, B, T, K, w.data_ptr(), N,
+                 int(bool(relu_in)), *[g[n].data_ptr() if n in want else 0 for n in ("dx", "dw", "db")],
+                 _scratch(workspace, need, dev) if need else 0, need, _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_linear_bwd")
+    return g
+
+
 class AdamW:
     """AdamW over a list of parameters in one launch sequence (txl_adamw_step),
     with the moments in fp32 or in 8 bits.
