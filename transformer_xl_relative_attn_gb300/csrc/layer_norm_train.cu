@@ -10,9 +10,16 @@
 //   dgamma = sum over rows of dout xh,  dbeta = sum over rows of dout
 //
 // (dx is the gradient of x and of y alike.)  bf16 or fp32 in and out, fp32
-// arithmetic, statistics and parameter gradients.  dgamma and dbeta are summed
-// in a fixed order (partial sums per row range, then their sum): the same
-// inputs give the same bits.
+// arithmetic, statistics and parameter gradients.
+//
+// Both passes are bound by memory: a row is read once, held in registers (E
+// elements per lane, W warps per row), reduced by shuffles and, with several
+// warps, through shared memory, and written once.  Rows of a multiple of 16
+// bytes move as 16-byte vectors, others element by element with the same code.
+// The backward pass is persistent: each thread keeps its columns' sums of dout xh
+// and dout in registers over all rows of its CTA, so dgamma and dbeta cost no
+// second pass over the rows; the CTAs' sums go to the workspace and a second
+// launch adds them, in a fixed order (the same inputs give the same bits).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,26 +30,45 @@ namespace txl {
 
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
+// V consecutive elements as floats, 16 bytes at a time where V elements are 16 bytes.
+template <typename T, int V>
+struct Vec;
 template <>
-__device__ __forceinline__ float to_f<float>(float v) {
-    return v;
-}
+struct Vec<float, 4> {
+    static __device__ __forceinline__ void load(const float* p, float* f) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
 template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-    return __bfloat162float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
+struct Vec<float, 1> {
+    static __device__ __forceinline__ void load(const float* p, float* f) { f[0] = *p; }
+    static __device__ __forceinline__ void store(float* p, const float* f) { *p = f[0]; }
+};
 template <>
-__device__ __forceinline__ float from_f<float>(float v) {
-    return v;
-}
+struct Vec<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = __bfloat1622float2(h[e]);
+            f[2 * e] = x.x, f[2 * e + 1] = x.y;
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+};
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
+struct Vec<__nv_bfloat16, 1> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) { f[0] = __bfloat162float(*p); }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) { *p = __float2bfloat16_rn(f[0]); }
+};
 
 __device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
@@ -50,131 +76,337 @@ __device__ __forceinline__ float warp_sum(float s) {
     return s;
 }
 
-// One warp per row.
-template <typename T>
-__global__ void __launch_bounds__(256) ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y,
-                                                     const T* __restrict__ gamma, const T* __restrict__ beta,
-                                                     long long rows, int d, float eps, T* __restrict__ out,
-                                                     float* __restrict__ mean_out, float* __restrict__ rstd_out) {
-    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (r >= rows) return;
-    const T* xr = x + r * d;
-    const T* yr = y ? y + r * d : nullptr;
+// A CTA's threads: R rows side by side, W warps on each.
+template <int W>
+struct Shape {
+    static constexpr int THREADS = W < 8 ? 256 : 32 * W;
+    static constexpr int R = THREADS / (32 * W);
+    static constexpr int TPR = 32 * W;  // threads per row
+};
+
+// Sum over the W warps of a row.  sh: [2][THREADS / 32], `phase` alternates from
+// call to call, so one barrier per call is enough.
+template <int W>
+__device__ __forceinline__ float row_sum(float s, float* sh, int phase) {
+    s = warp_sum(s);
+    if (W == 1) return s;
+    constexpr int N = Shape<W>::THREADS / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh[phase * N + warp] = s;
+    __syncthreads();
+    float a = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) a += sh[phase * N + warp / W * W + w];
+    return a;
+}
+template <int W>
+__device__ __forceinline__ float2 row_sum2(float2 s, float2* sh, int phase) {
+    s = make_float2(warp_sum(s.x), warp_sum(s.y));
+    if (W == 1) return s;
+    constexpr int N = Shape<W>::THREADS / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh[phase * N + warp] = s;
+    __syncthreads();
+    float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float2 t = sh[phase * N + warp / W * W + w];
+        a.x += t.x, a.y += t.y;
+    }
+    return a;
+}
+
+// E elements of row r of a tensor, this thread's: vectors of V, `t` + TPR i.
+template <typename T, int V, int E, int TPR>
+__device__ __forceinline__ void load_row(const T* p, long long r, int d, int t, float (&f)[E]) {
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) {
+        const int c = (t + TPR * i) * V;
+        if (c < d && TXL_BOUNDS(c + V <= d, 901, r * d + c)) {
+            Vec<T, V>::load(p + r * d + c, f + V * i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[V * i + k] = 0.f;
+        }
+    }
+}
+
+template <typename T, int V, int E, int W>
+__global__ void __launch_bounds__(Shape<W>::THREADS)
+ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restrict__ gamma,
+              const T* __restrict__ beta, long long rows, int d, float eps, T* __restrict__ out,
+              float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+    using S = Shape<W>;
+    __shared__ float sh[2 * S::THREADS / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = threadIdx.x % S::TPR;
+    const long long r = (long long)blockIdx.x * S::R + threadIdx.x / S::TPR;
+    const bool in = r < rows;  // (the barriers of a row are the CTA's)
+    float z[E];
+    if (in) {
+        load_row<T, V, E, S::TPR>(x, r, d, t, z);
+        if (y) {
+            float b[E];
+            load_row<T, V, E, S::TPR>(y, r, d, t, b);
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] += b[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) z[e] = 0.f;
+    }
     float s = 0.f;
-    for (int c = lane; c < d; c += 32) s += to_f(xr[c]) + (yr ? to_f(yr[c]) : 0.f);
-    const float mean = warp_sum(s) / d;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += z[e];
+    const float mean = row_sum<W>(s, sh, 0) / d;
     float q = 0.f;
-    for (int c = lane; c < d; c += 32) {
-        const float t = to_f(xr[c]) + (yr ? to_f(yr[c]) : 0.f) - mean;
-        q = fmaf(t, t, q);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (t + S::TPR * (e / V)) * V;
+        z[e] -= mean;
+        if (c < d) q = fmaf(z[e], z[e], q);
     }
-    const float rstd = 1.f / sqrtf(warp_sum(q) / d + eps);
-    for (int c = lane; c < d; c += 32) {
-        const float t = to_f(xr[c]) + (yr ? to_f(yr[c]) : 0.f) - mean;
-        out[r * d + c] = from_f<T>(fmaf(t * rstd, to_f(gamma[c]), to_f(beta[c])));
+    const float rstd = 1.f / sqrtf(row_sum<W>(q, sh, 1) / d + eps);
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) {
+        const int c = (t + S::TPR * i) * V;
+        if (c < d && TXL_BOUNDS(c + V <= d && r < rows, 902, r * d + c)) {
+            float g[V], b[V], o[V];
+            Vec<T, V>::load(gamma + c, g);
+            Vec<T, V>::load(beta + c, b);
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[k] = fmaf(z[V * i + k] * rstd, g[k], b[k]);
+            Vec<T, V>::store(out + r * d + c, o);
+        }
     }
-    if (lane == 0) {
+    if (t == 0) {
         mean_out[r] = mean;
         rstd_out[r] = rstd;
     }
 }
 
-// dx: one warp per row.
-template <typename T>
-__global__ void __launch_bounds__(256) ln_bwd_dx_kernel(const T* __restrict__ dout, const T* __restrict__ x,
-                                                        const T* __restrict__ y, const T* __restrict__ gamma,
-                                                        const float* __restrict__ mean,
-                                                        const float* __restrict__ rstd, const T* __restrict__ dres,
-                                                        long long rows, int d, T* __restrict__ dx) {
-    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (r >= rows) return;
-    const float mu = mean[r], rs = rstd[r];
-    float s1 = 0.f, s2 = 0.f;
-    for (int c = lane; c < d; c += 32) {
-        const float z = to_f(x[r * d + c]) + (y ? to_f(y[r * d + c]) : 0.f);
-        const float g = to_f(dout[r * d + c]) * to_f(gamma[c]);
-        s1 += g;
-        s2 = fmaf(g, (z - mu) * rs, s2);
+// CTAs per SM that the backward kernel is compiled for.
+template <int E, int W>
+constexpr int bwd_ctas() {
+    return Shape<W>::THREADS > 256 ? 1 : (E <= 8 ? 3 : 2);
+}
+
+template <typename T, int V, int E, int W>
+__global__ void __launch_bounds__(Shape<W>::THREADS, bwd_ctas<E, W>())
+ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __restrict__ y,
+              const T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
+              const T* __restrict__ dres, long long rows, int d, T* __restrict__ dx, float* __restrict__ part) {
+    using S = Shape<W>;
+    __shared__ float2 sh[2 * S::THREADS / 32];
+    __shared__ float fold[S::R > 1 ? S::THREADS / 2 * 2 * E : 1];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = threadIdx.x % S::TPR, lr = threadIdx.x / S::TPR;
+    float dg[E], db[E], gam[E];
+    load_row<T, V, E, S::TPR>(gamma, 0, d, t, gam);
+#pragma unroll
+    for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
+    int phase = 0;
+    for (long long r0 = (long long)blockIdx.x * S::R; r0 < rows; r0 += (long long)gridDim.x * S::R, phase ^= 1) {
+        const long long r = r0 + lr;
+        const bool in = r < rows;
+        float xh[E], g[E];
+        float rs = 0.f;
+        float2 s = make_float2(0.f, 0.f);
+        if (in) {
+            const float mu = mean[r];
+            rs = rstd[r];
+            load_row<T, V, E, S::TPR>(x, r, d, t, xh);
+            load_row<T, V, E, S::TPR>(dout, r, d, t, g);
+            if (y) {
+                float b[E];
+                load_row<T, V, E, S::TPR>(y, r, d, t, b);
+#pragma unroll
+                for (int e = 0; e < E; ++e) xh[e] += b[e];
+            }
+            // behind the row's end g is 0: what xh holds there reaches no sum
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                xh[e] = (xh[e] - mu) * rs;
+                dg[e] = fmaf(g[e], xh[e], dg[e]);
+                db[e] += g[e];
+                g[e] *= gam[e];
+                s.x += g[e];
+                s.y = fmaf(g[e], xh[e], s.y);
+            }
+            // dres is added to rs g here: its loads run beside the reduction, and hold
+            // no registers of their own through it
+            if (dres) {
+                float a[E];
+                load_row<T, V, E, S::TPR>(dres, r, d, t, a);
+#pragma unroll
+                for (int e = 0; e < E; ++e) g[e] = fmaf(g[e], rs, a[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) g[e] *= rs;
+            }
+        }
+        s = row_sum2<W>(s, sh, phase);
+        if (!in) continue;
+        const float c1 = rs * s.x / d, c2 = rs * s.y / d;
+#pragma unroll
+        for (int i = 0; i < E / V; ++i) {
+            const int c = (t + S::TPR * i) * V;
+            if (c < d && TXL_BOUNDS(c + V <= d, 903, r * d + c)) {
+                float o[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) o[k] = g[V * i + k] - fmaf(xh[V * i + k], c2, c1);
+                Vec<T, V>::store(dx + r * d + c, o);
+            }
+        }
     }
-    s1 = warp_sum(s1) / d;
-    s2 = warp_sum(s2) / d;
-    for (int c = lane; c < d; c += 32) {
-        const float z = to_f(x[r * d + c]) + (y ? to_f(y[r * d + c]) : 0.f);
-        const float g = to_f(dout[r * d + c]) * to_f(gamma[c]);
-        float v = rs * (g - s1 - (z - mu) * rs * s2);
-        if (dres) v += to_f(dres[r * d + c]);
-        dx[r * d + c] = from_f<T>(v);
+    // the CTA's rows fold in halves, into the first row's threads
+    if (S::R > 1) {
+#pragma unroll
+        for (int half = S::R / 2; half > 0; half >>= 1) {
+            __syncthreads();
+            const int n = half * S::TPR;
+            if (lr >= half && lr < 2 * half) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    fold[(2 * e) * n + threadIdx.x - n] = dg[e];
+                    fold[(2 * e + 1) * n + threadIdx.x - n] = db[e];
+                }
+            }
+            __syncthreads();
+            if (lr < half) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    dg[e] += fold[(2 * e) * n + threadIdx.x];
+                    db[e] += fold[(2 * e + 1) * n + threadIdx.x];
+                }
+            }
+        }
+    }
+    if (lr > 0) return;
+    float* to = part + (size_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (t + S::TPR * (e / V)) * V + e % V;
+        if (c < d) {
+            to[c] = dg[e];
+            to[d + c] = db[e];
+        }
     }
 }
 
-// Partial sums of dgamma and dbeta over one range of rows: part[range][2][d].
-template <typename T>
-__global__ void __launch_bounds__(256) ln_bwd_part_kernel(const T* __restrict__ dout, const T* __restrict__ x,
-                                                          const T* __restrict__ y, const float* __restrict__ mean,
-                                                          const float* __restrict__ rstd, long long rows, int d,
-                                                          long long range, float* __restrict__ part) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= d) return;
-    const long long r0 = blockIdx.y * range, r1 = r0 + range < rows ? r0 + range : rows;
-    float a = 0.f, b = 0.f;
-    for (long long r = r0; r < r1; ++r) {
-        const float z = to_f(x[r * d + c]) + (y ? to_f(y[r * d + c]) : 0.f);
-        const float g = to_f(dout[r * d + c]);
-        a = fmaf(g, (z - mean[r]) * rstd[r], a);
-        b += g;
-    }
-    part[(size_t)blockIdx.y * 2 * d + c] = a;
-    part[(size_t)blockIdx.y * 2 * d + d + c] = b;
-}
-
-__global__ void __launch_bounds__(256) ln_bwd_sum_kernel(const float* __restrict__ part, int n_part, int d,
-                                                         float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= 2 * d) return;
+// dgamma and dbeta: the CTAs' sums of 32 columns per CTA, 32 threads on each.
+__global__ void __launch_bounds__(1024) ln_bwd_sum_kernel(const float* __restrict__ part, int n_part, int d,
+                                                          float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    __shared__ float sh[32][33];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float a = 0.f;
-    for (int p = 0; p < n_part; ++p) a += part[(size_t)p * 2 * d + c];
-    if (c < d)
-        dgamma[c] = a;
-    else
-        dbeta[c - d] = a;
+    if (c < 2 * d) {
+#pragma unroll 4
+        for (int p = w; p < n_part; p += 32) a += part[(size_t)p * 2 * d + c];
+    }
+    sh[w][lane] = a;
+    __syncthreads();
+    const float s = warp_sum(sh[lane][w]);  // column w of this CTA's 32
+    const int cw = blockIdx.x * 32 + w;
+    if (lane == 0 && cw < 2 * d) {
+        if (cw < d)
+            dgamma[cw] = s;
+        else
+            dbeta[cw - d] = s;
+    }
 }
 
-constexpr int kPartRows = 64;  // rows of one partial sum, at least
-constexpr int kMaxParts = 1024;
-
-int ln_parts(long long rows) {
-    const long long p = (rows + kPartRows - 1) / kPartRows;
-    return (int)(p < 1 ? 1 : (p > kMaxParts ? kMaxParts : p));
+// Launch with programmatic stream serialisation (every kernel here waits for
+// the one before it before its first global access).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-template <typename T>
+// Calls f with the element and warp counts that a row of d elements takes: as
+// few warps as hold it at 32 elements per lane (forward) or 16 (backward, which
+// keeps two sums per element besides).
+template <int E, int W>
+struct Pick {
+    static constexpr int e = E, w = W;
+};
+template <typename F>
+cudaError_t pick_fwd(int d, F f) {
+    if (d <= 256) return f(Pick<8, 1>());
+    if (d <= 512) return f(Pick<16, 1>());
+    if (d <= 1024) return f(Pick<32, 1>());
+    if (d <= 2048) return f(Pick<32, 2>());
+    if (d <= 4096) return f(Pick<32, 4>());
+    if (d <= 8192) return f(Pick<32, 8>());
+    return f(Pick<32, 16>());
+}
+template <typename F>
+cudaError_t pick_bwd(int d, F f) {
+    if (d <= 256) return f(Pick<8, 1>());
+    if (d <= 512) return f(Pick<16, 1>());
+    if (d <= 1024) return f(Pick<16, 2>());
+    if (d <= 2048) return f(Pick<16, 4>());
+    if (d <= 4096) return f(Pick<16, 8>());
+    if (d <= 8192) return f(Pick<16, 16>());
+    return f(Pick<16, 32>());
+}
+
+// CTAs of the backward pass: one round of resident ones at most.
+int bwd_grid(long long rows, int d) {
+    int per_sm = 1, r = 1;
+    pick_bwd(d, [&](auto k) {
+        per_sm = bwd_ctas<decltype(k)::e, decltype(k)::w>();
+        r = Shape<decltype(k)::w>::R;
+        return cudaSuccess;
+    });
+    const long long want = (rows + r - 1) / r, most = (long long)per_sm * current_sm_count();
+    return (int)(want < 1 ? 1 : (want < most ? want : most));
+}
+
+template <typename T, int V>
 cudaError_t ln_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows, int d,
                    float eps, void* out, float* mean, float* rstd, cudaStream_t stream) {
     if (rows <= 0) return cudaSuccess;
-    ln_fwd_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
-        static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(gamma),
-        static_cast<const T*>(beta), rows, d, eps, static_cast<T*>(out), mean, rstd);
-    return cudaGetLastError();
+    return pick_fwd(d, [&](auto k) {
+        constexpr int E = decltype(k)::e, W = decltype(k)::w;
+        const long long ctas = (rows + Shape<W>::R - 1) / Shape<W>::R;
+        if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+        return launch_pdl(ln_fwd_kernel<T, V, E, W>, (unsigned)ctas, (unsigned)Shape<W>::THREADS, stream,
+                          static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(gamma),
+                          static_cast<const T*>(beta), rows, d, eps, static_cast<T*>(out), mean, rstd);
+    });
 }
 
-template <typename T>
+template <typename T, int V>
 cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
                    const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
                    float* dbeta, float* part, cudaStream_t stream) {
-    const T* dd = static_cast<const T*>(dout);
-    const T* xx = static_cast<const T*>(x);
-    const T* yy = static_cast<const T*>(y);
-    const int parts = ln_parts(rows);
-    if (rows > 0)
-        ln_bwd_dx_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
-            dd, xx, yy, static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d,
-            static_cast<T*>(dx));
-    ln_bwd_part_kernel<T><<<dim3((d + 255) / 256, parts), 256, 0, stream>>>(dd, xx, yy, mean, rstd, rows, d,
-                                                                         (rows + parts - 1) / parts, part);
-    ln_bwd_sum_kernel<<<(2 * d + 255) / 256, 256, 0, stream>>>(part, parts, d, dgamma, dbeta);
-    return cudaGetLastError();
+    // (no rows: one CTA that adds nothing writes the zeros to be summed)
+    const int grid = bwd_grid(rows, d);
+    const cudaError_t e = pick_bwd(d, [&](auto k) {
+        constexpr int E = decltype(k)::e, W = decltype(k)::w;
+        return launch_pdl(ln_bwd_kernel<T, V, E, W>, (unsigned)grid, (unsigned)Shape<W>::THREADS, stream,
+                          static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
+                          static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d,
+                          static_cast<T*>(dx), part);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, stream, part, grid, d, dgamma, dbeta);
 }
 
 }  // namespace
@@ -182,21 +414,24 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
 cudaError_t launch_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
                                   int d, float eps, void* out, float* mean, float* rstd, int bf16,
                                   cudaStream_t stream) {
-    return bf16 ? ln_fwd<__nv_bfloat16>(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream)
-                : ln_fwd<float>(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream);
+    if (bf16)
+        return (d % 8 ? ln_fwd<__nv_bfloat16, 1> : ln_fwd<__nv_bfloat16, 8>)(x, y, gamma, beta, rows, d, eps, out, mean,
+                                                                           rstd, stream);
+    return (d % 4 ? ln_fwd<float, 1> : ln_fwd<float, 4>)(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream);
 }
 
-size_t layer_norm_bwd_workspace_bytes(long long rows, int d) {
-    return (size_t)ln_parts(rows) * 2 * d * sizeof(float);
-}
+size_t layer_norm_bwd_workspace_bytes(long long rows, int d) { return (size_t)bwd_grid(rows, d) * 2 * d * sizeof(float); }
 
 cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
                                   const float* mean, const float* rstd, const void* dres, long long rows, int d,
                                   void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
                                   cudaStream_t stream) {
     float* part = static_cast<float*>(workspace);
-    return bf16 ? ln_bwd<__nv_bfloat16>(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part, stream)
-                : ln_bwd<float>(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part, stream);
+    if (bf16)
+        return (d % 8 ? ln_bwd<__nv_bfloat16, 1> : ln_bwd<__nv_bfloat16, 8>)(dout, x, y, gamma, mean, rstd, dres, rows, d,
+                                                                           dx, dgamma, dbeta, part, stream);
+    return (d % 4 ? ln_bwd<float, 1> : ln_bwd<float, 4>)(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta,
+                                                        part, stream);
 }
 
 TXL_BOUNDS_READER(bounds_word_layer_norm_train)
