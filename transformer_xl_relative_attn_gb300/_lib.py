@@ -166,12 +166,27 @@ def _invoke(device, name: str, *args):
     """Calls C entry point ``name`` with ``device`` current, so that the
     library's launches, its status word and its static scratch are those of
     the device the call's tensors live on."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    # entering the device's context costs more than the call where it is current already
+    index = device if type(device) is int else getattr(device, "index", None)
+    if index is not None and index == torch.cuda.current_device():
+        return fn(*args)
     with torch.cuda.device(device):
-        return getattr(load(), name)(*args)
+        return fn(*args)
+
+
+_functions: dict = {}
+# handle of a device's current stream without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, device) -> int:
     if stream is None:
+        index = device if type(device) is int else getattr(device, "index", None)
+        if _raw_stream is not None and index is not None:
+            return _raw_stream(index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -179,6 +194,9 @@ def _stream(stream, device) -> int:
 def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device=None) -> None:
     """Type, device, dtype, shape and contiguity of one argument.  ``device``:
     the device every tensor of the call must share (the kernels run there)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and
+            (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if device is not None and t.device != device:

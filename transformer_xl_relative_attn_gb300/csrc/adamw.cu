@@ -45,7 +45,15 @@ namespace txl {
 
 namespace {
 
-constexpr int kPerCta = 32;  // blocks per CTA (4 per warp)
+// Blocks per CTA: a multiple of its 8 warps, one each where that already gives
+// every SM no more than a few CTAs (a small step is over when its longest CTA is),
+// up to 8 each: fewer starts, and a prefetch that pays.
+constexpr unsigned kMinPerCta = 8, kMaxPerCta = 64;
+unsigned blocks_per_cta(long long blocks) {
+    unsigned per = kMinPerCta;
+    while (per < kMaxPerCta && blocks > 4ll * per * current_sm_count()) per *= 2;
+    return per;
+}
 
 // What the update launch needs of this step, written by adamw_coef_kernel.
 struct AdamwCoef {
@@ -97,22 +105,31 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// Over the warp, in one instruction (five exchanges deep it was 2 of 88
+// instructions an element, and their latency twice per block).
 __device__ __forceinline__ float warp_max_nan(float a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-    return a;
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(a));
+    return r;
 }
 
 // q >= 0 to a neighbouring e4m3 value, up with the probability of the fraction
-// by 16 random bits.  e4m3 keeps 3 mantissa bits, so 20 bits of the fp32
+// by 16 random bits (random20: those, followed by four zeros).  e4m3 keeps 3 mantissa bits, so 20 bits of the fp32
 // pattern are cut off after the random bits were added below the cut; its
 // subnormals (below 2^-6) step by 2^-9, which are the steps of the numbers
 // from 2^-6 on, so they are moved there and back.
-__device__ __forceinline__ float round_e4m3(float q, unsigned r16) {
-    const bool low = q < 0x1p-6f;
-    const float t = low ? __fadd_rn(q, 0x1p-6f) : q;
-    const float c = __uint_as_float((__float_as_uint(t) + (r16 << 4)) & 0xFFF00000u);
-    return fminf(low ? __fadd_rn(c, -0x1p-6f) : c, 448.f);
+// (What is rounded up past 448 is left to the conversion, which saturates there.)
+__device__ __forceinline__ float round_e4m3(float q, unsigned random20) {
+    const float c = q < 0x1p-6f ? 0x1p-6f : 0.f;
+    const float t = __uint_as_float((__float_as_uint(__fadd_rn(q, c)) + random20) & 0xFFF00000u);
+    return __fadd_rn(t, -c);
+}
+
+// 1 / x to 1 ulp (an x below 2^-126 counts as 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 template <typename T>
@@ -142,24 +159,25 @@ __device__ __forceinline__ float load1(const T* p) {
 __device__ __forceinline__ void store1(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 
-// Elements i .. i+3 of a tensor of n (0 behind its end).
+// Elements 0 .. 3 of p, of which `left` are the tensor's (0 behind its end).
+// `full`: the whole block is the tensor's.
 template <typename T>
-__device__ __forceinline__ void load4_tail(const T* p, long long i, long long n, float (&f)[4]) {
-    if (i + 4 <= n) {
-        load4(p + i, f);
+__device__ __forceinline__ void load4_tail(const T* p, bool full, int left, float (&f)[4]) {
+    if (full) {
+        load4(p, f);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = i + k < n ? load1(p + i + k) : 0.f;
+        for (int k = 0; k < 4; ++k) f[k] = k < left ? load1(p + k) : 0.f;
     }
 }
 template <typename T>
-__device__ __forceinline__ void store4_tail(T* p, long long i, long long n, const float (&f)[4]) {
-    if (i + 4 <= n) {
-        store4(p + i, f);
+__device__ __forceinline__ void store4_tail(T* p, bool full, int left, const float (&f)[4]) {
+    if (full) {
+        store4(p, f);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (i + k < n) store1(p + i + k, f[k]);
+            if (k < left) store1(p + k, f[k]);
     }
 }
 
@@ -180,21 +198,24 @@ __device__ __forceinline__ int find_entry(const AdamwTable<CAP>& t, unsigned b) 
 // Sum of g g over each CTA's blocks: part[blockIdx.x].
 template <typename G, int CAP>
 __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__ AdamwTable<CAP> t,
-                                                         unsigned n_blocks, float* __restrict__ part) {
+                                                         unsigned n_blocks, unsigned per,
+                                                         float* __restrict__ part) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sh[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned b0 = blockIdx.x * kPerCta;
+    const unsigned b0 = blockIdx.x * per, end = min(n_blocks, b0 + per);
     int e = find_entry(t, b0);
     float s = 0.f;
-    for (int k = warp; k < kPerCta && b0 + k < n_blocks; k += 8) {
-        const unsigned b = b0 + k;
+    for (unsigned b = b0 + warp; b < end; b += 8) {
         while (e + 1 < t.n && t.e[e + 1].start <= b) ++e;
-        const long long i = (long long)(b - t.e[e].start) * kAdamwBlock + lane * 4;
+        const long long i = (long long)(b - t.e[e].start) * kAdamwBlock, n = t.e[e].n - i;
+        const bool full = n >= kAdamwBlock;
+        const int left = full ? kAdamwBlock : (int)n - lane * 4;
+        const G* const gp = static_cast<const G*>(t.e[e].g) + i + lane * 4;
         float g[2][4];
-        load4_tail(static_cast<const G*>(t.e[e].g), i, t.e[e].n, g[0]);
-        load4_tail(static_cast<const G*>(t.e[e].g), i + 128, t.e[e].n, g[1]);
+        load4_tail(gp, full, left, g[0]);
+        load4_tail(gp + 128, full, left - 128, g[1]);
 #pragma unroll
         for (int x = 0; x < 8; ++x) s = fmaf(g[x >> 2][x & 3], g[x >> 2][x & 3], s);
     }
@@ -210,65 +231,72 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
 }
 
 // The step's coefficients, from the partial sums of g g (max_norm = 0: no clipping).
+// 1 - b^t = -expm1(t ln b) with ln b from the host: fp32 keeps it to 2^-22 however
+// small, and double precision's pow alone took longer than a small update.
 __global__ void __launch_bounds__(1024) adamw_coef_kernel(const float* __restrict__ part, unsigned n_part,
-                                                          double beta1, double beta2, double max_norm, unsigned seed,
-                                                          const float* lr, long long* steps, float* grad_norm,
-                                                          AdamwCoef* coef) {
+                                                          double ln_beta1, double ln_beta2, float max_norm,
+                                                          unsigned seed, const float* lr, long long* steps,
+                                                          float* grad_norm, AdamwCoef* coef) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ double sh[32];
-    __shared__ double corr[2];
+    __shared__ float sh[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    double s = 0.0;
-    for (unsigned i = threadIdx.x; i < n_part; i += blockDim.x) s += part[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sh[warp] = s;
     const long long t = *steps + 1;
-    if (threadIdx.x < 2) corr[threadIdx.x] = 1.0 - pow(threadIdx.x ? beta2 : beta1, (double)t);
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    AdamwCoef c = {1.f, 0.f, 0.f, *lr, mix32(seed + (unsigned)t * 0x9E3779B1u), 0};
-    if (max_norm > 0.0) {
-        double a = 0.0;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) a += sh[w];
-        const double norm = sqrt(a);
-        if (grad_norm) *grad_norm = (float)norm;
-        c.skip = !(norm < (double)INFINITY);
-        c.clip = norm > max_norm ? (float)(max_norm / norm) : 1.f;
+    const float rate = *lr;
+    float s = 0.f;
+    if (max_norm > 0.f) {
+        for (unsigned i = threadIdx.x; i < n_part; i += blockDim.x) s += part[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sh[warp] = s;
+        __syncthreads();
+        s = lane < (int)(blockDim.x >> 5) ? sh[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
-    c.step_size = (float)((double)c.lr / corr[0]);
-    c.root_corr = (float)(1.0 / sqrt(corr[1]));
+    if (threadIdx.x != 0) return;
+    AdamwCoef c = {1.f, 0.f, 0.f, rate, mix32(seed + (unsigned)t * 0x9E3779B1u), 0};
+    if (max_norm > 0.f) {
+        const float norm = sqrtf(s);
+        if (grad_norm) *grad_norm = norm;
+        c.skip = !(norm < INFINITY);
+        c.clip = norm > max_norm ? max_norm / norm : 1.f;
+    }
+    c.step_size = rate / -expm1f((float)((double)t * ln_beta1));
+    c.root_corr = 1.f / sqrtf(-expm1f((float)((double)t * ln_beta2)));
     if (!c.skip) *steps = t;
     *coef = c;
 }
 
 // One block's state in 8 bits: codes (4 per 32-bit word) and scale of x.
-// keep: what is not zero stays so.
-template <bool KEEP>
-__device__ __forceinline__ float quantize(const float (&x)[8], const unsigned (&r16)[8], unsigned (&code)[2]) {
+// ROOT: x is a square root, not negative, and what is not zero stays so.
+// random: 16 bits of it from bit SHIFT on are each element's.
+template <bool ROOT, int SHIFT>
+__device__ __forceinline__ float quantize(const float (&x)[8], const unsigned (&random)[8], unsigned (&code)[2]) {
     float a = fabsf(x[0]);
 #pragma unroll
     for (int k = 1; k < 8; ++k) a = max_nan(a, fabsf(x[k]));
     a = warp_max_nan(a);
     const bool fine = a > 0x1p-110f && a < INFINITY;
-    const float inv = fine ? __fmul_rn(__frcp_rn(a), 448.f) : 0.f;
+    const float inv = __fmul_rn(__frcp_rn(a), 448.f);
     float q[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float t = fine ? __fmul_rn(fabsf(x[k]), inv) : 0.f;
-        q[k] = round_e4m3(t, r16[k]);
-        if (KEEP && t > 0.f) q[k] = fmaxf(q[k], 0x1p-9f);
-        q[k] = copysignf(q[k], x[k]);
+        const float t = __fmul_rn(fabsf(x[k]), inv);
+        q[k] = round_e4m3(t, ((random[k] >> SHIFT) & 0xFFFFu) * 16u);
+        if (ROOT)
+            q[k] = fmaxf(q[k], t > 0.f ? 0x1p-9f : 0.f);
+        else
+            q[k] = copysignf(q[k], x[k]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
         const unsigned hi =
             __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
-        code[h] = lo | (hi << 16);
+        code[h] = fine ? lo | (hi << 16) : 0u;
     }
-    // a NaN is not above the limit, and stays
+    // a NaN is not at the limit or below, and stays
     return a <= 0x1p-110f ? 0.f : __fmul_rn(a, 1.f / 448.f);
 }
 
@@ -282,107 +310,155 @@ __device__ __forceinline__ void codes_to_float(unsigned w, float s, float* f) {
     }
 }
 
-// The update.  P: type of the parameters (bf16 with a master copy), G: of the
-// gradients.  `first`: the launch's first block in the flat buffers.
+// A lane's 8 elements of one block as they lie in memory, and where they go back.
+template <typename P, typename G, bool EIGHT>
+struct AdamwRaw {
+    P* p;       // the lane's first element
+    int left;   // elements of the tensor from there on, kAdamwBlock where the whole block is its
+    float wd;
+    unsigned blk;  // block of the flat buffers
+    float g[8], w[8];
+    float m[EIGHT ? 1 : 8], v[EIGHT ? 1 : 8];
+    unsigned mc[2], vc[2];
+    float ms, vs;
+};
+
 template <typename P, typename G, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks,
-                                                    unsigned first, const AdamwFlat flat, float b1, float b1c,
-                                                    float b2, float b2c, float eps,
-                                                    const AdamwCoef* __restrict__ coef) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void adamw_load(const AdamwTable<CAP>& t, int& e, unsigned b, unsigned first,
+                                           const AdamwFlat& flat, AdamwRaw<P, G, EIGHT>& r) {
     constexpr bool MASTER = sizeof(P) == 2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned b0 = blockIdx.x * kPerCta;
-    const AdamwCoef c = *coef;
-    if (c.skip) return;
-    int e = find_entry(t, b0);
-    for (int k = warp; k < kPerCta && b0 + k < n_blocks; k += 8) {
-        const unsigned b = b0 + k;
-        while (e + 1 < t.n && t.e[e + 1].start <= b) ++e;
-        const long long n = t.e[e].n;
-        const long long i = (long long)(b - t.e[e].start) * kAdamwBlock + lane * 4;
-        P* const pp = static_cast<P*>(t.e[e].p);
-        const G* const gp = static_cast<const G*>(t.e[e].g);
-        const float decay = t.e[e].wd * c.lr;
-        const size_t blk = (size_t)first + b, at = blk * kAdamwBlock + lane * 4;
-        float g[8], p[8], m[8], v[8];
+    const int lane = threadIdx.x & 31;
+    while (e + 1 < t.n && t.e[e + 1].start <= b) ++e;
+    const long long i = (long long)(b - t.e[e].start) * kAdamwBlock, n = t.e[e].n - i;
+    const bool full = n >= kAdamwBlock;
+    r.left = full ? kAdamwBlock : (int)n - lane * 4;
+    r.p = static_cast<P*>(t.e[e].p) + i + lane * 4;
+    r.wd = t.e[e].wd;
+    r.blk = first + b;
+    const G* const gp = static_cast<const G*>(t.e[e].g) + i + lane * 4;
+    const size_t at = (size_t)r.blk * kAdamwBlock + lane * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        load4_tail(gp + 128 * h, full, r.left - 128 * h, *reinterpret_cast<float(*)[4]>(r.g + 4 * h));
+        if (MASTER)
+            load4(flat.master + at + 128 * h, *reinterpret_cast<float(*)[4]>(r.w + 4 * h));
+        else
+            load4_tail(reinterpret_cast<const float*>(r.p) + 128 * h, full, r.left - 128 * h,
+                       *reinterpret_cast<float(*)[4]>(r.w + 4 * h));
+        if constexpr (EIGHT) {
+            r.mc[h] = *reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(flat.m) + at + 128 * h);
+            r.vc[h] = *reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(flat.v) + at + 128 * h);
+        } else {
+            load4(static_cast<const float*>(flat.m) + at + 128 * h, *reinterpret_cast<float(*)[4]>(r.m + 4 * h));
+            load4(static_cast<const float*>(flat.v) + at + 128 * h, *reinterpret_cast<float(*)[4]>(r.v + 4 * h));
+        }
+    }
+    if constexpr (EIGHT) {
+        r.ms = flat.ms[r.blk];
+        r.vs = flat.vs[r.blk];
+    }
+}
+
+template <typename P, typename G, bool EIGHT>
+__device__ __forceinline__ void adamw_update(const AdamwRaw<P, G, EIGHT>& r, const AdamwFlat& flat,
+                                             const AdamwCoef& c, float b1, float b1c, float b2, float b2c,
+                                             float eps) {
+    constexpr bool MASTER = sizeof(P) == 2;
+    const int lane = threadIdx.x & 31;
+    const size_t at = (size_t)r.blk * kAdamwBlock + lane * 4;
+    const float decay = r.wd * c.lr;
+    const bool full = r.left == kAdamwBlock;
+    float m[8], v[8], p[8], root[8];
+    if constexpr (EIGHT) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            load4_tail(gp, i + 128 * h, n, *reinterpret_cast<float(*)[4]>(g + 4 * h));
-            if (MASTER)
-                load4(flat.master + at + 128 * h, *reinterpret_cast<float(*)[4]>(p + 4 * h));
-            else
-                load4_tail(reinterpret_cast<const float*>(pp), i + 128 * h, n, *reinterpret_cast<float(*)[4]>(p + 4 * h));
+            codes_to_float(r.mc[h], r.ms, m + 4 * h);
+            codes_to_float(r.vc[h], r.vs, v + 4 * h);
         }
-        if (EIGHT) {
-            const uint8_t* mc = static_cast<const uint8_t*>(flat.m) + at;
-            const uint8_t* vc = static_cast<const uint8_t*>(flat.v) + at;
-            const float ms = flat.ms[blk], vs = flat.vs[blk];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                codes_to_float(*reinterpret_cast<const unsigned*>(mc + 128 * h), ms, m + 4 * h);
-                codes_to_float(*reinterpret_cast<const unsigned*>(vc + 128 * h), vs, v + 4 * h);
-            }
+        for (int x = 0; x < 8; ++x) v[x] = __fmul_rn(v[x], v[x]);
+    } else {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = __fmul_rn(v[x], v[x]);
-        } else {
+        for (int x = 0; x < 8; ++x) m[x] = r.m[x], v[x] = r.v[x];
+    }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                load4(static_cast<const float*>(flat.m) + at + 128 * h, *reinterpret_cast<float(*)[4]>(m + 4 * h));
-                load4(static_cast<const float*>(flat.v) + at + 128 * h, *reinterpret_cast<float(*)[4]>(v + 4 * h));
-            }
+    for (int x = 0; x < 8; ++x) {
+        // each product and sum rounded by itself: what the states become does not hang on
+        // how the compiler fuses them
+        const float gs = __fmul_rn(r.g[x], c.clip);
+        m[x] = __fadd_rn(__fmul_rn(m[x], b1), __fmul_rn(gs, b1c));
+        v[x] = __fadd_rn(__fmul_rn(v[x], b2), __fmul_rn(__fmul_rn(gs, gs), b2c));
+        root[x] = __fsqrt_rn(v[x]);
+        // the quotient to 2 ulp: it is added to p scaled by the step size
+        const float u = m[x] * rcp_approx(fmaf(root[x], c.root_corr, eps));
+        p[x] = r.w[x] - fmaf(r.w[x], decay, u * c.step_size);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float(&p4)[4] = *reinterpret_cast<const float(*)[4]>(p + 4 * h);
+        store4_tail(r.p + 128 * h, full, r.left - 128 * h, p4);
+        if (MASTER) store4(flat.master + at + 128 * h, p4);
+    }
+    if constexpr (EIGHT) {
+        unsigned random[8], code[2];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) random[x] = mix32((unsigned)at + 128u * (x >> 2) + (x & 3) + c.key);
+        uint8_t* mc = static_cast<uint8_t*>(flat.m) + at;
+        uint8_t* vc = static_cast<uint8_t*>(flat.v) + at;
+        const float ms = quantize<false, 0>(m, random, code);
+        *reinterpret_cast<unsigned*>(mc) = code[0];
+        *reinterpret_cast<unsigned*>(mc + 128) = code[1];
+        const float vs = quantize<true, 16>(root, random, code);
+        *reinterpret_cast<unsigned*>(vc) = code[0];
+        *reinterpret_cast<unsigned*>(vc + 128) = code[1];
+        if (lane == 0) {
+            flat.ms[r.blk] = ms;
+            flat.vs[r.blk] = vs;
         }
-        float root[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            // each product and sum rounded by itself: what the states become does not hang on
-            // how the compiler fuses them
-            const float gs = __fmul_rn(g[x], c.clip);
-            m[x] = __fadd_rn(__fmul_rn(m[x], b1), __fmul_rn(gs, b1c));
-            v[x] = __fadd_rn(__fmul_rn(v[x], b2), __fmul_rn(__fmul_rn(gs, gs), b2c));
-            root[x] = __fsqrt_rn(v[x]);
-            // the quotient to 2 ulp: it is added to p scaled by the step size
-            const float u = __fdividef(m[x], fmaf(root[x], c.root_corr, eps));
-            p[x] -= fmaf(p[x], decay, u * c.step_size);
-        }
+    } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float(&p4)[4] = *reinterpret_cast<const float(*)[4]>(p + 4 * h);
-            store4_tail(pp, i + 128 * h, n, p4);
-            if (MASTER) store4(flat.master + at + 128 * h, p4);
-        }
-        if (EIGHT) {
-            unsigned lo[8], hi[8], code[2];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const unsigned h = mix32((unsigned)at + 128u * (x >> 2) + (x & 3) + c.key);
-                lo[x] = h & 0xFFFFu;
-                hi[x] = h >> 16;
-            }
-            uint8_t* mc = static_cast<uint8_t*>(flat.m) + at;
-            uint8_t* vc = static_cast<uint8_t*>(flat.v) + at;
-            const float ms = quantize<false>(m, lo, code);
-            *reinterpret_cast<unsigned*>(mc) = code[0];
-            *reinterpret_cast<unsigned*>(mc + 128) = code[1];
-            const float vs = quantize<true>(root, hi, code);
-            *reinterpret_cast<unsigned*>(vc) = code[0];
-            *reinterpret_cast<unsigned*>(vc + 128) = code[1];
-            if (lane == 0) {
-                flat.ms[blk] = ms;
-                flat.vs[blk] = vs;
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                store4(static_cast<float*>(flat.m) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(m + 4 * h));
-                store4(static_cast<float*>(flat.v) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(v + 4 * h));
-            }
+            store4(static_cast<float*>(flat.m) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(m + 4 * h));
+            store4(static_cast<float*>(flat.v) + at + 128 * h, *reinterpret_cast<const float(*)[4]>(v + 4 * h));
         }
     }
 }
 
-unsigned ctas(unsigned blocks) { return (blocks + kPerCta - 1) / kPerCta; }
+// The update.  P: type of the parameters (bf16 with a master copy), G: of the
+// gradients.  `first`: the launch's first block in the flat buffers.  With 8-bit
+// states a block takes longer to compute than to fetch, so the next one's loads
+// are issued before it.
+template <typename P, typename G, bool EIGHT, int CAP>
+__global__ void __launch_bounds__(256, EIGHT ? 3 : 4)
+adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks, unsigned per, unsigned first, const AdamwFlat flat,
+             float b1, float b1c, float b2, float b2c, float eps, const AdamwCoef* __restrict__ coef) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const unsigned warp = threadIdx.x >> 5, b0 = blockIdx.x * per;
+    const AdamwCoef c = *coef;
+    if (c.skip) return;
+    const unsigned b1st = b0 + warp, end = min(n_blocks, b0 + per);
+    if (b1st >= end) return;
+    int e = find_entry(t, b1st);
+    if constexpr (EIGHT) {
+        AdamwRaw<P, G, EIGHT> next;
+        adamw_load(t, e, b1st, first, flat, next);
+#pragma unroll 1
+        for (unsigned b = b1st; b < end; b += 8) {
+            const AdamwRaw<P, G, EIGHT> cur = next;
+            if (b + 8 < end) adamw_load(t, e, b + 8, first, flat, next);
+            adamw_update(cur, flat, c, b1, b1c, b2, b2c, eps);
+        }
+    } else {
+        for (unsigned b = b1st; b < end; b += 8) {
+            AdamwRaw<P, G, EIGHT> cur;
+            adamw_load(t, e, b, first, flat, cur);
+            adamw_update(cur, flat, c, b1, b1c, b2, b2c, eps);
+        }
+    }
+}
+
+unsigned ctas(unsigned blocks, unsigned per) { return (blocks + per - 1) / per; }
 
 // Launch with programmatic stream serialisation (every kernel here waits for
 // the one before it before its first global access).
@@ -429,25 +505,26 @@ template <int CAP>
 cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     AdamwCoef* coef = static_cast<AdamwCoef*>(a.workspace);
     float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + coef_bytes());
+    const unsigned per = blocks_per_cta(blocks);
     unsigned n_part = 0;
     cudaError_t e = cudaSuccess;
     if (a.max_norm > 0) {
         e = each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned) {
             float* to = part + n_part;
-            n_part += ctas(n);
-            return a.bf16_grad ? launch_pdl(adamw_norm_kernel<__nv_bfloat16, CAP>, ctas(n), 256u, stream, t, n, to)
-                               : launch_pdl(adamw_norm_kernel<float, CAP>, ctas(n), 256u, stream, t, n, to);
+            n_part += ctas(n, per);
+            return a.bf16_grad ? launch_pdl(adamw_norm_kernel<__nv_bfloat16, CAP>, ctas(n, per), 256u, stream, t, n, per, to)
+                               : launch_pdl(adamw_norm_kernel<float, CAP>, ctas(n, per), 256u, stream, t, n, per, to);
         });
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(adamw_coef_kernel, 1, n_part ? 1024u : 32u, stream, part, n_part, a.beta1, a.beta2, a.max_norm, a.seed,
-                   a.lr, a.steps, a.grad_norm, coef);
+    e = launch_pdl(adamw_coef_kernel, 1, a.max_norm > 0 ? 1024u : 32u, stream, part, n_part, std::log(a.beta1),
+                   std::log(a.beta2), (float)a.max_norm, a.seed, a.lr, a.steps, a.grad_norm, coef);
     if (e != cudaSuccess) return e;
     const AdamwFlat flat = {a.master, a.exp_avg, a.exp_avg_scale, a.exp_avg_sq, a.exp_avg_sq_scale};
     const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
     return each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned first) {
         auto go = [&](auto kern) {
-            return launch_pdl(kern, ctas(n), 256u, stream, t, n, first, flat, b1, b1c, b2, b2c, (float)a.eps, coef);
+            return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, first, flat, b1, b1c, b2, b2c, (float)a.eps, coef);
         };
         using B = __nv_bfloat16;
         if (a.eight_bit) {
@@ -473,7 +550,7 @@ long long adamw_blocks(const txl_adamw_tensor* tensors, int n_tensors) {
 // Coefficients, and one partial sum per CTA of each group of tensors (a group's
 // last CTA may be partly filled: one more per group at most).
 size_t adamw_workspace_bytes(long long blocks) {
-    return coef_bytes() + (size_t)(blocks / kPerCta + blocks / kSmallTable + 2) * sizeof(float);
+    return coef_bytes() + (size_t)(blocks / blocks_per_cta(blocks) + blocks / kSmallTable + 2) * sizeof(float);
 }
 
 cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream) {

@@ -5,7 +5,7 @@ step of the computation runs in libtxl.so's CUDA kernels."""
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import functools
 from typing import Sequence
 
 import torch
@@ -13,6 +13,7 @@ import torch
 from . import _lib
 from ._lib import TXL_BF16, TXL_F32, AdamwTensor, TxlError, _dtype_code, _invoke, _need, _stream
 
+_HERE = contextlib.nullcontext()
 STATE_BLOCK = 256  # elements of one block of a flat optimizer state
 
 
@@ -21,7 +22,7 @@ def _on(stream, device):
     hands freed memory out again in the order of the stream it was allocated
     on, so a call's buffers belong to the call's stream."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -36,8 +37,14 @@ def _scratch(workspace, need: int, device) -> int:
     return workspace.data_ptr()
 
 
-def _row_args(x, y, gamma, beta, extra):
-    """Checks the tensors of a LayerNorm call; returns (rows, d)."""
+@functools.lru_cache(maxsize=1024)
+def _workspace_need(device, name: str, *sizes) -> int:
+    """Workspace of a call of these sizes on ``device``: a function of both alone."""
+    return int(_invoke(device, name, *sizes))
+
+
+def _row_args(x, y, gamma, beta):
+    """Checks the tensors that both LayerNorm calls share; returns (rows, d)."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor [..., d]")
     if x.dtype not in (torch.bfloat16, torch.float32):
@@ -52,9 +59,6 @@ def _row_args(x, y, gamma, beta, extra):
     _need(gamma, "gamma", (d,), dt, dev)
     if beta is not None:
         _need(beta, "beta", (d,), dt, dev)
-    for name, t in extra:
-        if t is not None:
-            _need(t, name, shape, dt, dev)
     return x.numel() // d, d
 
 
@@ -67,17 +71,21 @@ def layer_norm_fwd(x, gamma, beta, y=None, eps=1e-5, out=None, mean=None, rstd=N
     (y optional), keeping the statistics that layer_norm_bwd takes.  x [..., d]
     bf16 or fp32 with 1 <= d <= 16384; mean, rstd fp32 [...].  Returns
     (out, mean, rstd); out overlaps no input."""
-    rows, d = _row_args(x, y, gamma, beta, (("out", out),))
+    rows, d = _row_args(x, y, gamma, beta)
     dev, st = x.device, x.shape[:-1]
     with _on(stream, dev):
         if out is None:
             out = torch.empty_like(x)
+        else:
+            _need(out, "out", x.shape, x.dtype, dev)
         if mean is None:
             mean = torch.empty(st, dtype=torch.float32, device=dev)
+        else:
+            _need(mean, "mean", st, torch.float32, dev)
         if rstd is None:
             rstd = torch.empty(st, dtype=torch.float32, device=dev)
-    _need(mean, "mean", st, torch.float32, dev)
-    _need(rstd, "rstd", st, torch.float32, dev)
+        else:
+            _need(rstd, "rstd", st, torch.float32, dev)
     rc = _invoke(dev, "txl_layer_norm_fwd", x.data_ptr(), _ptr(y), gamma.data_ptr(), beta.data_ptr(), rows, d,
                  float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _dtype_code(x), _stream(stream, dev))
     if rc != 0:
@@ -101,13 +109,14 @@ def layer_norm_bwd(dout, x, gamma, mean, rstd, y=None, dres=None, stream=None, w
     (fp32 [d], summed in a fixed order).  grads: a dict of preallocated tensors
     to fill; workspace: a uint8 tensor of at least
     layer_norm_bwd_workspace_bytes(...) bytes (allocated here when None)."""
-    rows, d = _row_args(x, y, gamma, None, (("dout", dout), ("dres", dres)))
-    if dout is None:
-        raise TypeError("dout must be a torch.Tensor")
+    rows, d = _row_args(x, y, gamma, None)
     dev, st = x.device, x.shape[:-1]
+    _need(dout, "dout", x.shape, x.dtype, dev)
+    if dres is not None:
+        _need(dres, "dres", x.shape, x.dtype, dev)
     _need(mean, "mean", st, torch.float32, dev)
     _need(rstd, "rstd", st, torch.float32, dev)
-    need = int(_invoke(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, _dtype_code(x)))
+    need = _workspace_need(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, _dtype_code(x))
     with _on(stream, dev):
         if grads is None:
             g = {"dx": torch.empty_like(x), "dgamma": torch.empty(d, dtype=torch.float32, device=dev),
@@ -166,7 +175,7 @@ def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, wo
     _need(x, "x", x.shape, bf)
     _need(w, "w", (N, K), bf, dev)
     _need(dy, "dy", (B, T, N), bf, dev)
-    need = int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want)))
+    need = _workspace_need(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want))
     f32 = torch.float32
     spec = {"dx": (x.shape, bf), "dw": ((N, K), f32), "db": ((N,), f32)}
     with _on(stream, dev):
