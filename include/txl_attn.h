@@ -388,7 +388,8 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
  * (TXL_ERR_ALIAS).  workspace as for txl_layer_norm_bwd, of
  * txl_linear_bwd_workspace_bytes(...) bytes (0: none needed, not touched).
  */
-size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw);
+size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
+                                      int want_db);
 int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, int K, const void* w, int N,
                    int relu_in, void* dx, float* dw, float* db, void* workspace, size_t ws_bytes, void* stream);
 

@@ -188,8 +188,8 @@ def test_workspace_is_checked():
     """A long reduction over few tiles is split over the GPU's SMs: its parts
     need a workspace, and a missing, small or overlapping one is refused."""
     lib, A, G = txl.load(), 1 << 40, 1 << 30  # addresses that are compared, never dereferenced
-    need = lib.txl_linear_bwd_workspace_bytes(0, 1, 100000, 128, 136, 1, 1)
-    assert need > 0 and lib.txl_linear_bwd_workspace_bytes(0, 1, 100000, 128, 136, 1, 0) == 0
+    need = lib.txl_linear_bwd_workspace_bytes(0, 1, 100000, 128, 136, 1, 1, 1)
+    assert need > 0 and lib.txl_linear_bwd_workspace_bytes(0, 1, 100000, 128, 136, 1, 0, 0) == 0
     call = lambda ws, n: lib.txl_linear_bwd(A, A + G, 0, 1, 100000, 128, A + 2 * G, 136, 0, A + 3 * G, A + 4 * G, A + 5 * G, ws, n, None)
     assert call(None, need) == -7 and call(A + 6 * G, need - 1) == -7 and call(A + 6 * G + 16, need) == -7
     assert call(A + 4 * G, need) == -4

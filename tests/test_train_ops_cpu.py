@@ -72,7 +72,7 @@ def test_linear_bwd_rejects_bad_arguments(lib):
     assert call(K=132) == -2 and call(N=100) == -2 and call(layout=1, K=72) == -2
     assert call(B=1 << 20, T=1 << 10) == -2 and call(K=1 << 21) == -2
     assert call(dx=addr(1)) == -4 and call(dw=addr(4), db=addr(4) + 64) == -4 and call(dw=addr(2)) == -4
-    assert lib.txl_linear_bwd_workspace_bytes(0, 2, 100, 132, 136, 1, 1) == 0
+    assert lib.txl_linear_bwd_workspace_bytes(0, 2, 100, 132, 136, 1, 1, 1) == 0
 
 
 def table(*entries):

@@ -108,7 +108,7 @@ def load() -> ctypes.CDLL:
         lib.txl_layer_norm_bwd_workspace_bytes.restype = sz
         lib.txl_layer_norm_bwd.argtypes = [vp] * 7 + [ll, i] + [vp] * 3 + [i, vp, sz, vp]
         lib.txl_layer_norm_bwd.restype = i
-        lib.txl_linear_bwd_workspace_bytes.argtypes = [i] * 7
+        lib.txl_linear_bwd_workspace_bytes.argtypes = [i] * 8
         lib.txl_linear_bwd_workspace_bytes.restype = sz
         lib.txl_linear_bwd.argtypes = [vp, vp] + [i] * 4 + [vp, i, i] + [vp] * 4 + [sz, vp]
         lib.txl_linear_bwd.restype = i

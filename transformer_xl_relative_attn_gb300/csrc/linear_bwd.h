@@ -11,6 +11,7 @@ namespace txl {
 cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, int T, int K, const void* w, int N,
                               int relu, void* dx, float* dw, float* db, void* workspace, int* status,
                               cudaStream_t stream);
-size_t linear_bwd_workspace_bytes(int heads, int B, int T, int K, int N, bool want_dx, bool want_dw);
+size_t linear_bwd_workspace_bytes(int heads, int B, int T, int K, int N, bool want_dx, bool want_dw,
+                                  bool want_db);
 
 }  // namespace txl

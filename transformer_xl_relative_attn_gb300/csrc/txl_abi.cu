@@ -733,9 +733,11 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
                                                   workspace, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
 }
 
-size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw) {
+size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
+                                      int want_db) {
     if (linear_bwd_sizes(x_layout, B, T, K, N) != TXL_OK) return 0;
-    return txl::linear_bwd_workspace_bytes(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0);
+    return txl::linear_bwd_workspace_bytes(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0,
+                                           want_db != 0);
 }
 
 int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, int K, const void* w, int N,
@@ -745,7 +747,8 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
     if (rc != TXL_OK) return rc;
     for (const void* p : {dy, x, w, (const void*)dx, (const void*)dw, (const void*)db})
         if (!aligned16(p)) return TXL_ERR_MISALIGNED;
-    const size_t need = txl_linear_bwd_workspace_bytes(x_layout, B, T, K, N, dx != nullptr, dw != nullptr);
+    const size_t need = txl_linear_bwd_workspace_bytes(x_layout, B, T, K, N, dx != nullptr, dw != nullptr,
+                                                       db != nullptr);
     if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
     const size_t rows = (size_t)B * T, nx = rows * K * 2, nw = (size_t)N * K;
     Range r[] = {range_of(dy, rows * N * 2, false),     range_of(x, nx, false),

@@ -154,7 +154,7 @@ def linear_bwd_workspace_bytes(x_shape, N, want=("dx", "dw", "db"), device=None)
     one; the split depends on its SM count)."""
     layout, B, T, K = _linear_shape(torch.empty(x_shape, device="meta"))
     dev = device if device is not None else torch.cuda.current_device()
-    return int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want)))
+    return int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, *("dx" in want, "dw" in want, "db" in want)))
 
 
 def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, workspace=None, grads=None):
@@ -175,7 +175,7 @@ def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, wo
     _need(x, "x", x.shape, bf)
     _need(w, "w", (N, K), bf, dev)
     _need(dy, "dy", (B, T, N), bf, dev)
-    need = _workspace_need(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, int("dx" in want), int("dw" in want))
+    need = _workspace_need(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, *("dx" in want, "dw" in want, "db" in want))
     f32 = torch.float32
     spec = {"dx": (x.shape, bf), "dw": ((N, K), f32), "db": ((N,), f32)}
     with _on(stream, dev):
