@@ -24,15 +24,18 @@
 // a dw accumulator takes 1024 rows at a time and the epilogue adds these in registers:
 // at 6144 rows the error went from 3.3e-6 to below that of an fp32 product.
 //
-// A TMA instruction costs its issuing thread some 100 cycles whatever it loads, and an
-// L2 miss far more: a stage of 48 KB is two instructions where the widths are
-// multiples of 64 (boxes of several 64-column slices), six otherwise.
+// TMA is what the loads need all of: an instruction costs its issuing thread some
+// 100 cycles whatever it loads, so a stage of 32 KB is two instructions where the widths
+// are multiples of 64 (boxes of two 64-column slices), up to four otherwise; and results
+// leave through plain stores of whole lines (a warp turns its rows in shared memory)
+// rather than TMA stores, which held the loads up (base512's second feed-forward layer
+// without its mask: 22.5 us with them).
 //
 // Roles (384 threads, one CTA per SM): warp 0 lane 0 issues the TMA loads, warp 1
 // the MMAs, warps 2-3 the column sums, warps 4-11 the epilogue; two accumulators
 // let an epilogue overlap the next tile's MMAs.  Every wait is bounded (1 s) and
 // reports through the device status word.  Rows, N and K need not fill tiles: TMA
-// fills with zeros behind the ends and clips its stores.
+// fills with zeros behind the ends.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,28 +47,33 @@
 namespace txl {
 
 namespace lb {
-constexpr int BM = 128;
+constexpr int BM = 128;  // rows of a CTA's accumulator
 constexpr int BR = 64;   // reduction per stage
 constexpr int CHAIN = 16;  // stages that one dw accumulator takes
 constexpr int NTHREADS = 384;
 constexpr uint32_t SZ_BOX = 64 * 64 * 2;  // 64 rows of 64 bf16: 8 KB
-constexpr uint32_t SZ_A = 2 * SZ_BOX;
-constexpr int MAX_STAGES = 6;
+constexpr uint32_t SZ_A = 2 * SZ_BOX;     // 128 of M
+constexpr uint32_t SZ_B = 2 * SZ_BOX;     // 128 of N: of a pair's 256, each CTA holds half
+constexpr int STAGES = 6;
+constexpr uint32_t SZ_SLOT = 4096;        // a staged slice: 32 rows of 128 bytes
+constexpr uint32_t OFF_A = 0;
+constexpr uint32_t OFF_B = STAGES * SZ_A;
+constexpr uint32_t OFF_STG = OFF_B + STAGES * SZ_B;  // a slot per epilogue warp
+constexpr uint32_t OFF_BAR = OFF_STG + 8 * SZ_SLOT;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget of one sm_103a CTA");
 
-template <int BN_>
+// Two CTAs of a cluster work one 256 x 256 tile (PAIR), or one CTA a 128 x 128 tile.
+// Either way a CTA loads 128 + 128 columns per stage; as a pair the tensor cores read
+// each other's half of the second operand, and do twice the work on the same loads.
+template <bool PAIR>
 struct Cfg {
-    static constexpr int BN = BN_;
-    static constexpr int STAGES = BN_ == 256 ? 4 : 6;
-    static constexpr uint32_t SZ_B = BN_ / 64 * SZ_BOX;
-    static constexpr uint32_t OFF_A = 0;
-    static constexpr uint32_t OFF_B = STAGES * SZ_A;
-    static constexpr uint32_t OFF_STG = OFF_B + STAGES * SZ_B;  // 4 KB per epilogue warp
-    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * 4096;
-    static constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
-    static constexpr uint32_t TMEM_COLS = 2 * BN_;
-    static constexpr uint32_t IDESC_DX = idesc_bf16_f32(BM, BN_, 1, 0);
-    static constexpr uint32_t IDESC_DW = idesc_bf16_f32(BM, BN_, 1, 1);
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget of one sm_103a CTA");
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TM = BM * CTAS;  // tile
+    static constexpr int BN = PAIR ? 256 : 128;
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static constexpr uint32_t IDESC_DX = idesc_bf16_f32(TM, BN, 1, 0);
+    static constexpr uint32_t IDESC_DW = idesc_bf16_f32(TM, BN, 1, 1);
 };
 }  // namespace lb
 
@@ -73,7 +81,6 @@ struct LbParams {
     int T, B;       // rows per batch row, batch rows (rows layout: all rows, 1)
     int K, N;
     int heads;      // x and dx are [B, K / 64, T, 64]
-    int relu;
     int n_kt, n_nt, n_tt;  // tiles along K, N and T (per batch row)
     int t_steps;           // 64-row steps per batch row
     int n_steps;           // 64-column steps of N
@@ -84,6 +91,8 @@ struct LbParams {
     int db_rows;           // parts of db (row ranges); 0: no db
     const __nv_bfloat16* x;
     const __nv_bfloat16* dy;
+    __nv_bfloat16* dx;
+    float* dw;             // [splits, N, K]
     float* db;             // [db_rows, N]
     int* status;
 };
@@ -92,23 +101,21 @@ struct LbMaps {
     CUtensorMap dy;   // (column, row, batch row), boxes of 64 x 128: dx's first operand
     CUtensorMap dyc;  // dw's: (element, row, 64-column slice, batch row), boxes of two slices of 64 rows;
                       // N not a multiple of 64: one slice of N, boxes of 64 x 64
-    CUtensorMap w;    // (element, row, slice), boxes of BN / 64 slices of 64 rows; K not a multiple of 64: one slice
+    CUtensorMap w;    // (element, row, slice), boxes of two slices of 64 rows; K not a multiple of 64: one slice
     CUtensorMap x;    // the same, with the batch row
-    CUtensorMap dx;   // (element, row, slice, batch row), boxes of 32 rows; rows layout: one slice of K
-    CUtensorMap dw;  // (column, row, split), boxes of 32 x 32
 };
 
 struct LbShared {
-    uint64_t full[lb::MAX_STAGES];
-    uint64_t empty[lb::MAX_STAGES];
+    uint64_t full[lb::STAGES];  // a pair's: those of its first CTA
+    uint64_t empty[lb::STAGES];
     uint64_t acc_full[2];
-    uint64_t acc_empty[2];
+    uint64_t acc_empty[2];  // a pair's: those of its first CTA
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
 
-// The items of one CTA, the same sequence for every role.  dw items are dealt in
+// The items of one CTA (or pair), the same sequence for every role.  dw items are dealt in
 // turn first (the long ones).  Where they do not divide evenly, the CTAs from
 // `heavy` on have one less: they take `extra` dx tiles each ahead of the rest, which
 // is then dealt in turn from the last CTA down.
@@ -116,9 +123,9 @@ struct LbSchedule {
     const LbParams& p;
     int c, g, light, head;  // CTA, CTAs, CTAs with one dw item less, dx tiles dealt to them ahead
     int w, e, d;            // next dw item, next extra tile, next dx tile
-    __device__ __forceinline__ explicit LbSchedule(const LbParams& p_) : p(p_) {
-        c = blockIdx.x;
-        g = gridDim.x;
+    __device__ __forceinline__ LbSchedule(const LbParams& p_, int ctas) : p(p_) {
+        c = blockIdx.x / ctas;
+        g = gridDim.x / ctas;
         light = p.heavy ? g - p.heavy : 0;
         head = min(p.n_d, light * p.extra);
         w = c;
@@ -154,20 +161,21 @@ struct LbItem {
     int m0, k0, s0, s1, b, split;
 };
 
-template <int BN>
+template <bool PAIR>
 __device__ __forceinline__ LbItem lb_item(const LbParams& p, bool dw, int i) {
+    using C = lb::Cfg<PAIR>;
     LbItem it;
-    it.k0 = (i % p.n_kt) * BN;
+    it.k0 = (i % p.n_kt) * C::BN;
     int rest = i / p.n_kt;
     if (dw) {
-        it.m0 = (rest % p.n_nt) * lb::BM;
+        it.m0 = (rest % p.n_nt) * C::TM;
         it.split = rest / p.n_nt;
         it.b = 0;
         const long long total = (long long)p.B * p.t_steps;
         it.s0 = (int)(total * it.split / p.splits);
         it.s1 = (int)(total * (it.split + 1) / p.splits);
     } else {
-        it.m0 = (rest % p.n_tt) * lb::BM;
+        it.m0 = (rest % p.n_tt) * C::TM;
         it.b = rest / p.n_tt;
         it.split = 0;
         it.s0 = 0;
@@ -178,28 +186,108 @@ __device__ __forceinline__ LbItem lb_item(const LbParams& p, bool dw, int i) {
 
 namespace {
 
-__device__ __forceinline__ void lb_load_4d(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                           int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
+// TMA loads into this CTA's shared memory that signal `bar`, of a pair its first
+// CTA's (a shared::cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void lb_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
 }
-__device__ __forceinline__ void lb_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\t"
-        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-        "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void lb_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                           int c3) {
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
 }
-__device__ __forceinline__ void lb_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
-        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-        "r"(src), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
+// shared::cluster address of a shared variable in the pair's CTA `rank`
+__device__ __forceinline__ uint32_t lb_mapa(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
 }
+__device__ __forceinline__ uint32_t lb_cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the CTA, or of both of the pair.
+template <bool PAIR>
+__device__ __forceinline__ void lb_sync() {
+    if (PAIR) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+}
+// Arrives on a barrier of the pair's first CTA.
+__device__ __forceinline__ void lb_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void lb_tmem_alloc(uint32_t* dst, uint32_t cols) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void lb_tmem_dealloc(uint32_t taddr, uint32_t cols) {
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+    else
+        tmem_dealloc(taddr, cols);
+}
+template <bool PAIR>
+__device__ __forceinline__ void lb_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader));
+    else
+        mma_ss_elect(d, a, b, idesc, accumulate, leader);
+}
+// Arrives on `bar` when the MMAs so far are done, in both CTAs of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void lb_commit(uint64_t* bar) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        mma_commit(bar);
+}
+
 // tmem_ld32 for 16 columns (the running sums leave no registers for 32).
 __device__ __forceinline__ void lb_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -209,29 +297,40 @@ __device__ __forceinline__ void lb_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) 
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void lb_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void lb_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Waits for something that is on its way whatever else went wrong (a load that was
+// issued, a commit): with the time limit, but not cut short by another role's abort.
+__device__ __forceinline__ bool lb_wait_landed(uint64_t* bar, uint32_t parity, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            record_status(status, kDevTimeoutDrain);
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ uint4 lb_ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
 }  // namespace
 
-template <int BN_>
+template <bool PAIR, bool RELU>
 __global__ void __launch_bounds__(lb::NTHREADS, 1)
 linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
     using namespace lb;
-    using C = Cfg<BN_>;
-    constexpr int BN = C::BN, STAGES = C::STAGES;
-    constexpr uint32_t SZ_B = C::SZ_B;
+    using C = Cfg<PAIR>;
+    constexpr int BN = C::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    LbShared* sh = reinterpret_cast<LbShared*>(smem + C::OFF_BAR);
+    LbShared* sh = reinterpret_cast<LbShared*>(smem + OFF_BAR);
     const uint32_t s_base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? lb_cta_rank() : 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 1) {
-        tmem_alloc(&sh->tmem_base, C::TMEM_COLS);
-        tmem_relinquish();
-    }
+    if (warp == 1) lb_tmem_alloc<PAIR>(&sh->tmem_base, C::TMEM_COLS);
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sh->full[s], 1);
@@ -239,7 +338,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 8);
+            mbar_init(&sh->acc_empty[a], 8 * C::CTAS);  // one arrival per epilogue warp
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -250,131 +349,126 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
         tma_prefetch_desc(&maps.x);
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) __syncthreads();
+    lb_sync<PAIR>();
     tc_fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = sh->tmem_base;
     volatile int* abort = &sh->abort;
-    LbSchedule sched(p);
+    LbSchedule sched(p, C::CTAS);
     bool dw;
     int item;
-
+    // Registers: the launch's 384 * 168 = 64512 as 128 * 80 + 256 * 208 (and 1024 to spare).  An epilogue thread
+    // keeps 128 running sums of dw, or 64 registers of the next mask, besides what it unpacks.
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
+        // A pair's full barriers are its first CTA's, which expects both CTAs' bytes; the
+        // second's loads may land before it does (the barrier waits for the arrival).
+        // One thread's instructions per stage bound the loads (at 870 cycles a stage took
+        // longer than its MMAs), so what does not change is kept out of the loops.
         if (lane == 0) {
             bool ok = true;
-            int c = 0;
+            uint32_t s = 0, phase = 1;  // slot, parity of its empty barrier (a fresh one passes for 1)
+            long long loads = 0;
+            const uint32_t full0 = PAIR ? lb_mapa(&sh->full[0], 0) : smem_u32(&sh->full[0]);
+            auto next_slot = [&](uint32_t& a, uint32_t& b, uint32_t& bar) {
+                if (!mbar_wait(&sh->empty[s], phase, kDevTimeoutProducer, abort, p.status)) return ok = false;
+                if (rank == 0) mbar_expect_tx(&sh->full[s], (SZ_A + SZ_B) * C::CTAS);
+                a = s_base + OFF_A + s * SZ_A;
+                b = s_base + OFF_B + s * SZ_B;
+                bar = full0 + 8 * s;
+                if (++s == STAGES) s = 0, phase ^= 1;
+                ++loads;
+                return true;
+            };
+            const bool n64 = p.n64, k64 = p.k64;
             while (ok && sched.next(dw, item)) {
-                const LbItem it = lb_item<BN>(p, dw, item);
-                int b = dw ? it.s0 / p.t_steps : it.b;
-                int r = (dw ? it.s0 - b * p.t_steps : it.s0) * BR;  // row of dy and x, or column of dy and row of w
-                for (int st = it.s0; st < it.s1; ++st, ++c) {
-                    const int s = c % STAGES;
-                    if (c >= STAGES &&
-                        !mbar_wait(&sh->empty[s], ((c / STAGES) & 1) ^ 1, kDevTimeoutProducer, abort, p.status)) {
-                        ok = false;
-                        break;
+                const LbItem it = lb_item<PAIR>(p, dw, item);
+                const int m = it.m0 + BM * rank, k = it.k0 + 128 * rank;  // this CTA's share
+                uint32_t a, b, bar;
+                if (dw) {
+                    const int m_el = n64 ? 0 : m, m_sl = n64 ? m >> 6 : 0, k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
+                    int bt = it.s0 / p.t_steps, t = (it.s0 - bt * p.t_steps) * BR;
+                    const int T = p.T;
+                    for (int n = it.s1 - it.s0; n > 0 && next_slot(a, b, bar); --n) {
+                        lb_load_4d<PAIR>(a, &maps.dyc, bar, m_el, t, m_sl, bt);
+                        lb_load_4d<PAIR>(b, &maps.x, bar, k_el, t, k_sl, bt);
+                        if (!n64) lb_load_4d<PAIR>(a + SZ_BOX, &maps.dyc, bar, m_el + 64, t, 0, bt);
+                        if (!k64) lb_load_4d<PAIR>(b + SZ_BOX, &maps.x, bar, k_el + 64, t, 0, bt);
+                        t += BR;
+                        if (t >= T) t = 0, ++bt;
                     }
-                    uint64_t* bar = &sh->full[s];
-                    mbar_expect_tx(bar, SZ_A + SZ_B);
-                    uint8_t* a = smem + C::OFF_A + s * SZ_A;
-                    uint8_t* bt = smem + C::OFF_B + s * SZ_B;
-                    if (dw) {
-                        if (p.n64) {
-                            lb_load_4d(a, &maps.dyc, bar, 0, r, it.m0 >> 6, b);
-                        } else {
-                            lb_load_4d(a, &maps.dyc, bar, it.m0, r, 0, b);
-                            lb_load_4d(a + SZ_BOX, &maps.dyc, bar, it.m0 + 64, r, 0, b);
-                        }
-                        if (p.k64) {
-                            lb_load_4d(bt, &maps.x, bar, 0, r, it.k0 >> 6, b);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < BN / 64; ++j)
-                                lb_load_4d(bt + j * SZ_BOX, &maps.x, bar, it.k0 + 64 * j, r, 0, b);
-                        }
-                        r += BR;
-                        if (r >= p.T) r = 0, ++b;
-                    } else {
-                        tma_load_3d(a, &maps.dy, bar, r, it.m0, b);
-                        if (p.k64) {
-                            tma_load_3d(bt, &maps.w, bar, 0, r, it.k0 >> 6);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(bt + j * SZ_BOX, &maps.w, bar, it.k0 + 64 * j, r, 0);
-                        }
+                } else {
+                    const int k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
+                    int r = 0;  // column of dy, row of w
+                    for (int n = it.s1; n > 0 && next_slot(a, b, bar); --n) {
+                        lb_load_3d<PAIR>(a, &maps.dy, bar, r, m, it.b);
+                        lb_load_3d<PAIR>(b, &maps.w, bar, k_el, r, k_sl);
+                        if (!k64) lb_load_3d<PAIR>(b + SZ_BOX, &maps.w, bar, k_el + 64, r, 0);
                         r += BR;
                     }
                 }
             }
-            // the last load into each slot has landed before the CTA exits
-            for (int i = c - STAGES; i < c; ++i)
-                if (i >= 0) {
-                    const uint64_t t0n = globaltimer_ns();
-                    while (!mbar_try_wait(&sh->full[i % STAGES], (i / STAGES) & 1))
-                        if (globaltimer_ns() - t0n > kWaitLimitNs) {
-                            record_status(p.status, kDevTimeoutDrain);
-                            break;
-                        }
-                }
+            // the last load into each slot has landed before the CTAs exit
+            for (int i = 0; i < STAGES && rank == 0; ++i) {
+                const long long c = loads - 1 - i;
+                if (c >= 0) lb_wait_landed(&sh->full[c % STAGES], (c / STAGES) & 1, p.status);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
-        const uint32_t leader = elect_one();
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kDevTimeoutMma, abort, p.status));
-            return ok;
-        };
-        const uint64_t dA0 = smem_desc_sw128(s_base + C::OFF_A, 16, 1024);          // K-major: rows of dy
-        const uint64_t dAm = smem_desc_sw128(s_base + C::OFF_A, SZ_BOX, 1024);      // MN-major: columns of dy
-        const uint64_t dB0 = smem_desc_sw128(s_base + C::OFF_B, SZ_BOX, 1024);      // MN-major
-        int c = 0, j = 0;  // stages consumed, accumulators filled
-        while (ok && sched.next(dw, item)) {
-            const LbItem it = lb_item<BN>(p, dw, item);
-            int st = it.s0;
-            do {
-                const int first = st, last = dw ? min(it.s1, st + CHAIN) : it.s1;
-                const int acc = j & 1;
-                if (j >= 2 && !wait(&sh->acc_empty[acc], ((j >> 1) - 1) & 1)) break;
-                tc_fence_after();
-                const uint32_t d_acc = tmem + acc * BN;
-                for (; st < last; ++st, ++c) {
-                    const int s = c % STAGES;
-                    if (!wait(&sh->full[s], (c / STAGES) & 1)) break;
+        if (rank == 0) {
+            const uint32_t leader = elect_one();
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kDevTimeoutMma, abort, p.status));
+                return ok;
+            };
+            const uint64_t dA0 = smem_desc_sw128(s_base + OFF_A, 16, 1024);      // K-major: rows of dy
+            const uint64_t dAm = smem_desc_sw128(s_base + OFF_A, SZ_BOX, 1024);  // MN-major: columns of dy
+            const uint64_t dB0 = smem_desc_sw128(s_base + OFF_B, SZ_BOX, 1024);  // MN-major
+            uint32_t s = 0, phase = 0;  // slot, parity of its full barrier
+            int j = 0;                  // accumulators filled
+            while (ok && sched.next(dw, item)) {
+                const LbItem it = lb_item<PAIR>(p, dw, item);
+                // dx's first operand steps along its rows (32 bytes per MMA), dw's and every
+                // second one by 16 rows of 128 bytes
+                const uint64_t dA = dw ? dAm : dA0;
+                const uint64_t a_step = dw ? 128 : 2;
+                const uint32_t idesc = dw ? C::IDESC_DW : C::IDESC_DX;
+                int left = it.s1 - it.s0;
+                do {
+                    const int acc = j & 1, n = dw ? min(left, CHAIN) : left;
+                    if (j >= 2 && !wait(&sh->acc_empty[acc], ((j >> 1) - 1) & 1)) break;
                     tc_fence_after();
-                    const uint64_t bd = dB0 + s * (SZ_B >> 4);
-                    if (dw) {
-                        const uint64_t a = dAm + s * (SZ_A >> 4);
+                    const uint32_t d_acc = tmem + acc * BN;
+                    uint32_t more_than_first = 0;
+                    for (int i = 0; i < n; ++i) {
+                        if (!wait(&sh->full[s], phase)) break;
+                        tc_fence_after();
+                        const uint64_t ad = dA + s * (SZ_A >> 4), bd = dB0 + s * (SZ_B >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < BR / 16; ++kk)
-                            mma_ss_elect(d_acc, a + 128 * kk, bd + 128 * kk, C::IDESC_DW,
-                                         (st > first || kk > 0) ? 1u : 0u, leader);
-                    } else {
-                        const uint64_t a = dA0 + s * (SZ_A >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < BR / 16; ++kk)
-                            mma_ss_elect(d_acc, a + 2 * kk, bd + 128 * kk, C::IDESC_DX,
-                                         (st > first || kk > 0) ? 1u : 0u, leader);
+                        for (int kk = 0; kk < BR / 16; ++kk) {
+                            lb_mma<PAIR>(d_acc, ad + a_step * kk, bd + 128 * kk, idesc, more_than_first, leader);
+                            more_than_first = 1;
+                        }
+                        if (leader) lb_commit<PAIR>(&sh->empty[s]);
+                        if (++s == STAGES) s = 0, phase ^= 1;
                     }
-                    if (leader) mma_commit(&sh->empty[s]);
-                }
-                if (!ok) break;
-                if (leader) mma_commit(&sh->acc_full[acc]);
-                ++j;
-            } while (st < it.s1);
-        }
-        if (leader) mma_commit(&sh->drain);
-        const uint64_t t0n = globaltimer_ns();
-        while (!mbar_try_wait(&sh->drain, 0))
-            if (globaltimer_ns() - t0n > kWaitLimitNs) {
-                record_status(p.status, kDevTimeoutDrain);
-                break;
+                    if (!ok) break;
+                    if (leader) lb_commit<PAIR>(&sh->acc_full[acc]);
+                    ++j;
+                    left -= n;
+                } while (left > 0);
             }
+            if (leader) lb_commit<PAIR>(&sh->drain);
+            lb_wait_landed(&sh->drain, 0, p.status);
+        }
         __syncwarp();
-    } else if (warp < 4) {
+    } else {
         // ---------------------------------------------------- column sums of dy
         // A warp adds 256 columns (8 per lane) over one of db_rows ranges of rows.
         if (p.db_rows) {
@@ -402,14 +496,17 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                 to[1] = make_float4(a[4], a[5], a[6], a[7]);
             }
         }
+    }
     } else {
         // ---------------------------------------------------- epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int wq = warp & 3;
         const int chalf = (warp - 4) >> 2;
         constexpr int CPW = BN / 64;  // 32-column chunks per warp
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t stg = s_base + C::OFF_STG + (uint32_t)(warp - 4) * 4096;
-        bool store_pending = false, ok = true;
+        const uint32_t stg = s_base + OFF_STG + (uint32_t)(warp - 4) * SZ_SLOT;
+        const uint32_t acc_empty0 = PAIR ? lb_mapa(&sh->acc_empty[0], 0) : 0;
+        bool ok = true;
         int j = 0;
         auto wait_acc = [&](int acc) {
             ok = __all_sync(0xffffffffu, mbar_wait(&sh->acc_full[acc], (j >> 1) & 1, kDevTimeoutSoftmax, abort, p.status));
@@ -419,21 +516,24 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
         auto free_acc = [&](int acc) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+            if (lane == 0) {
+                if (PAIR)
+                    lb_arrive_remote(acc_empty0 + 8 * acc);
+                else
+                    mbar_arrive(&sh->acc_empty[acc]);
+            }
         };
-        // the staged slice may be overwritten: its last store has read it
-        auto stage_free = [&] {
-            if (store_pending) lb_wait_read();
-            store_pending = false;
-            __syncwarp();
-        };
-        // A staged slice is 32 rows of 128 bytes (64 bf16 or 32 fp32 columns), its
-        // 16-byte chunk c at c ^ (row & 7): the swizzle of the store's map.
-        auto chunk_at = [&](int c16) { return stg + lane * 128 + ((c16 ^ (lane & 7)) << 4); };
-        while (ok && sched.next(dw, item)) {
-            const LbItem it = lb_item<BN>(p, dw, item);
-            const int m = it.m0 + 32 * wq;  // first row of this warp's 32
-            if (dw) {
+        // A slice of results, 32 rows of 128 bytes (64 bf16 or 32 fp32 columns), is written
+        // a row per thread and read back as whole lines, 8 threads on a row: 16-byte chunk c
+        // of a row lies at c ^ (row & 7), so that neither way two threads share a bank.
+        auto chunk_at = [&](int row, int c16) { return stg + row * 128 + ((c16 ^ (row & 7)) << 4); };
+        const int lrow = lane >> 3, lc = lane & 7;  // row (of 4 at a time) and chunk of this thread's line accesses
+        const uint32_t t_row = tmem + lane_off + 32 * CPW * chalf;
+        bool more = sched.next(dw, item);
+        for (; ok && more && dw; more = sched.next(dw, item)) {
+                const LbItem it = lb_item<PAIR>(p, true, item);
+                const int m = it.m0 + BM * rank + 32 * wq;  // first row of this warp's 32
+                const int k = it.k0 + 32 * CPW * chalf;     // its first column
                 float sum[CPW][32];
 #pragma unroll
                 for (int cc = 0; cc < CPW; ++cc)
@@ -446,7 +546,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
 #pragma unroll
                     for (int h = 0; h < 2 * CPW; ++h) {
                         uint32_t v[16];
-                        lb_tmem_ld16(tmem + lane_off + acc * BN + 32 * CPW * chalf + 16 * h, v);
+                        lb_tmem_ld16(t_row + acc * BN + 16 * h, v);
                         tmem_wait_ld();
                         if (h == 2 * CPW - 1) free_acc(acc);
 #pragma unroll
@@ -454,107 +554,137 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     }
                 }
                 if (!ok) break;
+                float* const out = p.dw + (size_t)it.split * p.N * p.K;
 #pragma unroll
                 for (int cc = 0; cc < CPW; ++cc) {
-                    const int k = it.k0 + 32 * (CPW * chalf + cc);
-                    stage_free();
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        st_shared_v4(chunk_at(q), __float_as_uint(sum[cc][4 * q]), __float_as_uint(sum[cc][4 * q + 1]),
-                                     __float_as_uint(sum[cc][4 * q + 2]), __float_as_uint(sum[cc][4 * q + 3]));
-                    fence_proxy_async_smem();
+                        st_shared_v4(chunk_at(lane, q), __float_as_uint(sum[cc][4 * q]),
+                                     __float_as_uint(sum[cc][4 * q + 1]), __float_as_uint(sum[cc][4 * q + 2]),
+                                     __float_as_uint(sum[cc][4 * q + 3]));
                     __syncwarp();
-                    if (lane == 0 && k < p.K && m < p.N) {
-                        lb_store_3d(&maps.dw, stg, k, m, it.split);
-                        store_pending = true;
+                    const int c = k + 32 * cc + 4 * lc;  // K is a multiple of 8
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + lrow;
+                        const uint4 v = lb_ld_shared_v4(chunk_at(row, lc));
+                        const size_t at = (size_t)(m + row) * p.K + c;
+                        if (m + row < p.N && c < p.K && TXL_BOUNDS(at + 4 <= (size_t)p.N * p.K && it.split < p.splits, 803, at))
+                            *reinterpret_cast<uint4*>(out + at) = v;
                     }
+                    __syncwarp();
                 }
-                continue;
-            }
-            // The ReLU mask of the warp's 32 rows, fetched while the MMAs run: x comes in as
-            // whole lines (a lane per 8 columns), a byte per lane goes through the staging
-            // area, and each thread takes its row's: bit x of keep[cc] for column x of chunk
-            // cc.  (With each thread reading its own row of x, one line per lane and load,
-            // the epilogue took longer than the tile: 44 us instead of 22 without the mask.)
-            uint32_t keep[CPW];
-            if (p.relu) {
-                constexpr int G = 4 * CPW, ROWS = 32 / G;  // 8-column groups of a row; rows per load
-                stage_free();
-                const int g = lane % G, kq = it.k0 + 32 * CPW * chalf + 8 * g;  // K is a multiple of 8
-                constexpr int BATCH = 8;  // loads in flight per thread
-#pragma unroll 1
-                for (int i0 = 0; i0 < 32 / ROWS; i0 += BATCH) {
-                    uint4 w4[BATCH];
+        }
+        // dx: this thread's lines of a tile, in x and dx: rows row, row + 4, .. + 28 and 8
+        // columns from c on of each 64-column slice
+        constexpr int SL = CPW / 2;  // slices
+        struct Lines {
+            long long at;  // of the first line
+            int rows, cols;  // rows of T and columns of K from there on
+        };
+        const int row_stride = p.heads ? 64 : p.K;
+        const long long slice_stride = p.heads ? 64ll * p.T : 64;
+        auto lines_of = [&](int i) {
+            const LbItem it = lb_item<PAIR>(p, false, i);
+            const int row = it.m0 + BM * rank + 32 * wq + lrow, c = it.k0 + 32 * CPW * chalf + 8 * lc;
+            const long long col = p.heads ? (((long long)it.b * (p.K >> 6) + (c >> 6)) * p.T) * 64 + (c & 63)
+                                          : (long long)it.b * p.T * p.K + c;
+            return Lines{col + (long long)row * row_stride, p.T - row, p.K - c};
+        };
+        auto line_in = [&](const Lines& l, int sl, int i) {  // K is a multiple of 8
+            return 4 * i < l.rows && 64 * sl < l.cols &&
+                   TXL_BOUNDS(l.at + sl * slice_stride + (long long)(4 * i) * row_stride + 8 <= (long long)p.B * p.T * p.K, 802,
+                              l.at);
+        };
+        // The ReLU mask of the lines, 8 bits each, from x: fetched a tile ahead, while that
+        // tile's results leave (fetched at the tile's start it took longer than the MMAs).
+        auto fetch = [&](uint4 (&x4)[8], const Lines& l, int sl) {
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = ROWS * (i0 + i) + lane / G;
-                        const size_t at = p.heads
-                                              ? (((size_t)it.b * (p.K >> 6) + (kq >> 6)) * p.T + m + row) * 64 + (kq & 63)
-                                              : ((size_t)it.b * p.T + m + row) * p.K + kq;
-                        w4[i] = make_uint4(0, 0, 0, 0);
-                        if (m + row < p.T && kq < p.K && TXL_BOUNDS(at + 8 <= (size_t)p.B * p.T * p.K, 802, at))
-                            w4[i] = __ldg(reinterpret_cast<const uint4*>(p.x + at));
-                    }
+            for (int i = 0; i < 8; ++i)
+                x4[i] = line_in(l, sl, i) ? __ldg(reinterpret_cast<const uint4*>(
+                                                p.x + l.at + sl * slice_stride + (long long)(4 * i) * row_stride))
+                                          : make_uint4(0, 0, 0, 0);
+        };
+        auto mask_of = [&](uint4 (&x4)[8], uint32_t (&keep)[2]) {
+            keep[0] = keep[1] = 0;
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&w4[i]);
-                        uint32_t bits = 0;
+            for (int i = 0; i < 8; ++i) {
+                // (not moved ahead of what was issued since the fetch)
+                asm volatile("" : "+r"(x4[i].x), "+r"(x4[i].y), "+r"(x4[i].z), "+r"(x4[i].w));
+                const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = __bfloat1622float2(h2[e]);
-                            bits |= (f.x > 0.f ? 1u : 0u) << (2 * e);
-                            bits |= (f.y > 0.f ? 1u : 0u) << (2 * e + 1);
-                        }
-                        const int row = ROWS * (i0 + i) + lane / G;
-                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(stg + row * G + g), "r"(bits) : "memory");
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t on = __hgt2_mask(h2[e], __floats2bfloat162_rn(0.f, 0.f));
+                    keep[i >> 2] |= (on & 0x00010001u) << (4 * (i & 3) + e);  // low halves below bit 16
                 }
-                __syncwarp();
-#pragma unroll
-                for (int cc = 0; cc < CPW; ++cc)
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(keep[cc]) : "r"(stg + lane * G + 4 * cc) : "memory");
-                __syncwarp();
             }
+        };
+        Lines cur = {}, next = {};
+        uint32_t keep[SL][2];
+        if (ok && more) {
+            next = lines_of(item);
+            if (RELU) {
+#pragma unroll
+                for (int sl = 0; sl < SL; ++sl) {
+                    uint4 x4[8];
+                    fetch(x4, next, sl);
+                    mask_of(x4, keep[sl]);
+                }
+            }
+        }
+        while (ok && more) {
+            cur = next;
+            more = sched.next(dw, item);
+            if (more) next = lines_of(item);
             const int acc = j & 1;
             if (!wait_acc(acc)) break;
 #pragma unroll
-            for (int cc = 0; cc < CPW; ++cc) {
-                uint32_t v[32];
-                tmem_ld32(tmem + lane_off + acc * BN + 32 * (CPW * chalf + cc), v);
-                tmem_wait_ld();
-                if (cc == CPW - 1) free_acc(acc);
-                if (p.relu) {
+            for (int sl = 0; sl < SL; ++sl) {
+                uint4 x4[8];
+                if (RELU && more) fetch(x4, next, sl);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = (keep[cc] >> x) & 1u ? v[x] : 0u;
+                for (int hc = 0; hc < 2; ++hc) {
+                    uint32_t v[32];
+                    tmem_ld32(t_row + acc * BN + 64 * sl + 32 * hc, v);
+                    tmem_wait_ld();
+                    if (sl == SL - 1 && hc == 1) free_acc(acc);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st_shared_v4(chunk_at(lane, 4 * hc + q),
+                                     pack_bf16x2(__uint_as_float(v[8 * q + 0]), __uint_as_float(v[8 * q + 1])),
+                                     pack_bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
+                                     pack_bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
+                                     pack_bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7])));
                 }
-                if ((cc & 1) == 0) stage_free();
+                __syncwarp();
+                __nv_bfloat16* const to = p.dx + cur.at + sl * slice_stride;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st_shared_v4(chunk_at(4 * (cc & 1) + q),
-                                 pack_bf16x2(__uint_as_float(v[8 * q + 0]), __uint_as_float(v[8 * q + 1])),
-                                 pack_bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
-                                 pack_bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
-                                 pack_bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7])));
-                if (cc & 1) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    const int k = it.k0 + 32 * (CPW * chalf + cc - 1);  // the slice's first column
-                    if (lane == 0 && k < p.K && m < p.T) {
-                        lb_store_4d(&maps.dx, stg, p.heads ? 0 : k, m, p.heads ? k >> 6 : 0, it.b);
-                        store_pending = true;
+                for (int i = 0; i < 8; ++i) {
+                    uint4 v = lb_ld_shared_v4(chunk_at(4 * i + lrow, lc));
+                    if (RELU) {
+                        uint32_t* o = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] &= ((keep[sl][i >> 2] >> (4 * (i & 3) + e)) & 0x00010001u) * 0xFFFFu;
                     }
+                    if (line_in(cur, sl, i)) *reinterpret_cast<uint4*>(to + (long long)(4 * i) * row_stride) = v;
                 }
+                __syncwarp();
+                if (RELU && more) mask_of(x4, keep[sl]);
             }
             ++j;
         }
-        if (lane == 0) lb_wait_all();
     }
 
     tc_fence_before();
     __syncthreads();
+    // the second CTA's barriers have had the last of the first one's commits
+    if (PAIR && rank == 1 && warp == 1) lb_wait_landed(&sh->drain, 0, p.status);
+    __syncwarp();
+    lb_sync<PAIR>();  // no CTA of a pair exits while the other may signal it or read its operands
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
+        lb_tmem_dealloc<PAIR>(tmem, C::TMEM_COLS);
     }
 }
 
@@ -628,21 +758,26 @@ bool lb_encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// How the call is cut: tile width, splits of dw's reduction, schedule.
+// How the call is cut: pairs or single CTAs, splits of dw's reduction, schedule.
 struct LbPlan {
-    int bn, grid;
+    bool pair;
+    int grid;
     LbParams p;
 };
 
-// Microseconds that a stage takes by tile width, and that the parts of one more split
-// cost per byte of dw (write and read, through L2); measured on base512's and large384's
-// layers.
-constexpr double kStep256 = 0.40, kStep128 = 0.25, kSplitPerByte = 0.4e-6, kSumLaunch = 2.0;
+// Microseconds that a stage takes a pair or a CTA, that a dx tile's and a dw item's end
+// add to the last of a unit, that the parts of one more split cost per byte of dw (write
+// and read, through L2), and that the second launch costs; measured on base512's and
+// large384's layers.
+constexpr double kStepPair = 0.36, kStepOne = 0.27, kTail = 3.0, kSplitPerByte = 0.4e-6, kSumLaunch = 2.0;
+
+#ifndef LB_FORCE
+#define LB_FORCE(pair, s) true
+#endif
 
 LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw) {
-    LbPlan pl;
+    LbPlan pl = {};
     LbParams& p = pl.p;
-    p = {};
     p.T = heads ? T : B * T;
     p.B = heads ? B : 1;
     p.K = K;
@@ -650,43 +785,45 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
     p.heads = heads;
     p.k64 = K % 64 == 0;
     p.n64 = N % 64 == 0;
-    p.n_nt = ceil_div(N, lb::BM);
-    p.n_tt = ceil_div(p.T, lb::BM);
     p.t_steps = ceil_div(p.T, lb::BR);
     p.n_steps = ceil_div(N, lb::BR);
     const int sms = current_sm_count();
     const long long total = (long long)p.B * p.t_steps;
-    // The tile width and the splits with the least time by this model: the CTA with
-    // most to do has all its dw items, or an even share of all stages and half a dx
-    // tile; splits add their parts' traffic and the second launch.
-    double best = 0;
-    pl.bn = 0;
-    for (int bn : {256, 128}) {
-        const double step = bn == 256 ? kStep256 : kStep128;
-        const long long kt = ceil_div(K, bn), n_d = want_dx ? (long long)p.B * p.n_tt * kt : 0, wt = p.n_nt * kt;
+    // Tiles, splits and schedule with the least time by this model: the stages of the
+    // unit (pair or CTA) with most to do, and the parts' traffic.
+    double best = -1;
+    for (int ctas : {2, 1}) {
+        const int most_units = sms / ctas, tile = lb::BM * ctas;
+        if (most_units < 1) continue;
+        const int kt = ceil_div(K, tile), nt = ceil_div(N, tile), tt = ceil_div(p.T, tile);
+        const long long n_d = want_dx ? (long long)p.B * tt * kt : 0;
         for (int s = 1; s <= (want_dw ? 32 : 1) && s <= total; ++s) {
-            const double even = ((want_dw ? wt * (double)total : 0.0) + (double)n_d * p.n_steps) / sms;
-            double steps = even + (n_d ? p.n_steps * 0.5 : 0.0);
-            if (n_d && steps < p.n_steps) steps = p.n_steps;
-            if (want_dw) {
-                const double most = (double)((wt * s + sms - 1) / sms) * ceil_div(total, s);
-                if (steps < most) steps = most;
-            }
-            const double cost = steps * step + (s > 1 ? kSumLaunch + s * (N * 4.0 * K) * kSplitPerByte : 0.0);
-            if (!pl.bn || cost < best) {
-                best = cost;
-                pl.bn = bn;
-                p.splits = s;
-            }
+            if (!LB_FORCE(ctas == 2, s)) continue;
+            const long long n_w = want_dw ? (long long)nt * kt * s : 0;
+            const int units = (int)(n_w + n_d < most_units ? n_w + n_d : most_units);
+            const int heavy = (int)(n_w % units), light = heavy ? units - heavy : 0;
+            const double len = (double)total / s;  // stages of a dw item
+            const int extra = light ? (int)(len / p.n_steps) : 0;
+            const long long head = n_d < (long long)light * extra ? n_d : (long long)light * extra, rest = n_d - head;
+            const double all = (double)(n_w / units) * len, turn = (double)((rest + units - 1) / units) * p.n_steps;
+            const double hi = all + (heavy ? len : 0.0) + (rest % units > light || !light ? turn : (double)(rest / units) * p.n_steps);
+            const double lo = all + (light ? (double)((head + light - 1) / light) * p.n_steps : 0.0) + turn;
+            const double cost = (hi > lo ? hi : lo) * (ctas == 2 ? kStepPair : kStepOne) + kTail +
+                                (s > 1 ? kSumLaunch + s * (N * 4.0 * K) * kSplitPerByte : 0.0);
+            if (best >= 0 && cost >= best) continue;
+            best = cost;
+            pl.pair = ctas == 2;
+            pl.grid = units * ctas;
+            p.splits = s;
+            p.n_kt = kt;
+            p.n_nt = nt;
+            p.n_tt = tt;
+            p.n_w = (int)n_w;
+            p.n_d = (int)n_d;
+            p.heavy = heavy;
+            p.extra = extra;
         }
     }
-    p.n_kt = ceil_div(K, pl.bn);
-    p.n_d = want_dx ? (int)((long long)p.B * p.n_tt * p.n_kt) : 0;
-    p.n_w = want_dw ? p.n_nt * p.n_kt * p.splits : 0;
-    const long long items = (long long)p.n_w + p.n_d;
-    pl.grid = (int)(items < sms ? items : sms);
-    p.heavy = p.n_w % pl.grid;
-    p.extra = p.heavy ? (int)(total / p.splits / p.n_steps) : 0;
     // row ranges of db: as many as give each of the two summing warps per CTA one, of 16
     // rows at least
     const long long rows = (long long)B * T, groups = (N + 255) / 256;
@@ -696,25 +833,28 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
     return pl;
 }
 
-template <int BN>
+template <bool PAIR, bool RELU>
 cudaError_t lb_launch(const LbMaps& maps, const LbPlan& pl, cudaStream_t stream) {
-    using C = lb::Cfg<BN>;
     static PerDeviceOnce attrs;
     const cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(linear_bwd_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        return cudaFuncSetAttribute(linear_bwd_kernel<PAIR, RELU>, cudaFuncAttributeMaxDynamicSharedMemorySize, lb::SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.grid);
     cfg.blockDim = dim3(lb::NTHREADS);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.dynamicSmemBytes = lb::SMEM_BYTES;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_bwd_kernel<BN>, maps, pl.p);
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_bwd_kernel<PAIR, RELU>, maps, pl.p);
 }
 
 size_t part_bytes(const LbPlan& pl) {
@@ -750,17 +890,17 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, i
                               cudaStream_t stream) {
     LbPlan pl = lb_plan(B, T, K, N, heads, dx != nullptr, dw != nullptr);
     LbParams& p = pl.p;
-    p.relu = relu;
     p.x = static_cast<const __nv_bfloat16*>(x);
     p.dy = static_cast<const __nv_bfloat16*>(dy);
+    p.dx = static_cast<__nv_bfloat16*>(dx);
     p.status = status;
     if (!db) p.db_rows = 0;
     const bool split = p.splits > 1;
     float* part = split ? static_cast<float*>(workspace) : dw;
+    p.dw = part;
     p.db = db ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(pl)) : nullptr;
     LbMaps maps;
     const cuuint64_t Tt = p.T, Bb = p.B, Kk = K, Nn = N;
-    const cuuint32_t slices = pl.bn / 64;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     {
         const cuuint64_t dims[3] = {Nn, Tt, Bb}, strides[2] = {Nn * 2, Tt * Nn * 2};
@@ -777,7 +917,7 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, i
     {
         const cuuint64_t cut[3] = {64, Nn, Kk / 64}, cut_str[2] = {Kk * 2, 128};
         const cuuint64_t one[3] = {Kk, Nn, 1}, one_str[2] = {Kk * 2, Nn * Kk * 2};
-        const cuuint32_t cut_box[3] = {64, 64, slices}, one_box[3] = {64, 64, 1};
+        const cuuint32_t cut_box[3] = {64, 64, 2}, one_box[3] = {64, 64, 1};
         if (!lb_encode(&maps.w, bf, w, 3, p.k64 ? cut : one, p.k64 ? cut_str : one_str, p.k64 ? cut_box : one_box))
             return cudaErrorInvalidValue;
     }
@@ -785,20 +925,12 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, i
         const cuuint64_t rows_dims[4] = {Kk, Tt, 1, 1}, rows_str[3] = {Kk * 2, Tt * Kk * 2, Tt * Kk * 2};
         const cuuint64_t cut_dims[4] = {64, Tt, Kk / 64, Bb};
         const cuuint64_t heads_str[3] = {128, Tt * 128, Tt * Kk * 2}, cut_str[3] = {Kk * 2, 128, Tt * Kk * 2};
-        const cuuint32_t box[4] = {64, 64, p.k64 ? slices : 1, 1}, out_box[4] = {64, 32, 1, 1};
+        const cuuint32_t box[4] = {64, 64, p.k64 ? 2u : 1u, 1};
         if (!lb_encode(&maps.x, bf, x, 4, p.k64 ? cut_dims : rows_dims, heads ? heads_str : p.k64 ? cut_str : rows_str, box))
             return cudaErrorInvalidValue;
-        if (!lb_encode(&maps.dx, bf, dx ? dx : x, 4, heads ? cut_dims : rows_dims, heads ? heads_str : rows_str, out_box))
-            return cudaErrorInvalidValue;
     }
-    if (dw) {
-        const cuuint64_t dims[3] = {Kk, Nn, (cuuint64_t)p.splits}, strides[2] = {Kk * 4, Nn * Kk * 4};
-        const cuuint32_t box[3] = {32, 32, 1};
-        if (!lb_encode(&maps.dw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    } else {
-        maps.dw = maps.dx;
-    }
-    const cudaError_t e = pl.bn == 256 ? lb_launch<256>(maps, pl, stream) : lb_launch<128>(maps, pl, stream);
+    const cudaError_t e = pl.pair ? (relu ? lb_launch<true, true> : lb_launch<true, false>)(maps, pl, stream)
+                                  : (relu ? lb_launch<false, true> : lb_launch<false, false>)(maps, pl, stream);
     if (e != cudaSuccess || (!split && !db)) return e;
     return lb_sum(part, dw, p.splits, p.db, db, N, K, p.db_rows, stream);
 }
