@@ -612,11 +612,11 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                 // (not moved ahead of what was issued since the fetch)
                 asm volatile("" : "+r"(x4[i].x), "+r"(x4[i].y), "+r"(x4[i].z), "+r"(x4[i].w));
                 const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
+                uint32_t four = 0;  // bit e for the low half of word e, bit 16 + e for its high half
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t on = __hgt2_mask(h2[e], __floats2bfloat162_rn(0.f, 0.f));
-                    keep[i >> 2] |= (on & 0x00010001u) << (4 * (i & 3) + e);  // low halves below bit 16
-                }
+                for (int e = 0; e < 4; ++e)
+                    four |= __hgt2_mask(h2[e], __floats2bfloat162_rn(0.f, 0.f)) & (0x00010001u << e);
+                keep[i >> 2] += four << (4 * (i & 3));
             }
         };
         Lines cur = {}, next = {};
@@ -664,8 +664,12 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     if (RELU) {
                         uint32_t* o = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] &= ((keep[sl][i >> 2] >> (4 * (i & 3) + e)) & 0x00010001u) * 0xFFFFu;
+                        for (int e = 0; e < 4; ++e) {
+                            // the two bits to the tops of the halves, and these over the halves
+                            uint32_t on = keep[sl][i >> 2] << (15 - 4 * (i & 3) - e);
+                            asm("prmt.b32 %0, %0, 0, 0xBB99;" : "+r"(on));
+                            o[e] &= on;
+                        }
                     }
                     if (line_in(cur, sl, i)) *reinterpret_cast<uint4*>(to + (long long)(4 * i) * row_stride) = v;
                 }
