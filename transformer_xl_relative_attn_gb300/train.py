@@ -14,6 +14,7 @@ from . import _lib
 from ._lib import TXL_BF16, TXL_F32, AdamwTensor, TxlError, _dtype_code, _invoke, _need, _stream
 
 _HERE = contextlib.nullcontext()
+_LINEAR_GRADS = frozenset(("dx", "dw", "db"))
 STATE_BLOCK = 256  # elements of one block of a flat optimizer state
 
 
@@ -29,7 +30,7 @@ def _on(stream, device):
 
 
 def _scratch(workspace, need: int, device) -> int:
-    """Address of a call's workspace (the C call checks address and size)."""
+    """Address of a caller's workspace (the C call checks its alignment)."""
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if workspace.numel() * workspace.element_size() < need:
@@ -38,28 +39,26 @@ def _scratch(workspace, need: int, device) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_need(device, name: str, *sizes) -> int:
-    """Workspace of a call of these sizes on ``device``: a function of both alone."""
-    return int(_invoke(device, name, *sizes))
+def _workspace_need(index: int, name: str, *sizes) -> int:
+    """Workspace of a call of these sizes on device ``index``: a function of both alone."""
+    return int(_invoke(index, name, *sizes))
 
 
-def _row_args(x, y, gamma, beta):
-    """Checks the tensors that both LayerNorm calls share; returns (rows, d)."""
+def _row_args(x, y, gamma):
+    """Checks the tensors that both LayerNorm calls share; returns (rows, d, shape, dtype, device)."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor [..., d]")
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {x.dtype}: bf16 or fp32 only")
-    d = x.shape[-1]
     shape, dt, dev = x.shape, x.dtype, x.device
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    d = shape[-1]
     if d == 0:
         raise ValueError("x must have a last axis of at least one element")
     _need(x, "x", shape, dt)
     if y is not None:
         _need(y, "y", shape, dt, dev)
     _need(gamma, "gamma", (d,), dt, dev)
-    if beta is not None:
-        _need(beta, "beta", (d,), dt, dev)
-    return x.numel() // d, d
+    return x.numel() // d, d, shape, dt, dev
 
 
 def _ptr(t) -> int:
@@ -71,21 +70,22 @@ def layer_norm_fwd(x, gamma, beta, y=None, eps=1e-5, out=None, mean=None, rstd=N
     (y optional), keeping the statistics that layer_norm_bwd takes.  x [..., d]
     bf16 or fp32 with 1 <= d <= 16384; mean, rstd fp32 [...].  Returns
     (out, mean, rstd); out overlaps no input."""
-    rows, d = _row_args(x, y, gamma, beta)
-    dev, st = x.device, x.shape[:-1]
+    rows, d, shape, dt, dev = _row_args(x, y, gamma)
+    _need(beta, "beta", (d,), dt, dev)
+    st, f32 = shape[:-1], torch.float32
     with _on(stream, dev):
         if out is None:
             out = torch.empty_like(x)
         else:
-            _need(out, "out", x.shape, x.dtype, dev)
+            _need(out, "out", shape, dt, dev)
         if mean is None:
-            mean = torch.empty(st, dtype=torch.float32, device=dev)
+            mean = torch.empty(st, dtype=f32, device=dev)
         else:
-            _need(mean, "mean", st, torch.float32, dev)
+            _need(mean, "mean", st, f32, dev)
         if rstd is None:
-            rstd = torch.empty(st, dtype=torch.float32, device=dev)
+            rstd = torch.empty(st, dtype=f32, device=dev)
         else:
-            _need(rstd, "rstd", st, torch.float32, dev)
+            _need(rstd, "rstd", st, f32, dev)
     rc = _invoke(dev, "txl_layer_norm_fwd", x.data_ptr(), _ptr(y), gamma.data_ptr(), beta.data_ptr(), rows, d,
                  float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _dtype_code(x), _stream(stream, dev))
     if rc != 0:
@@ -109,31 +109,36 @@ def layer_norm_bwd(dout, x, gamma, mean, rstd, y=None, dres=None, stream=None, w
     (fp32 [d], summed in a fixed order).  grads: a dict of preallocated tensors
     to fill; workspace: a uint8 tensor of at least
     layer_norm_bwd_workspace_bytes(...) bytes (allocated here when None)."""
-    rows, d = _row_args(x, y, gamma, None)
-    dev, st = x.device, x.shape[:-1]
-    _need(dout, "dout", x.shape, x.dtype, dev)
+    rows, d, shape, dt, dev = _row_args(x, y, gamma)
+    st, f32, code = shape[:-1], torch.float32, TXL_BF16 if dt is torch.bfloat16 else TXL_F32
+    _need(dout, "dout", shape, dt, dev)
     if dres is not None:
-        _need(dres, "dres", x.shape, x.dtype, dev)
-    _need(mean, "mean", st, torch.float32, dev)
-    _need(rstd, "rstd", st, torch.float32, dev)
-    need = _workspace_need(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, _dtype_code(x))
+        _need(dres, "dres", shape, dt, dev)
+    _need(mean, "mean", st, f32, dev)
+    _need(rstd, "rstd", st, f32, dev)
+    need = _workspace_need(dev.index, "txl_layer_norm_bwd_workspace_bytes", rows, d, code)
     with _on(stream, dev):
         if grads is None:
-            g = {"dx": torch.empty_like(x), "dgamma": torch.empty(d, dtype=torch.float32, device=dev),
-                 "dbeta": torch.empty(d, dtype=torch.float32, device=dev)}
+            dx = torch.empty_like(x)
+            dgamma = torch.empty(d, dtype=f32, device=dev)
+            dbeta = torch.empty(d, dtype=f32, device=dev)
+            grads = {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
         else:
-            g = grads
-            _need(g["dx"], "dx", x.shape, x.dtype, dev)
-            _need(g["dgamma"], "dgamma", (d,), torch.float32, dev)
-            _need(g["dbeta"], "dbeta", (d,), torch.float32, dev)
+            dx, dgamma, dbeta = grads["dx"], grads["dgamma"], grads["dbeta"]
+            _need(dx, "dx", shape, dt, dev)
+            _need(dgamma, "dgamma", (d,), f32, dev)
+            _need(dbeta, "dbeta", (d,), f32, dev)
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            at = workspace.data_ptr()
+        else:
+            at = _scratch(workspace, need, dev)
     rc = _invoke(dev, "txl_layer_norm_bwd", dout.data_ptr(), x.data_ptr(), _ptr(y), gamma.data_ptr(),
-                 mean.data_ptr(), rstd.data_ptr(), _ptr(dres), rows, d, g["dx"].data_ptr(), g["dgamma"].data_ptr(),
-                 g["dbeta"].data_ptr(), _dtype_code(x), _scratch(workspace, need, dev), need, _stream(stream, dev))
+                 mean.data_ptr(), rstd.data_ptr(), _ptr(dres), rows, d, dx.data_ptr(), dgamma.data_ptr(),
+                 dbeta.data_ptr(), code, at, need, _stream(stream, dev))
     if rc != 0:
         raise TxlError(rc, "txl_layer_norm_bwd")
-    return g
+    return grads
 
 
 def _linear_shape(x):
@@ -168,31 +173,46 @@ def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, wo
     layout, B, T, K = _linear_shape(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be [N, K]")
-    bad = [n for n in want if n not in ("dx", "dw", "db")]
-    if bad or not want:
+    if not want or not _LINEAR_GRADS.issuperset(want):
         raise ValueError(f"want names gradients out of dx, dw, db: got {want}")
-    N, dev, bf = w.shape[0], x.device, torch.bfloat16
+    N, dev, bf, f32 = w.shape[0], x.device, torch.bfloat16, torch.float32
     _need(x, "x", x.shape, bf)
     _need(w, "w", (N, K), bf, dev)
     _need(dy, "dy", (B, T, N), bf, dev)
-    need = _workspace_need(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, *("dx" in want, "dw" in want, "db" in want))
-    f32 = torch.float32
-    spec = {"dx": (x.shape, bf), "dw": ((N, K), f32), "db": ((N,), f32)}
+    wx, ww, wb = "dx" in want, "dw" in want, "db" in want
+    need = _workspace_need(dev.index, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, wx, ww, wb)
+    dx = dw = db = None
     with _on(stream, dev):
         if grads is None:
-            g = {n: torch.empty(spec[n][0], dtype=spec[n][1], device=dev) for n in want}
+            grads = {}
+            if wx:
+                grads["dx"] = dx = torch.empty_like(x)
+            if ww:
+                grads["dw"] = dw = torch.empty((N, K), dtype=f32, device=dev)
+            if wb:
+                grads["db"] = db = torch.empty(N, dtype=f32, device=dev)
         else:
-            g = grads
-            for n in want:
-                _need(g[n], n, spec[n][0], spec[n][1], dev)
-        if workspace is None and need:
+            if wx:
+                dx = grads["dx"]
+                _need(dx, "dx", x.shape, bf, dev)
+            if ww:
+                dw = grads["dw"]
+                _need(dw, "dw", (N, K), f32, dev)
+            if wb:
+                db = grads["db"]
+                _need(db, "db", (N,), f32, dev)
+        if workspace is not None:
+            at = _scratch(workspace, need, dev)
+        elif need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            at = workspace.data_ptr()
+        else:
+            at = 0
     rc = _invoke(dev, "txl_linear_bwd", dy.data_ptr(), x.data_ptr(), layout, B, T, K, w.data_ptr(), N,
-                 int(bool(relu_in)), *[g[n].data_ptr() if n in want else 0 for n in ("dx", "dw", "db")],
-                 _scratch(workspace, need, dev) if need else 0, need, _stream(stream, dev))
+                 int(bool(relu_in)), _ptr(dx), _ptr(dw), _ptr(db), at, need, _stream(stream, dev))
     if rc != 0:
         raise TxlError(rc, "txl_linear_bwd")
-    return g
+    return grads
 
 
 class AdamW:
