@@ -83,6 +83,7 @@ struct AdamwTable {
 };
 
 struct AdamwFlat {
+    unsigned blocks;  // of each buffer
     float* master;
     void* m;
     float* ms;
@@ -164,7 +165,7 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float
 // `full`: the whole block is the tensor's.
 template <typename T>
 __device__ __forceinline__ void load4_tail(const T* p, bool full, int left, float (&f)[4]) {
-    if (full) {
+    if (full && TXL_BOUNDS(left >= 4, 1001, left)) {
         load4(p, f);
     } else {
 #pragma unroll
@@ -173,7 +174,7 @@ __device__ __forceinline__ void load4_tail(const T* p, bool full, int left, floa
 }
 template <typename T>
 __device__ __forceinline__ void store4_tail(T* p, bool full, int left, const float (&f)[4]) {
-    if (full) {
+    if (full && TXL_BOUNDS(left >= 4, 1002, left)) {
         store4(p, f);
     } else {
 #pragma unroll
@@ -336,6 +337,7 @@ __device__ __forceinline__ void adamw_load(const AdamwTable<CAP>& t, int& e, uns
     r.p = static_cast<P*>(t.e[e].p) + i + lane * 4;
     r.wd = t.e[e].wd;
     r.blk = first + b;
+    if (!TXL_BOUNDS(r.blk < flat.blocks, 1003, r.blk)) r.blk = 0;
     const G* const gp = static_cast<const G*>(t.e[e].g) + i + lane * 4;
     const size_t at = (size_t)r.blk * kAdamwBlock + lane * 4;
 #pragma unroll
@@ -521,7 +523,7 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     e = launch_pdl(adamw_coef_kernel, 1, a.max_norm > 0 ? 1024u : 32u, stream, part, n_part, std::log(a.beta1),
                    std::log(a.beta2), (float)a.max_norm, a.seed, a.lr, a.steps, a.grad_norm, coef);
     if (e != cudaSuccess) return e;
-    const AdamwFlat flat = {a.master, a.exp_avg, a.exp_avg_scale, a.exp_avg_sq, a.exp_avg_sq_scale};
+    const AdamwFlat flat = {(unsigned)blocks, a.master, a.exp_avg, a.exp_avg_scale, a.exp_avg_sq, a.exp_avg_sq_scale};
     const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
     return each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned first) {
         auto go = [&](auto kern) {
