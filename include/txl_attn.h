@@ -343,8 +343,7 @@ int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* 
 /*
  * LayerNorm for training: txl_layer_norm's forward that also keeps each row's
  * statistics, and its gradients.  Any row length 1 <= d <= 16384
- * (TXL_ERR_UNSUPPORTED beyond), any number of rows (0 too), dtype TXL_BF16 or
- * TXL_F32 for x, y, gamma, beta, out, dout, dres and dx; statistics and
+ * and 0 <= rows < 2^31 (TXL_ERR_UNSUPPORTED beyond), dtype TXL_BF16 or TXL_F32 for x, y, gamma, beta, out, dout, dres and dx; statistics and
  * parameter gradients fp32.
  *
  * txl_layer_norm_fwd: with z = x + y (y may be null),

@@ -340,3 +340,17 @@ def test_bound_tensors_are_checked():
     shared = torch.ones(8, 8, device="cuda")               # one gradient for two parameters is read twice
     txl.AdamW([p, torch.zeros(8, 8, device="cuda")], [shared, shared], lr=1e-3).step()
     assert float((p + 1e-3).abs().max()) < 1e-8
+
+
+def test_storage_given_away_stays_valid():
+    """A parameter that is given other storage after binding: the step goes to the
+    memory that was bound, which is still there."""
+    p, g = torch.ones(1 << 20, device="cuda"), torch.ones(1 << 20, device="cuda")
+    opt = txl.AdamW([p], [g], lr=1e-2)
+    old = p.data_ptr()
+    p.data = torch.zeros(1 << 20, device="cuda")
+    fresh = torch.full((1 << 20,), 5.0, device="cuda")  # would take the freed memory
+    assert fresh.data_ptr() != old
+    opt.step()
+    torch.cuda.synchronize()
+    assert bool((p == 0).all()) and bool((fresh == 5).all())

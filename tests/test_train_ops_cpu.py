@@ -33,7 +33,7 @@ def test_layer_norm_fwd_rejects_bad_arguments(lib):
         assert call(**{name: addr(7) + 8}) == -3, name
     assert call(rows=-1) == -1 and call(d=0) == -1 and call(dtype=2) == -1
     assert call(eps=-1.0) == -1 and call(eps=math.nan) == -1
-    assert call(d=16385) == -2 and call(rows=1 << 40, d=2) == -2
+    assert call(d=16385) == -2 and call(rows=1 << 31, d=2) == -2 and call(rows=1 << 30, d=2048) == -2
     assert call(out=addr(0)) == -4 and call(y=addr(3)) == -4            # out over x, over y
     assert call(mean=addr(4), rstd=addr(4) + 16) == -4                    # the statistics overlap
     assert call(rows=0, x=None, out=None, mean=None, rstd=None) == 0      # nothing to do

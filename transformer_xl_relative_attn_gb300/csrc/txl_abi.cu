@@ -662,8 +662,8 @@ bool any_written_overlap(Range* r, size_t n) {
 
 constexpr int kLayerNormMaxD = 16384;
 
-// rows * d below 2^40, so that byte offsets stay far inside 64 bits.
-bool row_data_too_large(long long rows, int d) { return rows > (1ll << 40) / d; }
+// At most 2^31 - 1 rows (a CTA takes one or more), rows * d below 2^40.
+bool row_data_too_large(long long rows, int d) { return rows > 0x7FFFFFFFll || rows > (1ll << 40) / d; }
 
 bool bad_workspace(const void* workspace, size_t bytes, size_t need) {
     return need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || bytes < need);

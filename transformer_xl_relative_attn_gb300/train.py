@@ -223,8 +223,10 @@ class AdamW:
     parameters get an fp32 master copy, which the steps update and round into
     them: the forward kernels keep reading the same tensors); ``grads``: one
     gradient per parameter, fp32 or bf16, the buffers that the backward calls
-    fill.  Both are bound here: step() reads the gradients from these buffers and
-    updates these parameters in place.  ``weight_decay``: one number, or one per
+    fill.  Both are bound here, as a captured graph binds them: step() reads the
+    gradients from this memory and updates the parameters in this memory, which
+    the optimizer keeps alive (a tensor that is given other storage later, as by
+    ``p.data = ...``, is no longer the one that is stepped).  ``weight_decay``: one number, or one per
     parameter.  ``max_norm``: gradients are scaled by min(1, max_norm / norm), norm
     the 2-norm of all of them, kept in ``grad_norm`` [1]; a norm that is not finite
     makes the step change nothing.  ``state_bits`` 8: the moments as e4m3 codes
@@ -264,6 +266,7 @@ class AdamW:
             self._table[i] = AdamwTensor(p.data_ptr(), g.data_ptr(), p.numel(), decay[i], 0)
             self.starts.append(total)
             total += -(-p.numel() // STATE_BLOCK) * STATE_BLOCK
+        self._storages = [t.untyped_storage() for t in self.params + self.grads]
         self.betas, self.eps, self.weight_decay = tuple(map(float, betas)), float(eps), decay
         self.state_bits, self.max_norm, self.seed = state_bits, max_norm, int(seed) & 0xFFFFFFFF
         self._fixed_stream = stream
