@@ -86,6 +86,13 @@ struct Vec<__nv_bfloat16, 1> {
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float2& pair(float* f, int i) { return reinterpret_cast<float2*>(f)[i]; }
 
+// 1 / sqrt(a) to about 1 ulp: the approximation and one Newton step (0 and infinities as
+// they come from the approximation).
+__device__ __forceinline__ float inv_sqrt(float a) {
+    const float r = rsqrtf(a), h = 0.5f * a * r;
+    return a > 0.f && a < INFINITY ? fmaf(r, fmaf(-h, r, 0.5f), r) : r;
+}
+
 __device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -135,14 +142,14 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* sh, int phase) {
     return a;
 }
 
-// E elements of row r of a tensor, this thread's: vectors of V, `t` + TPR i.
+// E elements of a row, this thread's: vectors of V, the i-th `TPR V i` elements behind p,
+// of which `left` (from p on) are the row's; 0 behind its end.
 template <typename T, int V, int E, int TPR>
-__device__ __forceinline__ void load_row(const T* p, long long r, int d, int t, float (&f)[E]) {
+__device__ __forceinline__ void load_row(const T* p, int left, float (&f)[E]) {
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
-        const int c = (t + TPR * i) * V;
-        if (c < d && TXL_BOUNDS(c + V <= d, 901, r * d + c)) {
-            Vec<T, V>::load(p + r * d + c, f + V * i);
+        if (TPR * V * i < left && TXL_BOUNDS(TPR * V * i + V <= left, 901, left)) {
+            Vec<T, V>::load(p + TPR * V * i, f + V * i);
         } else {
 #pragma unroll
             for (int k = 0; k < V; ++k) f[V * i + k] = 0.f;
@@ -153,7 +160,7 @@ __device__ __forceinline__ void load_row(const T* p, long long r, int d, int t, 
 template <typename T, int V, int E, int W>
 __global__ void __launch_bounds__(Shape<W, 128>::THREADS)
 ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restrict__ gamma,
-              const T* __restrict__ beta, long long rows, int d, float eps, T* __restrict__ out,
+              const T* __restrict__ beta, long long rows, int d, float inv_d, float eps, T* __restrict__ out,
               float* __restrict__ mean_out, float* __restrict__ rstd_out) {
     using S = Shape<W, 128>;
     __shared__ float sh[2 * S::THREADS / 32];
@@ -162,12 +169,14 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     const int t = threadIdx.x % S::TPR;
     const long long r = (long long)blockIdx.x * S::R + threadIdx.x / S::TPR;
     const bool in = r < rows;  // (the barriers of a row are the CTA's)
+    const int left = d - t * V;
+    const long long at = r * d + t * V;
     alignas(8) float z[E];
     if (in) {
-        load_row<T, V, E, S::TPR>(x, r, d, t, z);
+        load_row<T, V, E, S::TPR>(x + at, left, z);
         if (y) {
             alignas(8) float b[E];
-            load_row<T, V, E, S::TPR>(y, r, d, t, b);
+            load_row<T, V, E, S::TPR>(y + at, left, b);
 #pragma unroll
             for (int e = 0; e < E / 2; ++e) pair(z, e) = __fadd2_rn(pair(z, e), pair(b, e));
         }
@@ -178,11 +187,11 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     float2 s = both(0.f);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) s = __fadd2_rn(s, pair(z, e));
-    const float mean = row_sum<W>(s.x + s.y, sh, 0) / d;
+    const float mean = row_sum<W>(s.x + s.y, sh, 0) * inv_d;
     // (behind the row's end z is 0 and stays so)
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
-        const float m = (t + S::TPR * i) * V < d ? -mean : 0.f;
+        const float m = S::TPR * V * i < left ? -mean : 0.f;
         if (V == 1)
             z[i] += m;
         else
@@ -192,22 +201,22 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     float2 q = both(0.f);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) q = __ffma2_rn(pair(z, e), pair(z, e), q);
-    const float rstd = 1.f / sqrtf(row_sum<W>(q.x + q.y, sh, 1) / d + eps);
+    const float rstd = inv_sqrt(fmaf(row_sum<W>(q.x + q.y, sh, 1), inv_d, eps));
     if (!in) return;
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
-        const int c = (t + S::TPR * i) * V;
-        if (c < d && TXL_BOUNDS(c + V <= d && r < rows, 902, r * d + c)) {
+        constexpr int OFF = S::TPR * V;
+        if (OFF * i < left && TXL_BOUNDS(OFF * i + V <= left && r < rows, 902, at)) {
             alignas(8) float g[V], b[V], o[V];
-            Vec<T, V>::load(gamma + c, g);
-            Vec<T, V>::load(beta + c, b);
+            Vec<T, V>::load(gamma + t * V + OFF * i, g);
+            Vec<T, V>::load(beta + t * V + OFF * i, b);
             if (V == 1)
                 o[0] = fmaf(z[i] * rstd, g[0], b[0]);
             else
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
                     pair(o, e) = __ffma2_rn(__fmul2_rn(pair(z, V / 2 * i + e), both(rstd)), pair(g, e), pair(b, e));
-            Vec<T, V>::store(out + r * d + c, o);
+            Vec<T, V>::store(out + at + OFF * i, o);
         }
     }
     if (t == 0) {
@@ -226,7 +235,8 @@ template <typename T, int V, int E, int W>
 __global__ void __launch_bounds__(Shape<W>::THREADS, bwd_ctas<E, W>())
 ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __restrict__ y,
               const T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
-              const T* __restrict__ dres, long long rows, int d, T* __restrict__ dx, float* __restrict__ part) {
+              const T* __restrict__ dres, long long rows, int d, float inv_d, T* __restrict__ dx,
+              float* __restrict__ part) {
     using S = Shape<W>;
     __shared__ float2 sh[2 * S::THREADS / 32];
     __shared__ float fold[S::R > 1 ? S::THREADS / 2 * 2 * E : 1];
@@ -234,24 +244,30 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = threadIdx.x % S::TPR, lr = threadIdx.x / S::TPR;
     alignas(8) float dg[E], db[E], gam[E];
-    load_row<T, V, E, S::TPR>(gamma, 0, d, t, gam);
+    const int left = d - t * V;
+    load_row<T, V, E, S::TPR>(gamma + t * V, left, gam);
 #pragma unroll
     for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
     int phase = 0;
-    for (long long r0 = (long long)blockIdx.x * S::R; r0 < rows; r0 += (long long)gridDim.x * S::R, phase ^= 1) {
-        const long long r = r0 + lr;
-        const bool in = r < rows;
+    // where this thread's elements of its rows lie, row after row
+    const long long first = (long long)blockIdx.x * S::R + lr, step = (long long)gridDim.x * S::R, hop = step * d;
+    long long at = first * d + t * V;
+    int todo = (int)(rows > (long long)blockIdx.x * S::R ? (rows - (long long)blockIdx.x * S::R + step - 1) / step : 0);
+    const float *mp = mean + first, *rp = rstd + first;
+    long long past = rows - first;  // rows from this thread's on
+    for (; todo > 0; --todo, phase ^= 1, at += hop, past -= step, mp += step, rp += step) {
+        const bool in = past > 0;
         alignas(8) float xh[E], g[E];
         float rs = 0.f;
         float2 s = both(0.f);
         if (in) {
-            const float mu = mean[r];
-            rs = rstd[r];
-            load_row<T, V, E, S::TPR>(x, r, d, t, xh);
-            load_row<T, V, E, S::TPR>(dout, r, d, t, g);
+            const float mu = *mp;
+            rs = *rp;
+            load_row<T, V, E, S::TPR>(x + at, left, xh);
+            load_row<T, V, E, S::TPR>(dout + at, left, g);
             if (y) {
                 alignas(8) float b[E];
-                load_row<T, V, E, S::TPR>(y, r, d, t, b);
+                load_row<T, V, E, S::TPR>(y + at, left, b);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) pair(xh, e) = __fadd2_rn(pair(xh, e), pair(b, e));
             }
@@ -274,7 +290,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
             // no registers of their own through it
             if (dres) {
                 alignas(8) float a[E];
-                load_row<T, V, E, S::TPR>(dres, r, d, t, a);
+                load_row<T, V, E, S::TPR>(dres + at, left, a);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) pair(g, e) = __ffma2_rn(pair(g, e), both(rs), pair(a, e));
             } else {
@@ -284,13 +300,13 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
         }
         s = row_sum2<W>(s, sh, phase);
         if (!in) continue;
-        const float2 c1 = both(-rs * s.x / d), c2 = both(-rs * s.y / d);
+        const float2 c1 = both(-rs * s.x * inv_d), c2 = both(-rs * s.y * inv_d);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) pair(g, e) = __fadd2_rn(__ffma2_rn(pair(xh, e), c2, pair(g, e)), c1);
 #pragma unroll
         for (int i = 0; i < E / V; ++i) {
-            const int c = (t + S::TPR * i) * V;
-            if (c < d && TXL_BOUNDS(c + V <= d, 903, r * d + c)) Vec<T, V>::store(dx + r * d + c, g + V * i);
+            constexpr int OFF = S::TPR * V;
+            if (OFF * i < left && TXL_BOUNDS(OFF * i + V <= left, 903, at)) Vec<T, V>::store(dx + at + OFF * i, g + V * i);
         }
     }
     // the CTA's rows fold in halves, into the first row's threads
@@ -419,7 +435,7 @@ cudaError_t ln_fwd(const void* x, const void* y, const void* gamma, const void* 
         if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
         return launch_pdl(ln_fwd_kernel<T, V, E, W>, (unsigned)ctas, (unsigned)Shape<W, 128>::THREADS, stream,
                           static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(gamma),
-                          static_cast<const T*>(beta), rows, d, eps, static_cast<T*>(out), mean, rstd);
+                          static_cast<const T*>(beta), rows, d, 1.f / d, eps, static_cast<T*>(out), mean, rstd);
     });
 }
 
@@ -433,7 +449,7 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
         constexpr int E = decltype(k)::e, W = decltype(k)::w;
         return launch_pdl(ln_bwd_kernel<T, V, E, W>, (unsigned)grid, (unsigned)Shape<W>::THREADS, stream,
                           static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
-                          static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d,
+                          static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d, 1.f / d,
                           static_cast<T*>(dx), part);
     });
     if (e != cudaSuccess) return e;
