@@ -7,22 +7,23 @@
 //
 // One persistent launch holds both products.  In both the second operand (W for
 // dx, x for dw) is read with K contiguous and its other axis reduced over (MN-major
-// for the tensor core) and the output is tiled 128 x BN with BN along K, so one
-// pipeline serves both: 64-row boxes of 64 columns land in shared memory the same
-// way, and only dy's view differs (K-major with the rows as M for dx, MN-major
-// with the columns as M for dw).  Nothing is transposed in memory.
+// for the tensor core), so one pipeline serves both: 64-row boxes of 64 columns land
+// in shared memory the same way, and only dy's view differs (K-major with the rows as M
+// for dx, MN-major with the columns as M for dw).  Nothing is transposed in memory.
+// Two CTAs of a cluster share a 256 x 256 tile (cta_group::2), or one CTA takes 128 x
+// 128 where the larger tiles would leave SMs idle.
 //
 // The ReLU mask is a factor of the epilogue of dx, read from x before the tile's
 // MMAs end.  db is summed by two warps of every CTA that have no part in the products,
 // from dy in global memory (L2 mostly: the products read it at the same time).
 //
-// dw has few tiles and a long reduction (base512's second feed-forward layer: 32
-// tiles over 11264 rows), so its rows are split over several CTAs, each writing an
+// dw has few tiles and a long reduction (base512's second feed-forward layer: 16
+// tiles over 11264 rows), so its rows are split over several pairs, each writing an
 // fp32 partial tile to the workspace; a second launch adds the parts, and db's, in a
 // fixed order (the same inputs give the same bits).  The tensor core cuts off what it
 // adds to an accumulator (1.7e-8 of the result per MMA on random data, measured), so
 // a dw accumulator takes 1024 rows at a time and the epilogue adds these in registers:
-// at 6144 rows the error went from 3.3e-6 to below that of an fp32 product.
+// at 6144 rows the error went from 3.3e-6 to 1.0e-6 (an fp32 library product's: 0.8e-6).
 //
 // TMA is what the loads need all of: an instruction costs its issuing thread some
 // 100 cycles whatever it loads, so a stage of 32 KB is two instructions where the widths
@@ -310,7 +311,10 @@ __device__ __forceinline__ bool lb_wait_landed(uint64_t* bar, uint32_t parity, i
 }
 __device__ __forceinline__ uint4 lb_ld_shared_v4(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -358,145 +362,146 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
     LbSchedule sched(p, C::CTAS);
     bool dw;
     int item;
-    // Registers: the launch's 384 * 168 = 64512 as 128 * 80 + 256 * 208 (and 1024 to spare).  An epilogue thread
-    // keeps 128 running sums of dw, or 64 registers of the next mask, besides what it unpacks.
+    // Registers: the launch's 384 * 168 = 64512 as 128 * 80 + 256 * 208 (1024 to spare).  An
+    // epilogue thread keeps 128 running sums of dw besides what it unpacks; a single spilled
+    // register costs more than the split (with 230 KB of shared memory in use L1 holds little).
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 0) {
-        // ---------------------------------------------------- TMA producer
-        // A pair's full barriers are its first CTA's, which expects both CTAs' bytes; the
-        // second's loads may land before it does (the barrier waits for the arrival).
-        // One thread's instructions per stage bound the loads (at 870 cycles a stage took
-        // longer than its MMAs), so what does not change is kept out of the loops.
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t s = 0, phase = 1;  // slot, parity of its empty barrier (a fresh one passes for 1)
-            long long loads = 0;
-            const uint32_t full0 = PAIR ? lb_mapa(&sh->full[0], 0) : smem_u32(&sh->full[0]);
-            auto next_slot = [&](uint32_t& a, uint32_t& b, uint32_t& bar) {
-                if (!mbar_wait(&sh->empty[s], phase, kDevTimeoutProducer, abort, p.status)) return ok = false;
-                if (rank == 0) mbar_expect_tx(&sh->full[s], (SZ_A + SZ_B) * C::CTAS);
-                a = s_base + OFF_A + s * SZ_A;
-                b = s_base + OFF_B + s * SZ_B;
-                bar = full0 + 8 * s;
-                if (++s == STAGES) s = 0, phase ^= 1;
-                ++loads;
-                return true;
-            };
-            const bool n64 = p.n64, k64 = p.k64;
-            while (ok && sched.next(dw, item)) {
-                const LbItem it = lb_item<PAIR>(p, dw, item);
-                const int m = it.m0 + BM * rank, k = it.k0 + 128 * rank;  // this CTA's share
-                uint32_t a, b, bar;
-                if (dw) {
-                    const int m_el = n64 ? 0 : m, m_sl = n64 ? m >> 6 : 0, k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
-                    int bt = it.s0 / p.t_steps, t = (it.s0 - bt * p.t_steps) * BR;
-                    const int T = p.T;
-                    for (int n = it.s1 - it.s0; n > 0 && next_slot(a, b, bar); --n) {
-                        lb_load_4d<PAIR>(a, &maps.dyc, bar, m_el, t, m_sl, bt);
-                        lb_load_4d<PAIR>(b, &maps.x, bar, k_el, t, k_sl, bt);
-                        if (!n64) lb_load_4d<PAIR>(a + SZ_BOX, &maps.dyc, bar, m_el + 64, t, 0, bt);
-                        if (!k64) lb_load_4d<PAIR>(b + SZ_BOX, &maps.x, bar, k_el + 64, t, 0, bt);
-                        t += BR;
-                        if (t >= T) t = 0, ++bt;
-                    }
-                } else {
-                    const int k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
-                    int r = 0;  // column of dy, row of w
-                    for (int n = it.s1; n > 0 && next_slot(a, b, bar); --n) {
-                        lb_load_3d<PAIR>(a, &maps.dy, bar, r, m, it.b);
-                        lb_load_3d<PAIR>(b, &maps.w, bar, k_el, r, k_sl);
-                        if (!k64) lb_load_3d<PAIR>(b + SZ_BOX, &maps.w, bar, k_el + 64, r, 0);
-                        r += BR;
-                    }
-                }
-            }
-            // the last load into each slot has landed before the CTAs exit
-            for (int i = 0; i < STAGES && rank == 0; ++i) {
-                const long long c = loads - 1 - i;
-                if (c >= 0) lb_wait_landed(&sh->full[c % STAGES], (c / STAGES) & 1, p.status);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer
-        if (rank == 0) {
-            const uint32_t leader = elect_one();
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kDevTimeoutMma, abort, p.status));
-                return ok;
-            };
-            const uint64_t dA0 = smem_desc_sw128(s_base + OFF_A, 16, 1024);      // K-major: rows of dy
-            const uint64_t dAm = smem_desc_sw128(s_base + OFF_A, SZ_BOX, 1024);  // MN-major: columns of dy
-            const uint64_t dB0 = smem_desc_sw128(s_base + OFF_B, SZ_BOX, 1024);  // MN-major
-            uint32_t s = 0, phase = 0;  // slot, parity of its full barrier
-            int j = 0;                  // accumulators filled
-            while (ok && sched.next(dw, item)) {
-                const LbItem it = lb_item<PAIR>(p, dw, item);
-                // dx's first operand steps along its rows (32 bytes per MMA), dw's and every
-                // second one by 16 rows of 128 bytes
-                const uint64_t dA = dw ? dAm : dA0;
-                const uint64_t a_step = dw ? 128 : 2;
-                const uint32_t idesc = dw ? C::IDESC_DW : C::IDESC_DX;
-                int left = it.s1 - it.s0;
-                do {
-                    const int acc = j & 1, n = dw ? min(left, CHAIN) : left;
-                    if (j >= 2 && !wait(&sh->acc_empty[acc], ((j >> 1) - 1) & 1)) break;
-                    tc_fence_after();
-                    const uint32_t d_acc = tmem + acc * BN;
-                    uint32_t more_than_first = 0;
-                    for (int i = 0; i < n; ++i) {
-                        if (!wait(&sh->full[s], phase)) break;
-                        tc_fence_after();
-                        const uint64_t ad = dA + s * (SZ_A >> 4), bd = dB0 + s * (SZ_B >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < BR / 16; ++kk) {
-                            lb_mma<PAIR>(d_acc, ad + a_step * kk, bd + 128 * kk, idesc, more_than_first, leader);
-                            more_than_first = 1;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 0) {
+            // ---------------------------------------------------- TMA producer
+            // A pair's full barriers are its first CTA's, which expects both CTAs' bytes; the
+            // second's loads may land before it does (the barrier waits for the arrival).
+            // One thread's instructions per stage bound the loads (at 870 cycles a stage took
+            // longer than its MMAs), so what does not change is kept out of the loops.
+            if (lane == 0) {
+                bool ok = true;
+                uint32_t s = 0, phase = 1;  // slot, parity of its empty barrier (a fresh one passes for 1)
+                long long loads = 0;
+                const uint32_t full0 = PAIR ? lb_mapa(&sh->full[0], 0) : smem_u32(&sh->full[0]);
+                auto next_slot = [&](uint32_t& a, uint32_t& b, uint32_t& bar) {
+                    if (!mbar_wait(&sh->empty[s], phase, kDevTimeoutProducer, abort, p.status)) return ok = false;
+                    if (rank == 0) mbar_expect_tx(&sh->full[s], (SZ_A + SZ_B) * C::CTAS);
+                    a = s_base + OFF_A + s * SZ_A;
+                    b = s_base + OFF_B + s * SZ_B;
+                    bar = full0 + 8 * s;
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                    ++loads;
+                    return true;
+                };
+                const bool n64 = p.n64, k64 = p.k64;
+                while (ok && sched.next(dw, item)) {
+                    const LbItem it = lb_item<PAIR>(p, dw, item);
+                    const int m = it.m0 + BM * rank, k = it.k0 + 128 * rank;  // this CTA's share
+                    uint32_t a, b, bar;
+                    if (dw) {
+                        const int m_el = n64 ? 0 : m, m_sl = n64 ? m >> 6 : 0, k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
+                        int bt = it.s0 / p.t_steps, t = (it.s0 - bt * p.t_steps) * BR;
+                        const int T = p.T;
+                        for (int n = it.s1 - it.s0; n > 0 && next_slot(a, b, bar); --n) {
+                            lb_load_4d<PAIR>(a, &maps.dyc, bar, m_el, t, m_sl, bt);
+                            lb_load_4d<PAIR>(b, &maps.x, bar, k_el, t, k_sl, bt);
+                            if (!n64) lb_load_4d<PAIR>(a + SZ_BOX, &maps.dyc, bar, m_el + 64, t, 0, bt);
+                            if (!k64) lb_load_4d<PAIR>(b + SZ_BOX, &maps.x, bar, k_el + 64, t, 0, bt);
+                            t += BR;
+                            if (t >= T) t = 0, ++bt;
                         }
-                        if (leader) lb_commit<PAIR>(&sh->empty[s]);
-                        if (++s == STAGES) s = 0, phase ^= 1;
-                    }
-                    if (!ok) break;
-                    if (leader) lb_commit<PAIR>(&sh->acc_full[acc]);
-                    ++j;
-                    left -= n;
-                } while (left > 0);
-            }
-            if (leader) lb_commit<PAIR>(&sh->drain);
-            lb_wait_landed(&sh->drain, 0, p.status);
-        }
-        __syncwarp();
-    } else {
-        // ---------------------------------------------------- column sums of dy
-        // A warp adds 256 columns (8 per lane) over one of db_rows ranges of rows.
-        if (p.db_rows) {
-            const int groups = (p.N + 255) >> 8;
-            const long long rows = (long long)p.B * p.T;
-            for (int u = blockIdx.x * 2 + warp - 2; u < groups * p.db_rows; u += 2 * gridDim.x) {
-                const int part = u / groups, n = (u - part * groups) * 256 + lane * 8;  // N is a multiple of 8
-                if (n >= p.N) continue;
-                const long long r0 = rows * part / p.db_rows, r1 = rows * (part + 1) / p.db_rows;
-                float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-                for (long long r = r0; r < r1; ++r) {
-                    if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.dy + r * p.N + n));
-                    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = __bfloat1622float2(h[e]);
-                        a[2 * e] += f.x;
-                        a[2 * e + 1] += f.y;
+                    } else {
+                        const int k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
+                        int r = 0;  // column of dy, row of w
+                        for (int n = it.s1; n > 0 && next_slot(a, b, bar); --n) {
+                            lb_load_3d<PAIR>(a, &maps.dy, bar, r, m, it.b);
+                            lb_load_3d<PAIR>(b, &maps.w, bar, k_el, r, k_sl);
+                            if (!k64) lb_load_3d<PAIR>(b + SZ_BOX, &maps.w, bar, k_el + 64, r, 0);
+                            r += BR;
+                        }
                     }
                 }
-                float4* to = reinterpret_cast<float4*>(p.db + (size_t)part * p.N + n);
-                to[0] = make_float4(a[0], a[1], a[2], a[3]);
-                to[1] = make_float4(a[4], a[5], a[6], a[7]);
+                // the last load into each slot has landed before the CTAs exit
+                for (int i = 0; i < STAGES && rank == 0; ++i) {
+                    const long long c = loads - 1 - i;
+                    if (c >= 0) lb_wait_landed(&sh->full[c % STAGES], (c / STAGES) & 1, p.status);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------------------------------------------- MMA issuer
+            if (rank == 0) {
+                const uint32_t leader = elect_one();
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kDevTimeoutMma, abort, p.status));
+                    return ok;
+                };
+                const uint64_t dA0 = smem_desc_sw128(s_base + OFF_A, 16, 1024);      // K-major: rows of dy
+                const uint64_t dAm = smem_desc_sw128(s_base + OFF_A, SZ_BOX, 1024);  // MN-major: columns of dy
+                const uint64_t dB0 = smem_desc_sw128(s_base + OFF_B, SZ_BOX, 1024);  // MN-major
+                uint32_t s = 0, phase = 0;  // slot, parity of its full barrier
+                int j = 0;                  // accumulators filled
+                while (ok && sched.next(dw, item)) {
+                    const LbItem it = lb_item<PAIR>(p, dw, item);
+                    // dx's first operand steps along its rows (32 bytes per MMA), dw's and every
+                    // second one by 16 rows of 128 bytes
+                    const uint64_t dA = dw ? dAm : dA0;
+                    const uint64_t a_step = dw ? 128 : 2;
+                    const uint32_t idesc = dw ? C::IDESC_DW : C::IDESC_DX;
+                    int left = it.s1 - it.s0;
+                    do {
+                        const int acc = j & 1, n = dw ? min(left, CHAIN) : left;
+                        if (j >= 2 && !wait(&sh->acc_empty[acc], ((j >> 1) - 1) & 1)) break;
+                        tc_fence_after();
+                        const uint32_t d_acc = tmem + acc * BN;
+                        uint32_t more_than_first = 0;
+                        for (int i = 0; i < n; ++i) {
+                            if (!wait(&sh->full[s], phase)) break;
+                            tc_fence_after();
+                            const uint64_t ad = dA + s * (SZ_A >> 4), bd = dB0 + s * (SZ_B >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < BR / 16; ++kk) {
+                                lb_mma<PAIR>(d_acc, ad + a_step * kk, bd + 128 * kk, idesc, more_than_first, leader);
+                                more_than_first = 1;
+                            }
+                            if (leader) lb_commit<PAIR>(&sh->empty[s]);
+                            if (++s == STAGES) s = 0, phase ^= 1;
+                        }
+                        if (!ok) break;
+                        if (leader) lb_commit<PAIR>(&sh->acc_full[acc]);
+                        ++j;
+                        left -= n;
+                    } while (left > 0);
+                }
+                if (leader) lb_commit<PAIR>(&sh->drain);
+                lb_wait_landed(&sh->drain, 0, p.status);
+            }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------- column sums of dy
+            // A warp adds 256 columns (8 per lane) over one of db_rows ranges of rows.
+            if (p.db_rows) {
+                const int groups = (p.N + 255) >> 8;
+                const long long rows = (long long)p.B * p.T;
+                for (int u = blockIdx.x * 2 + warp - 2; u < groups * p.db_rows; u += 2 * gridDim.x) {
+                    const int part = u / groups, n = (u - part * groups) * 256 + lane * 8;  // N is a multiple of 8
+                    if (n >= p.N) continue;
+                    const long long r0 = rows * part / p.db_rows, r1 = rows * (part + 1) / p.db_rows;
+                    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+                    for (long long r = r0; r < r1; ++r) {
+                        if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.dy + r * p.N + n));
+                        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __bfloat1622float2(h[e]);
+                            a[2 * e] += f.x;
+                            a[2 * e + 1] += f.y;
+                        }
+                    }
+                    float4* to = reinterpret_cast<float4*>(p.db + (size_t)part * p.N + n);
+                    to[0] = make_float4(a[0], a[1], a[2], a[3]);
+                    to[1] = make_float4(a[4], a[5], a[6], a[7]);
+                }
             }
         }
-    }
     } else {
         // ---------------------------------------------------- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -569,7 +574,8 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                         const int row = 4 * i + lrow;
                         const uint4 v = lb_ld_shared_v4(chunk_at(row, lc));
                         const size_t at = (size_t)(m + row) * p.K + c;
-                        if (m + row < p.N && c < p.K && TXL_BOUNDS(at + 4 <= (size_t)p.N * p.K && it.split < p.splits, 803, at))
+                        if (m + row < p.N && c < p.K &&
+                            TXL_BOUNDS(at + 4 <= (size_t)p.N * p.K && it.split < p.splits, 803, at))
                             *reinterpret_cast<uint4*>(out + at) = v;
                     }
                     __syncwarp();
@@ -620,15 +626,17 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
             }
         };
         Lines cur = {}, next = {};
+        // Each slice of the next tile is on its way for a slice's time and packed behind it, the
+        // last one only when the next tile begins.
         uint32_t keep[SL][2];
+        uint4 x4[8];
         if (ok && more) {
             next = lines_of(item);
             if (RELU) {
 #pragma unroll
                 for (int sl = 0; sl < SL; ++sl) {
-                    uint4 x4[8];
+                    if (sl) mask_of(x4, keep[sl - 1]);
                     fetch(x4, next, sl);
-                    mask_of(x4, keep[sl]);
                 }
             }
         }
@@ -636,12 +644,15 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
             cur = next;
             more = sched.next(dw, item);
             if (more) next = lines_of(item);
+            uint32_t first[2];  // the next tile's first mask, until this one's is used
+            if (RELU) {
+                mask_of(x4, keep[SL - 1]);
+                if (more) fetch(x4, next, 0);
+            }
             const int acc = j & 1;
             if (!wait_acc(acc)) break;
 #pragma unroll
             for (int sl = 0; sl < SL; ++sl) {
-                uint4 x4[8];
-                if (RELU && more) fetch(x4, next, sl);
 #pragma unroll
                 for (int hc = 0; hc < 2; ++hc) {
                     uint32_t v[32];
@@ -674,8 +685,12 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     if (line_in(cur, sl, i)) *reinterpret_cast<uint4*>(to + (long long)(4 * i) * row_stride) = v;
                 }
                 __syncwarp();
-                if (RELU && more) mask_of(x4, keep[sl]);
+                if (RELU && more && sl + 1 < SL) {
+                    mask_of(x4, first);
+                    fetch(x4, next, sl + 1);
+                }
             }
+            if (SL > 1) keep[0][0] = first[0], keep[0][1] = first[1];
             ++j;
         }
     }
@@ -775,10 +790,6 @@ struct LbPlan {
 // large384's layers.
 constexpr double kStepPair = 0.36, kStepOne = 0.27, kTail = 3.0, kSplitPerByte = 0.4e-6, kSumLaunch = 2.0;
 
-#ifndef LB_FORCE
-#define LB_FORCE(pair, s) true
-#endif
-
 LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw) {
     LbPlan pl = {};
     LbParams& p = pl.p;
@@ -802,7 +813,6 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
         const int kt = ceil_div(K, tile), nt = ceil_div(N, tile), tt = ceil_div(p.T, tile);
         const long long n_d = want_dx ? (long long)p.B * tt * kt : 0;
         for (int s = 1; s <= (want_dw ? 32 : 1) && s <= total; ++s) {
-            if (!LB_FORCE(ctas == 2, s)) continue;
             const long long n_w = want_dw ? (long long)nt * kt * s : 0;
             const int units = (int)(n_w + n_d < most_units ? n_w + n_d : most_units);
             const int heavy = (int)(n_w % units), light = heavy ? units - heavy : 0;
@@ -810,7 +820,8 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
             const int extra = light ? (int)(len / p.n_steps) : 0;
             const long long head = n_d < (long long)light * extra ? n_d : (long long)light * extra, rest = n_d - head;
             const double all = (double)(n_w / units) * len, turn = (double)((rest + units - 1) / units) * p.n_steps;
-            const double hi = all + (heavy ? len : 0.0) + (rest % units > light || !light ? turn : (double)(rest / units) * p.n_steps);
+            const double fewer = (double)(rest / units) * p.n_steps;
+            const double hi = all + (heavy ? len : 0.0) + (rest % units > light || !light ? turn : fewer);
             const double lo = all + (light ? (double)((head + light - 1) / light) * p.n_steps : 0.0) + turn;
             const double cost = (hi > lo ? hi : lo) * (ctas == 2 ? kStepPair : kStepOne) + kTail +
                                 (s > 1 ? kSumLaunch + s * (N * 4.0 * K) * kSplitPerByte : 0.0);
@@ -841,7 +852,8 @@ template <bool PAIR, bool RELU>
 cudaError_t lb_launch(const LbMaps& maps, const LbPlan& pl, cudaStream_t stream) {
     static PerDeviceOnce attrs;
     const cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(linear_bwd_kernel<PAIR, RELU>, cudaFuncAttributeMaxDynamicSharedMemorySize, lb::SMEM_BYTES);
+        return cudaFuncSetAttribute(linear_bwd_kernel<PAIR, RELU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    lb::SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
