@@ -45,15 +45,18 @@ namespace txl {
 
 namespace {
 
-// Blocks per CTA: a multiple of its 8 warps, one each where that already gives
-// every SM no more than a few CTAs (a small step is over when its longest CTA is),
-// more otherwise: fewer starts, and a prefetch that pays.  Measured at 226.7 M
-// elements of 8 bits: 64 blocks 776 us, 256 blocks 757 us; at 37.8 M of 32 bits, which
-// prefetch nothing: 64 blocks 199 us, 256 blocks 212 us.
+// Blocks per CTA: as many as make full rounds of the CTAs that are resident at once (a
+// last round with a few of them takes as long as a full one), with at most 256 blocks of
+// 8 bits, whose prefetch wants a long run, or 64 of 32 bits; a multiple of the 8 warps.
+// Measured at 226.7 M elements of 8 bits: at most 64 blocks 776 us, 256 blocks 757 us, in
+// full rounds 750 us; at 37.8 M of 32 bits, which prefetch nothing: 64 blocks 199 us, 256
+// blocks 212 us.
+constexpr int kCtas8 = 3, kCtas32 = 4;  // per SM
 unsigned blocks_per_cta(long long blocks, bool eight) {
-    unsigned per = 8;
-    while (per < (eight ? 256u : 64u) && blocks > 4ll * per * current_sm_count()) per *= 2;
-    return per;
+    const long long most = eight ? 256 : 64, resident = (long long)current_sm_count() * (eight ? kCtas8 : kCtas32);
+    const long long rounds = (blocks + resident * most - 1) / (resident * most);
+    const long long per = rounds ? (blocks + resident * rounds - 1) / (resident * rounds) : 1;
+    return (unsigned)((per + 7) / 8 * 8);
 }
 
 // What the update launch needs of this step, written by adamw_coef_kernel.
@@ -432,7 +435,7 @@ __device__ __forceinline__ void adamw_update(const AdamwRaw<P, G, EIGHT>& r, con
 // states a block takes longer to compute than to fetch, so the next one's loads
 // are issued before it.
 template <typename P, typename G, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(256, EIGHT ? 3 : 4)
+__global__ void __launch_bounds__(256, EIGHT ? kCtas8 : kCtas32)
 adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks, unsigned per, unsigned first, const AdamwFlat flat,
              float b1, float b1c, float b2, float b2c, float eps, const AdamwCoef* __restrict__ coef) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -553,7 +556,7 @@ long long adamw_blocks(const txl_adamw_tensor* tensors, int n_tensors) {
 // Coefficients, and one partial sum per CTA of each group of tensors (a group's
 // last CTA may be partly filled: one more per group at most).
 size_t adamw_workspace_bytes(long long blocks) {
-    return coef_bytes() + (size_t)(blocks / blocks_per_cta(blocks, false) + blocks / kSmallTable + 2) * sizeof(float);
+    return coef_bytes() + (size_t)(blocks / 8 + blocks / kSmallTable + 2) * sizeof(float);
 }
 
 cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream) {
