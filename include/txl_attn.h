@@ -15,8 +15,8 @@
  * Conventions shared by every entry point
  *   - All tensors are dense, contiguous, row-major, on the current CUDA
  *     device; every pointer argument is a DEVICE pointer unless the call says
- *     otherwise.  The caller owns
- *     every buffer; the library never allocates, frees or retains them.
+ *     otherwise.  The caller owns every buffer; the library never allocates,
+ *     frees or retains them.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream) and never synchronise the host, except
  *     txl_sync_status().
@@ -342,9 +342,10 @@ int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* 
 
 /*
  * LayerNorm for training: txl_layer_norm's forward that also keeps each row's
- * statistics, and its gradients.  Any row length 1 <= d <= 16384
- * and 0 <= rows < 2^31 (TXL_ERR_UNSUPPORTED beyond), dtype TXL_BF16 or TXL_F32 for x, y, gamma, beta, out, dout, dres and dx; statistics and
- * parameter gradients fp32.
+ * statistics, and its gradients.  Any row length 1 <= d <= 16384 and
+ * 0 <= rows < 2^31 (TXL_ERR_UNSUPPORTED beyond); dtype TXL_BF16 or TXL_F32 for
+ * x, y, gamma, beta, out, dout, dres and dx; statistics and parameter gradients
+ * fp32.
  *
  * txl_layer_norm_fwd: with z = x + y (y may be null),
  *   mean[r] = sum z / d, rstd[r] = (sum (z - mean)^2 / d + eps)^(-1/2),

@@ -354,3 +354,39 @@ def test_storage_given_away_stays_valid():
     opt.step()
     torch.cuda.synchronize()
     assert bool((p == 0).all()) and bool((fresh == 5).all())
+
+
+def test_constructor_stream_is_ordered_with_the_current_one():
+    """An optimizer with a stream of its own: it sees what the current stream wrote
+    before, and set_lr, state_dict and load_state_dict stand in the order of both."""
+    big = torch.empty(1 << 28, device="cuda")
+
+    def busy():
+        for _ in range(20):  # some 3 ms of the stream it is issued on
+            big.fill_(0.0)
+
+    n = 1 << 16
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.ones(n, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    p.fill_(2.0)
+    opt = txl.AdamW([p], [g], lr=0.0, stream=st)
+    start = opt.state_dict()
+    busy()
+    opt.set_lr(0.5)
+    opt.step()
+    with torch.cuda.stream(st):
+        busy()
+    opt.step()
+    sd = opt.state_dict()
+    assert bool((start["master"] == 2).all()) and int(start["steps"]) == 0
+    # constant gradients: m / (1 - b1^t) = 1 and v / (1 - b2^t) = 1, so each step takes off 0.5
+    # (1 + 1e-8 and four fp32 roundings of values up to 2 apart from that)
+    assert int(sd["steps"]) == 2 and float((sd["master"] - 1).abs().max()) <= 2 * (0.5 * 8 * 2.0 ** -24 + 2.0 ** -24 * 2)
+    busy()
+    opt.load_state_dict(start)
+    opt.step()
+    sd = opt.state_dict()
+    # (start's lr of 0 came back)
+    assert int(sd["steps"]) == 1 and bool((sd["master"] == 2).all())

@@ -148,3 +148,5 @@ def test_binding_refuses_what_it_can_see():
         txl.AdamW([x], [x], lr=1e-3, max_norm=0.0)
     with pytest.raises(ValueError, match="weight_decay"):
         txl.AdamW([x], [x], lr=1e-3, weight_decay=[0.1, 0.2])
+    with pytest.raises(TypeError, match="dtype"):
+        txl.layer_norm_bwd_workspace_bytes(4, 8, torch.float16, device=0)

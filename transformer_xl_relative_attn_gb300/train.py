@@ -29,6 +29,21 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+@contextlib.contextmanager
+def _between(stream, device):
+    """Torch operations on the current stream, in order with a call's ``stream``:
+    they see what it has done, and what it does next sees them."""
+    if stream is None:
+        yield
+        return
+    with _on(stream, device):
+        own = torch.cuda.current_stream(device)
+    here = torch.cuda.current_stream(device)
+    here.wait_stream(own)
+    yield
+    own.wait_stream(here)
+
+
 def _scratch(workspace, need: int, device) -> int:
     """Address of a caller's workspace (the C call checks its alignment)."""
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
@@ -96,7 +111,9 @@ def layer_norm_fwd(x, gamma, beta, y=None, eps=1e-5, out=None, mean=None, rstd=N
 def layer_norm_bwd_workspace_bytes(rows, d, dtype=torch.bfloat16, device=None) -> int:
     """txl_layer_norm_bwd_workspace_bytes for a call on ``device`` (default: the
     current one)."""
-    code = TXL_BF16 if dtype == torch.bfloat16 else TXL_F32
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
+    code = TXL_BF16 if dtype is torch.bfloat16 else TXL_F32
     dev = device if device is not None else torch.cuda.current_device()
     return int(_invoke(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, code))
 
@@ -226,11 +243,14 @@ class AdamW:
     fill.  Both are bound here, as a captured graph binds them: step() reads the
     gradients from this memory and updates the parameters in this memory, which
     the optimizer keeps alive (a tensor that is given other storage later, as by
-    ``p.data = ...``, is no longer the one that is stepped).  ``weight_decay``: one number, or one per
-    parameter.  ``max_norm``: gradients are scaled by min(1, max_norm / norm), norm
-    the 2-norm of all of them, kept in ``grad_norm`` [1]; a norm that is not finite
-    makes the step change nothing.  ``state_bits`` 8: the moments as e4m3 codes
-    with one scale per 256 elements, rounded at random from ``seed``.
+    ``p.data = ...``, is no longer the one that is stepped).  ``weight_decay``: one
+    number, or one per parameter.  ``max_norm``: gradients are scaled by
+    min(1, max_norm / norm), norm the 2-norm of all of them, kept in ``grad_norm``
+    [1]; a norm that is not finite makes the step change nothing.  ``state_bits`` 8:
+    the moments as e4m3 codes with one scale per 256 elements, rounded at random
+    from ``seed``.  ``stream``: the stream of the steps (default: the current one
+    of each call); what is enqueued on the current stream when the optimizer is made
+    is waited for.
 
     Device values: ``lr`` [1] fp32 (set_lr), ``steps`` [1] int64 (steps done), the
     flat ``master`` (None for fp32 parameters) and states(); parameter i's part of
@@ -274,7 +294,10 @@ class AdamW:
             raise TxlError(-1, "txl_adamw_state_elements")
         need = int(_invoke(dev, "txl_adamw_workspace_bytes", self._table, n))
         f32 = dict(dtype=torch.float32, device=dev)
+        here = torch.cuda.current_stream(dev)
         with _on(stream, dev):
+            if stream is not None:
+                torch.cuda.current_stream(dev).wait_stream(here)  # what is still writing the parameters
             self.lr = torch.full((1,), float(lr), **f32)
             self.steps = torch.zeros(1, dtype=torch.int64, device=dev)
             self.grad_norm = torch.zeros(1, **f32) if max_norm is not None else None
@@ -295,8 +318,9 @@ class AdamW:
                       float(max_norm or 0.0), self.seed, _ptr(self.grad_norm), self._workspace.data_ptr(), need)
 
     def _copy_masters(self) -> None:
-        for p, a in zip(self.params, self.starts):
-            self.master[a:a + p.numel()].copy_(p.reshape(-1))
+        with torch.no_grad():
+            for p, a in zip(self.params, self.starts):
+                self.master[a:a + p.numel()].copy_(p.reshape(-1))
 
     def step(self, stream=None) -> None:
         """One step from the gradients as they stand, on ``stream`` (default:
@@ -307,8 +331,10 @@ class AdamW:
             raise TxlError(rc, "txl_adamw_step")
 
     def set_lr(self, lr: float) -> None:
-        """Learning rate of the steps that follow on the current stream."""
-        self.lr.fill_(float(lr))
+        """Learning rate of the steps that follow (in the order of the current
+        stream, and of the constructor's if it was given one)."""
+        with _between(self._fixed_stream, self.device):
+            self.lr.fill_(float(lr))
 
     def states(self) -> list:
         """The flat moments: [exp_avg, exp_avg_sq] in fp32, or with 8 bits
@@ -320,19 +346,24 @@ class AdamW:
     def state_dict(self) -> dict:
         """Step count, moments and master copy (checkpoint/resume; the
         parameters are the caller's)."""
-        return {"steps": self.steps.clone(), "lr": self.lr.clone(), "states": [s.clone() for s in self.states()],
-                "master": None if self.master is None else self.master.clone()}
+        with _between(self._fixed_stream, self.device):
+            return {"steps": self.steps.clone(), "lr": self.lr.clone(), "states": [s.clone() for s in self.states()],
+                    "master": None if self.master is None else self.master.clone()}
 
     def load_state_dict(self, sd: dict) -> None:
         """Restores state_dict's values.  bf16 parameters are set to the
         rounding of the restored master copy."""
         if len(sd["states"]) != len(self.states()) or (sd["master"] is None) != (self.master is None):
             raise ValueError("state of another state_bits or parameter type")
-        for mine, given in zip(self.states() + [self.steps, self.lr], list(sd["states"]) + [sd["steps"], sd["lr"]]):
-            if mine.shape != given.shape:
-                raise ValueError(f"state has shape {tuple(given.shape)}, expected {tuple(mine.shape)}")
-            mine.copy_(given)
+        pairs = list(zip(self.states() + [self.steps, self.lr], list(sd["states"]) + [sd["steps"], sd["lr"]]))
         if self.master is not None:
-            self.master.copy_(sd["master"])
-            for p, a in zip(self.params, self.starts):
-                p.copy_(self.master[a:a + p.numel()].view(p.shape))
+            pairs.append((self.master, sd["master"]))
+        for mine, given in pairs:
+            if mine.shape != given.shape or mine.dtype != given.dtype:
+                raise ValueError(f"state is {given.dtype} {tuple(given.shape)}, expected {mine.dtype} {tuple(mine.shape)}")
+        with torch.no_grad(), _between(self._fixed_stream, self.device):
+            for mine, given in pairs:
+                mine.copy_(given)
+            if self.master is not None:
+                for p, a in zip(self.params, self.starts):
+                    p.copy_(self.master[a:a + p.numel()].view(p.shape))
