@@ -24,6 +24,8 @@
 // adds to an accumulator (1.7e-8 of the result per MMA on random data, measured), so
 // a dw accumulator takes 1024 rows at a time and the epilogue adds these in registers:
 // at 6144 rows the error went from 3.3e-6 to 1.0e-6 (an fp32 library product's: 0.8e-6).
+// dx, which is rounded to bf16, takes its whole reduction in one accumulator (2048
+// columns: 2e-6 against the rounding's 2e-3).
 //
 // TMA is what the loads need all of: an instruction costs its issuing thread some
 // 100 cycles whatever it loads, so a stage of 32 KB is two instructions where the widths
@@ -37,6 +39,7 @@
 // let an epilogue overlap the next tile's MMAs.  Every wait is bounded (1 s) and
 // reports through the device status word.  Rows, N and K need not fill tiles: TMA
 // fills with zeros behind the ends.
+#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -817,7 +820,8 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
             const int units = (int)(n_w + n_d < most_units ? n_w + n_d : most_units);
             const int heavy = (int)(n_w % units), light = heavy ? units - heavy : 0;
             const double len = (double)total / s;  // stages of a dw item
-            const int extra = light ? (int)(len / p.n_steps) : 0;
+            // (no more than there are: light * extra stays an int)
+            const int extra = light ? (int)std::min(len / p.n_steps, (double)(n_d / light + 1)) : 0;
             const long long head = n_d < (long long)light * extra ? n_d : (long long)light * extra, rest = n_d - head;
             const double all = (double)(n_w / units) * len, turn = (double)((rest + units - 1) / units) * p.n_steps;
             const double fewer = (double)(rest / units) * p.n_steps;
