@@ -360,7 +360,8 @@ int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* 
  * row data are not looked at).  Outputs overlap neither inputs nor each other
  * (TXL_ERR_ALIAS).  workspace: device memory, 256-byte aligned, at least
  * txl_layer_norm_bwd_workspace_bytes(...) bytes (TXL_ERR_WORKSPACE), overlapping
- * no other argument (TXL_ERR_ALIAS); concurrent calls use distinct ones.
+ * no other argument (TXL_ERR_ALIAS); concurrent calls use distinct ones.  0 bytes:
+ * none needed, not touched.
  */
 int txl_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
                        int d, float eps, void* out, float* mean, float* rstd, int dtype, void* stream);
@@ -386,7 +387,7 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
  * 2^30 output tiles of 128 x 128).  Pointers 16-byte aligned
  * (TXL_ERR_MISALIGNED); outputs overlap neither inputs nor each other
  * (TXL_ERR_ALIAS).  workspace as for txl_layer_norm_bwd, of
- * txl_linear_bwd_workspace_bytes(...) bytes (0: none needed, not touched).
+ * txl_linear_bwd_workspace_bytes(...) bytes.
  */
 size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
                                       int want_db);

@@ -100,6 +100,21 @@ def test_forward_and_backward_match_fp64(rows, d, dtype, add):
     check_backward(t, mean, rstd, dres=not add)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 512), (BF, 1000), (BF, 2048), (BF, 514), (BF, 77), (BF, 1539),
+                                     (F32, 512), (F32, 1100), (F32, 33), (F32, 2049)])
+def test_backward_with_few_rows_and_with_one_more(dtype, d):
+    """Up to some number of rows no workspace is needed (the columns are summed by
+    CTAs of their own); both sides of it."""
+    few = max(r for r in range(1, 1 << 13) if txl.layer_norm_bwd_workspace_bytes(r, d, dtype) == 0)
+    assert txl.layer_norm_bwd_workspace_bytes(few + 1, d, dtype) > 0
+    for rows in (few, few + 1):
+        t = make(rows, d, dtype, True, seed=rows + d)
+        _, mean, rstd = check_forward(t)
+        got = check_backward(t, mean, rstd, dres=True)
+        again = check_backward(t, mean, rstd, dres=True)
+        assert all(torch.equal(got[k], again[k]) for k in got)
+
+
 def test_many_rows_and_a_leading_shape():
     t = make(0, 512, BF, True, seed=5, lead=(3, 700))
     out, mean, rstd = check_forward(t)

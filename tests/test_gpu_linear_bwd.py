@@ -74,6 +74,10 @@ def check(dy, x, w, relu, got, want=("dx", "dw", "db")):
     (4, 384, 1024, 1024, True, False),  # o_net of large384
     (1, 20000, 128, 128, False, False),  # a long reduction over few tiles
     (7, 1, 192, 64, True, False),       # single tokens in the heads layout
+    (1, 1024, 64, 4104, False, False),  # db without parts and with, and the last columns of a warp
+    (1, 1025, 64, 4104, False, False),
+    (2, 1024, 512, 2056, False, True),
+    (1, 2049, 512, 2056, False, True),
 ])
 def test_gradients_match_fp64(B, T, K, N, heads, relu):
     dy, x, w = make(B, T, K, N, heads, relu, seed=B * T + K + N)

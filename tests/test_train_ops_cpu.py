@@ -40,10 +40,10 @@ def test_layer_norm_fwd_rejects_bad_arguments(lib):
 
 
 def test_layer_norm_bwd_rejects_bad_arguments(lib):
-    need = lib.txl_layer_norm_bwd_workspace_bytes(64, 500, BF)
+    need = lib.txl_layer_norm_bwd_workspace_bytes(2000, 500, BF)
     assert need > 0
 
-    def call(dout=addr(0), x=addr(1), y=0, gamma=addr(2), mean=addr(3), rstd=addr(4), dres=0, rows=64, d=500,
+    def call(dout=addr(0), x=addr(1), y=0, gamma=addr(2), mean=addr(3), rstd=addr(4), dres=0, rows=2000, d=500,
              dx=addr(5), dgamma=addr(6), dbeta=addr(7), dtype=BF, ws=addr(8), ws_bytes=need):
         return lib.txl_layer_norm_bwd(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, dtype, ws,
                                       ws_bytes, None)

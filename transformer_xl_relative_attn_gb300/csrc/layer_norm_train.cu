@@ -19,7 +19,9 @@
 // The backward pass is persistent: each thread keeps its columns' sums of dout xh
 // and dout in registers over all rows of its CTA, so dgamma and dbeta cost no
 // second pass over the rows; the CTAs' sums go to the workspace and a second
-// launch adds them, in a fixed order (the same inputs give the same bits).
+// launch adds them, in a fixed order (the same inputs give the same bits).  With
+// few rows other CTAs of the same launch read the rows again for these sums, column
+// by column, and there is neither second launch nor workspace.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,6 +81,20 @@ struct Vec<__nv_bfloat16, 1> {
     static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) { f[0] = __bfloat162float(*p); }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) { *p = __float2bfloat16_rn(f[0]); }
 };
+
+// V sums, 16 bytes at a time where V allows it (one by one, V apart between lanes, they cost
+// a CTA of 4096 columns 9 us).
+template <int V>
+__device__ __forceinline__ void store_sums(float* p, const float* f) {
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) Vec<float, 4>::store(p + 4 * i, f + 4 * i);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    } else {
+        *p = f[0];
+    }
+}
 
 // Two fp32 operations per instruction: the rows' arithmetic, not memory, bounded these
 // kernels one element at a time (forward, bf16: 18 instructions per element, 68 % of the
@@ -231,17 +247,95 @@ constexpr int bwd_ctas() {
     return Shape<W>::THREADS > 256 ? 1 : (E <= 8 ? 3 : 2);
 }
 
-template <typename T, int V, int E, int W>
+// dgamma and dbeta of a few columns by one CTA: CL lanes of V columns side by side, at least
+// 32 bytes of a row, and as many threads below one another as the CTA has.
+template <typename T, int V, int W>
+struct Columns {
+    static constexpr int THREADS = Shape<W>::THREADS;
+    static constexpr int SECTOR = 32 / (int)sizeof(T) / V;
+    static constexpr int CL = SECTOR > THREADS / 128 ? SECTOR : THREADS / 128;
+    static constexpr int C = CL * V;           // columns of a CTA
+    static constexpr int RG = THREADS / CL;    // rows at a time
+    // Rows up to which this is done: 8 per thread, 16 of narrow vectors.  Bf16 with y, once
+    // against sums in the row CTAs and a second launch: 128 x 512 2.2 and 4.2 us, 1024 x 512
+    // 4.0 and 5.1, 2048 x 512 8.2 and 5.5; 512 x 500 3.4 and 5.1, 1024 x 500 5.5 and 5.1;
+    // 128 x 4096 3.3 and 13.2.
+    static constexpr int ROWS = (V >= 4 ? 8 : 16) * RG;
+};
+
+template <typename T, int V, int W>
+__device__ __forceinline__ void ln_bwd_columns(const T* __restrict__ dout, const T* __restrict__ x,
+                                               const T* __restrict__ y, const float* __restrict__ mean,
+                                               const float* __restrict__ rstd, int rows, int d, int cta, float* sh,
+                                               float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    using S = Columns<T, V, W>;
+    const int cl = threadIdx.x % S::CL, c = cta * S::C + cl * V;
+    float dg[V], db[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) dg[k] = db[k] = 0.f;
+    if (c < d && TXL_BOUNDS(c + V <= d, 904, c)) {
+#pragma unroll 2
+        for (int r = threadIdx.x / S::CL; r < rows; r += S::RG) {
+            const long long at = (long long)r * d + c;
+            const float mu = mean[r], rs = rstd[r];
+            alignas(8) float z[V], g[V];
+            Vec<T, V>::load(x + at, z);
+            Vec<T, V>::load(dout + at, g);
+            if (y) {
+                alignas(8) float b[V];
+                Vec<T, V>::load(y + at, b);
+#pragma unroll
+                for (int k = 0; k < V; ++k) z[k] += b[k];
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                dg[k] = fmaf(g[k], (z[k] - mu) * rs, dg[k]);
+                db[k] += g[k];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int o = S::CL; o < 32; o <<= 1) {
+            dg[k] += __shfl_xor_sync(0xffffffffu, dg[k], o);
+            db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+        }
+    }
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) < S::CL) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            sh[warp * 2 * S::C + cl * V + k] = dg[k];
+            sh[warp * 2 * S::C + S::C + cl * V + k] = db[k];
+        }
+    }
+    __syncthreads();
+    const int i = threadIdx.x, col = cta * S::C + i % S::C;
+    if (i >= 2 * S::C || col >= d) return;
+    float a = 0.f;
+#pragma unroll
+    for (int w = 0; w < S::THREADS / 32; ++w) a += sh[w * 2 * S::C + i];
+    (i < S::C ? dgamma : dbeta)[col] = a;
+}
+
+// FEW: CTAs from row_ctas on take columns, and part is not used.
+template <typename T, int V, int E, int W, bool FEW>
 __global__ void __launch_bounds__(Shape<W>::THREADS, bwd_ctas<E, W>())
 ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __restrict__ y,
               const T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
               const T* __restrict__ dres, long long rows, int d, float inv_d, T* __restrict__ dx,
-              float* __restrict__ part) {
+              int row_ctas, float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta) {
     using S = Shape<W>;
+    using Col = Columns<T, V, W>;
     __shared__ float2 sh[2 * S::THREADS / 32];
-    __shared__ float fold[S::R > 1 ? S::THREADS / 2 * 2 * E : 1];
+    __shared__ float fold[FEW ? S::THREADS / 32 * 2 * Col::C : S::R > 1 ? S::THREADS / 2 * 2 * E : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (FEW && (int)blockIdx.x >= row_ctas) {
+        ln_bwd_columns<T, V, W>(dout, x, y, mean, rstd, (int)rows, d, (int)blockIdx.x - row_ctas, fold, dgamma, dbeta);
+        return;
+    }
     const int t = threadIdx.x % S::TPR, lr = threadIdx.x / S::TPR;
     alignas(8) float dg[E], db[E], gam[E];
     const int left = d - t * V;
@@ -250,7 +344,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
     int phase = 0;
     // where this thread's elements of its rows lie, row after row
-    const long long first = (long long)blockIdx.x * S::R + lr, step = (long long)gridDim.x * S::R, hop = step * d;
+    const long long first = (long long)blockIdx.x * S::R + lr, step = (long long)row_ctas * S::R, hop = step * d;
     long long at = first * d + t * V;
     int todo = (int)(rows > (long long)blockIdx.x * S::R ? (rows - (long long)blockIdx.x * S::R + step - 1) / step : 0);
     const float *mp = mean + first, *rp = rstd + first;
@@ -279,8 +373,10 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 float2& h = pair(xh, e);
                 float2& q = pair(g, e);
                 h = __fmul2_rn(__fadd2_rn(h, both(-mu)), both(rs));
-                pair(dg, e) = __ffma2_rn(q, h, pair(dg, e));
-                pair(db, e) = __fadd2_rn(pair(db, e), q);
+                if (!FEW) {
+                    pair(dg, e) = __ffma2_rn(q, h, pair(dg, e));
+                    pair(db, e) = __fadd2_rn(pair(db, e), q);
+                }
                 q = __fmul2_rn(q, pair(gam, e));
                 s1 = __fadd2_rn(s1, q);
                 s2 = __ffma2_rn(q, h, s2);
@@ -309,6 +405,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
             if (OFF * i < left && TXL_BOUNDS(OFF * i + V <= left, 903, at)) Vec<T, V>::store(dx + at + OFF * i, g + V * i);
         }
     }
+    if (FEW) return;
     // the CTA's rows fold in halves, into the first row's threads
     if (S::R > 1) {
 #pragma unroll
@@ -335,11 +432,11 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     if (lr > 0) return;
     float* to = part + (size_t)blockIdx.x * 2 * d;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int c = (t + S::TPR * (e / V)) * V + e % V;
+    for (int i = 0; i < E / V; ++i) {
+        const int c = (t + S::TPR * i) * V;
         if (c < d) {
-            to[c] = dg[e];
-            to[d + c] = db[e];
+            store_sums<V>(to + c, dg + V * i);
+            store_sums<V>(to + d + c, db + V * i);
         }
     }
 }
@@ -413,16 +510,39 @@ cudaError_t pick_bwd(int d, F f) {
     return f(Pick<16, 32>());
 }
 
-// CTAs of the backward pass: one round of resident ones at most.
-int bwd_grid(long long rows, int d) {
-    int per_sm = 1, r = 1;
+// Calls f with the vector length of rows of d elements.
+template <int V>
+struct Width {
+    static constexpr int v = V;
+};
+template <typename T, typename F>
+auto pick_width(int d, F f) {
+    if constexpr (sizeof(T) == 2)
+        return d % 2 ? f(Width<1>()) : d % 8 ? f(Width<2>()) : f(Width<8>());
+    else
+        return d % 4 ? f(Width<1>()) : f(Width<4>());
+}
+
+// How the backward pass is launched: CTAs that take rows (one round of resident ones at
+// most), and CTAs that take columns (0: the row CTAs sum them, into as many parts).
+struct BwdGrid {
+    int rows, columns;
+};
+template <typename T>
+BwdGrid bwd_grid(long long rows, int d) {
+    BwdGrid g = {};
     pick_bwd(d, [&](auto k) {
-        per_sm = bwd_ctas<decltype(k)::e, decltype(k)::w>();
-        r = Shape<decltype(k)::w>::R;
+        constexpr int E = decltype(k)::e, W = decltype(k)::w, R = Shape<W>::R;
+        const long long want = (rows + R - 1) / R, most = (long long)bwd_ctas<E, W>() * current_sm_count();
+        g.rows = (int)(want < 1 ? 1 : (want < most ? want : most));
+        pick_width<T>(d, [&](auto v) {
+            using C = Columns<T, decltype(v)::v, W>;
+            if (rows <= C::ROWS) g.columns = (d + C::C - 1) / C::C;
+            return 0;
+        });
         return cudaSuccess;
     });
-    const long long want = (rows + r - 1) / r, most = (long long)per_sm * current_sm_count();
-    return (int)(want < 1 ? 1 : (want < most ? want : most));
+    return g;
 }
 
 template <typename T, int V>
@@ -443,17 +563,20 @@ template <typename T, int V>
 cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
                    const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
                    float* dbeta, float* part, cudaStream_t stream) {
-    // (no rows: one CTA that adds nothing writes the zeros to be summed)
-    const int grid = bwd_grid(rows, d);
+    // (no rows: CTAs that add nothing write the zeros)
+    const BwdGrid grid = bwd_grid<T>(rows, d);
     const cudaError_t e = pick_bwd(d, [&](auto k) {
         constexpr int E = decltype(k)::e, W = decltype(k)::w;
-        return launch_pdl(ln_bwd_kernel<T, V, E, W>, (unsigned)grid, (unsigned)Shape<W>::THREADS, stream,
-                          static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
-                          static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d, 1.f / d,
-                          static_cast<T*>(dx), part);
+        auto go = [&](auto kern) {
+            return launch_pdl(kern, (unsigned)(grid.rows + grid.columns), (unsigned)Shape<W>::THREADS, stream,
+                              static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
+                              static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d, 1.f / d,
+                              static_cast<T*>(dx), grid.rows, part, dgamma, dbeta);
+        };
+        return grid.columns ? go(ln_bwd_kernel<T, V, E, W, true>) : go(ln_bwd_kernel<T, V, E, W, false>);
     });
-    if (e != cudaSuccess) return e;
-    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, stream, part, grid, d, dgamma, dbeta);
+    if (e != cudaSuccess || grid.columns) return e;
+    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, stream, part, grid.rows, d, dgamma, dbeta);
 }
 
 }  // namespace
@@ -461,27 +584,32 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
 cudaError_t launch_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta, long long rows,
                                   int d, float eps, void* out, float* mean, float* rstd, int bf16,
                                   cudaStream_t stream) {
-    if (bf16)
-        return (d % 2   ? ln_fwd<__nv_bfloat16, 1>
-                : d % 8 ? ln_fwd<__nv_bfloat16, 2>
-                        : ln_fwd<__nv_bfloat16, 8>)(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream);
-    return (d % 4 ? ln_fwd<float, 1> : ln_fwd<float, 4>)(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream);
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        return pick_width<T>(d, [&](auto v) {
+            return ln_fwd<T, decltype(v)::v>(x, y, gamma, beta, rows, d, eps, out, mean, rstd, stream);
+        });
+    };
+    return bf16 ? go(__nv_bfloat16()) : go(float());
 }
 
-size_t layer_norm_bwd_workspace_bytes(long long rows, int d) { return (size_t)bwd_grid(rows, d) * 2 * d * sizeof(float); }
+size_t layer_norm_bwd_workspace_bytes(long long rows, int d, int bf16) {
+    const BwdGrid g = bf16 ? bwd_grid<__nv_bfloat16>(rows, d) : bwd_grid<float>(rows, d);
+    return g.columns ? 0 : (size_t)g.rows * 2 * d * sizeof(float);
+}
 
 cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
                                   const float* mean, const float* rstd, const void* dres, long long rows, int d,
                                   void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
                                   cudaStream_t stream) {
     float* part = static_cast<float*>(workspace);
-    if (bf16)
-        return (d % 2   ? ln_bwd<__nv_bfloat16, 1>
-                : d % 8 ? ln_bwd<__nv_bfloat16, 2>
-                        : ln_bwd<__nv_bfloat16, 8>)(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part,
-                                                    stream);
-    return (d % 4 ? ln_bwd<float, 1> : ln_bwd<float, 4>)(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta,
-                                                        part, stream);
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        return pick_width<T>(d, [&](auto v) {
+            return ln_bwd<T, decltype(v)::v>(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part, stream);
+        });
+    };
+    return bf16 ? go(__nv_bfloat16()) : go(float());
 }
 
 TXL_BOUNDS_READER(bounds_word_layer_norm_train)

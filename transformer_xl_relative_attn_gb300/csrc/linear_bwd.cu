@@ -81,26 +81,6 @@ struct Cfg {
 };
 }  // namespace lb
 
-struct LbParams {
-    int T, B;       // rows per batch row, batch rows (rows layout: all rows, 1)
-    int K, N;
-    int heads;      // x and dx are [B, K / 64, T, 64]
-    int n_kt, n_nt, n_tt;  // tiles along K, N and T (per batch row)
-    int t_steps;           // 64-row steps per batch row
-    int n_steps;           // 64-column steps of N
-    int splits;            // of dw's reduction
-    int n_w, n_d;          // dw items (tiles * splits), dx tiles
-    int heavy, extra;      // see LbSchedule
-    int k64, n64;          // K, N are multiples of 64: boxes of several slices
-    int db_rows;           // parts of db (row ranges); 0: no db
-    const __nv_bfloat16* x;
-    const __nv_bfloat16* dy;
-    __nv_bfloat16* dx;
-    float* dw;             // [splits, N, K]
-    float* db;             // [db_rows, N]
-    int* status;
-};
-
 struct LbMaps {
     CUtensorMap dy;   // (column, row, batch row), boxes of 64 x 128: dx's first operand
     CUtensorMap dyc;  // dw's: (element, row, 64-column slice, batch row), boxes of two slices of 64 rows;
@@ -321,6 +301,22 @@ __device__ __forceinline__ uint4 lb_ld_shared_v4(uint32_t addr) {
     return v;
 }
 
+// Eight bf16 onto eight sums; eight sums to memory.
+__device__ __forceinline__ void lb_add8(float (&a)[8], const uint4& v) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __bfloat1622float2(h[e]);
+        a[2 * e] += f.x;
+        a[2 * e + 1] += f.y;
+    }
+}
+__device__ __forceinline__ void lb_put8(float* p, const float (&a)[8]) {
+    float4* to = reinterpret_cast<float4*>(p);
+    to[0] = make_float4(a[0], a[1], a[2], a[3]);
+    to[1] = make_float4(a[4], a[5], a[6], a[7]);
+}
+
 }  // namespace
 
 template <bool PAIR, bool RELU>
@@ -478,7 +474,8 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
             __syncwarp();
         } else {
             // ---------------------------------------------------- column sums of dy
-            // A warp adds 256 columns (8 per lane) over one of db_rows ranges of rows.
+            // Many rows: a warp adds 256 columns (8 per lane) over one of db_rows ranges of rows.
+            // Few: 16 columns over all of them, 16 lanes on a column, with nothing left to add.
             if (p.db_rows) {
                 const int groups = (p.N + 255) >> 8;
                 const long long rows = (long long)p.B * p.T;
@@ -491,17 +488,31 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     for (long long r = r0; r < r1; ++r) {
                         if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
                         const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.dy + r * p.N + n));
-                        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = __bfloat1622float2(h[e]);
-                            a[2 * e] += f.x;
-                            a[2 * e + 1] += f.y;
-                        }
+                        lb_add8(a, v);
                     }
-                    float4* to = reinterpret_cast<float4*>(p.db + (size_t)part * p.N + n);
-                    to[0] = make_float4(a[0], a[1], a[2], a[3]);
-                    to[1] = make_float4(a[4], a[5], a[6], a[7]);
+                    lb_put8(p.db + (size_t)part * p.N + n, a);
+                }
+            } else if (p.db) {
+                const int rows = p.B * p.T;
+                for (int u = blockIdx.x * 2 + warp - 2; u * 16 < p.N; u += 2 * gridDim.x) {
+                    const int n = u * 16 + (lane & 1) * 8, end = n < p.N ? rows : 0;
+                    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int r = lane >> 1; r < end; r += 16 * 8) {  // 8 rows on their way at a time
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = r + 16 * i < end && TXL_BOUNDS(n + 8 <= p.N, 804, n)
+                                       ? __ldg(reinterpret_cast<const uint4*>(p.dy + (long long)(r + 16 * i) * p.N + n))
+                                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) lb_add8(a, v[i]);
+                    }
+#pragma unroll
+                    for (int o = 2; o < 32; o <<= 1)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
+                    if (lane < 2 && n < p.N) lb_put8(p.db + n, a);
                 }
             }
         }
@@ -780,20 +791,21 @@ bool lb_encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// How the call is cut: pairs or single CTAs, splits of dw's reduction, schedule.
-struct LbPlan {
-    bool pair;
-    int grid;
-    LbParams p;
-};
-
 // Microseconds that a stage takes a pair or a CTA, that a dx tile's and a dw item's end
 // add to the last of a unit, that the parts of one more split cost per byte of dw (write
 // and read, through L2), and that the second launch costs; measured on base512's and
 // large384's layers.
 constexpr double kStepPair = 0.36, kStepOne = 0.27, kTail = 3.0, kSplitPerByte = 0.4e-6, kSumLaunch = 2.0;
 
-LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw) {
+// Up to this many rows db is summed without parts, which is what a second launch would be
+// for where dw has none (512 -> 2048, 1024 rows: 10.1 us against 11.3, 2048 rows 11.5 against
+// 13.3, 4096 rows 23.3 against 19.4), or has one for dw's anyway (512 -> 512, 1536 rows: 10.0
+// us against 8.8).
+constexpr long long kDbOnce = 2048, kDbOnceSplit = 1024;
+
+}  // namespace
+
+LbPlan linear_bwd_plan(int heads, int B, int T, int K, int N, bool want_dx, bool want_dw) {
     LbPlan pl = {};
     LbParams& p = pl.p;
     p.T = heads ? T : B * T;
@@ -843,14 +855,13 @@ LbPlan lb_plan(int B, int T, int K, int N, int heads, bool want_dx, bool want_dw
             p.extra = extra;
         }
     }
-    // row ranges of db: as many as give each of the two summing warps per CTA one, of 16
-    // rows at least
+    // row ranges of db: as many as give each of the two summing warps per CTA one
     const long long rows = (long long)B * T, groups = (N + 255) / 256;
-    long long parts = 2ll * pl.grid / groups;
-    if (parts > rows / 16) parts = rows / 16;
-    p.db_rows = parts < 1 ? 1 : (int)parts;
+    p.db_rows = rows <= (p.splits > 1 ? kDbOnceSplit : kDbOnce) ? 0 : (int)std::max(1ll, std::min(2ll * pl.grid / groups, rows / 16));
     return pl;
 }
+
+namespace {
 
 template <bool PAIR, bool RELU>
 cudaError_t lb_launch(const LbMaps& maps, const LbPlan& pl, cudaStream_t stream) {
@@ -899,17 +910,14 @@ cudaError_t lb_sum(const float* part, float* dw, int splits, const float* db_par
 
 }  // namespace
 
-size_t linear_bwd_workspace_bytes(int heads, int B, int T, int K, int N, bool want_dx, bool want_dw, bool want_db) {
-    if (!want_dw) return 0;
-    const LbPlan pl = lb_plan(B, T, K, N, heads, want_dx, true);
-    return part_bytes(pl) + (want_db ? (size_t)pl.p.db_rows * N * 4 : 0);
+size_t linear_bwd_workspace_bytes(const LbPlan& pl, bool want_db) {
+    return part_bytes(pl) + (want_db ? (size_t)pl.p.db_rows * pl.p.N * 4 : 0);
 }
 
-cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, int T, int K, const void* w, int N,
-                              int relu, void* dx, float* dw, float* db, void* workspace, int* status,
-                              cudaStream_t stream) {
-    LbPlan pl = lb_plan(B, T, K, N, heads, dx != nullptr, dw != nullptr);
+cudaError_t launch_linear_bwd(LbPlan pl, const void* dy, const void* x, const void* w, int relu, void* dx, float* dw,
+                              float* db, void* workspace, int* status, cudaStream_t stream) {
     LbParams& p = pl.p;
+    const int K = p.K, N = p.N, heads = p.heads;
     p.x = static_cast<const __nv_bfloat16*>(x);
     p.dy = static_cast<const __nv_bfloat16*>(dy);
     p.dx = static_cast<__nv_bfloat16*>(dx);
@@ -918,7 +926,7 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, i
     const bool split = p.splits > 1;
     float* part = split ? static_cast<float*>(workspace) : dw;
     p.dw = part;
-    p.db = db ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(pl)) : nullptr;
+    p.db = p.db_rows ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(pl)) : db;
     LbMaps maps;
     const cuuint64_t Tt = p.T, Bb = p.B, Kk = K, Nn = N;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -951,8 +959,8 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, int heads, int B, i
     }
     const cudaError_t e = pl.pair ? (relu ? lb_launch<true, true> : lb_launch<true, false>)(maps, pl, stream)
                                   : (relu ? lb_launch<false, true> : lb_launch<false, false>)(maps, pl, stream);
-    if (e != cudaSuccess || (!split && !db)) return e;
-    return lb_sum(part, dw, p.splits, p.db, db, N, K, p.db_rows, stream);
+    if (e != cudaSuccess || (!split && !p.db_rows)) return e;
+    return lb_sum(part, dw, p.splits, p.db, p.db_rows ? db : nullptr, N, K, p.db_rows, stream);
 }
 
 TXL_BOUNDS_READER(bounds_word_linear_bwd)

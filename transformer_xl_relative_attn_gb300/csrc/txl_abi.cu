@@ -35,7 +35,7 @@ cudaError_t launch_layer_norm(const void* x, const void* y, const void* gamma, c
 cudaError_t launch_layer_norm_fwd(const void* x, const void* y, const void* gamma, const void* beta,
                                   long long rows, int d, float eps, void* out, float* mean, float* rstd,
                                   int bf16, cudaStream_t stream);
-size_t layer_norm_bwd_workspace_bytes(long long rows, int d);
+size_t layer_norm_bwd_workspace_bytes(long long rows, int d, int bf16);
 cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
                                   const float* mean, const float* rstd, const void* dres, long long rows,
                                   int d, void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
@@ -707,7 +707,7 @@ int txl_layer_norm_fwd(const void* x, const void* y, const void* gamma, const vo
 
 size_t txl_layer_norm_bwd_workspace_bytes(long long rows, int d, int dtype) {
     if (!elem_size(dtype) || rows < 0 || d <= 0 || d > kLayerNormMaxD || row_data_too_large(rows, d)) return 0;
-    return txl::layer_norm_bwd_workspace_bytes(rows, d);
+    return txl::layer_norm_bwd_workspace_bytes(rows, d, dtype == TXL_BF16);
 }
 
 int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
@@ -736,8 +736,8 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
 size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
                                       int want_db) {
     if (linear_bwd_sizes(x_layout, B, T, K, N) != TXL_OK) return 0;
-    return txl::linear_bwd_workspace_bytes(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0,
-                                           want_db != 0);
+    return txl::linear_bwd_workspace_bytes(
+        txl::linear_bwd_plan(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0), want_dw && want_db);
 }
 
 int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, int K, const void* w, int N,
@@ -747,8 +747,9 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
     if (rc != TXL_OK) return rc;
     for (const void* p : {dy, x, w, (const void*)dx, (const void*)dw, (const void*)db})
         if (!aligned16(p)) return TXL_ERR_MISALIGNED;
-    const size_t need = txl_linear_bwd_workspace_bytes(x_layout, B, T, K, N, dx != nullptr, dw != nullptr,
-                                                       db != nullptr);
+    const txl::LbPlan plan =
+        txl::linear_bwd_plan(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, dx != nullptr, dw != nullptr);
+    const size_t need = txl::linear_bwd_workspace_bytes(plan, db != nullptr);
     if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
     const size_t rows = (size_t)B * T, nx = rows * K * 2, nw = (size_t)N * K;
     Range r[] = {range_of(dy, rows * N * 2, false),     range_of(x, nx, false),
@@ -758,8 +759,8 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
     if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
     int* status = dev_status_ptr();
     if (!status) return TXL_ERR_CUDA;
-    return launch_status(txl::launch_linear_bwd(dy, x, x_layout == TXL_LAYOUT_HEADS, B, T, K, w, N, relu_in != 0, dx,
-                                                dw, db, workspace, status, static_cast<cudaStream_t>(stream)));
+    return launch_status(txl::launch_linear_bwd(plan, dy, x, w, relu_in != 0, dx, dw, db, workspace, status,
+                                                static_cast<cudaStream_t>(stream)));
 }
 
 long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors) {

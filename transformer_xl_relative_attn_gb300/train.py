@@ -145,11 +145,13 @@ def layer_norm_bwd(dout, x, gamma, mean, rstd, y=None, dres=None, stream=None, w
             _need(dx, "dx", shape, dt, dev)
             _need(dgamma, "dgamma", (d,), f32, dev)
             _need(dbeta, "dbeta", (d,), f32, dev)
-        if workspace is None:
+        if workspace is not None:
+            at = _scratch(workspace, need, dev)
+        elif need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             at = workspace.data_ptr()
         else:
-            at = _scratch(workspace, need, dev)
+            at = 0
     rc = _invoke(dev, "txl_layer_norm_bwd", dout.data_ptr(), x.data_ptr(), _ptr(y), gamma.data_ptr(),
                  mean.data_ptr(), rstd.data_ptr(), _ptr(dres), rows, d, dx.data_ptr(), dgamma.data_ptr(),
                  dbeta.data_ptr(), code, at, need, _stream(stream, dev))
