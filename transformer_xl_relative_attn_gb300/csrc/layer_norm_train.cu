@@ -15,9 +15,10 @@
 // Both passes are bound by memory: a row is read once, held in registers (E
 // elements per lane, W warps per row), reduced by shuffles and, with several
 // warps, through shared memory, and written once.  Rows of a multiple of 16
-// bytes move as 16-byte vectors, others element by element with the same code.
-// The backward pass is persistent: each thread keeps its columns' sums of dout xh
-// and dout in registers over all rows of its CTA, so dgamma and dbeta cost no
+// bytes move as 16-byte vectors, others by 4 or 2 bytes with the same code.
+// The backward pass is persistent: bulk copies bring rows ahead into a ring of stages in
+// shared memory, and each thread keeps its columns' sums of dout xh and dout in registers
+// over all rows of its CTA, so dgamma and dbeta cost no
 // second pass over the rows; the CTAs' sums go to the workspace and a second
 // launch adds them, in a fixed order (the same inputs give the same bits).  With
 // few rows other CTAs of the same launch read the rows again for these sums, column
@@ -241,6 +242,9 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     }
 }
 
+// Shared memory of the rings of an SM, beside 2 KB a CTA for the rest.
+constexpr size_t kRingRoom = 220 * 1024;
+
 // CTAs per SM that the backward kernel is compiled for.
 template <int E, int W>
 constexpr int bwd_ctas() {
@@ -256,11 +260,11 @@ struct Columns {
     static constexpr int CL = SECTOR > THREADS / 128 ? SECTOR : THREADS / 128;
     static constexpr int C = CL * V;           // columns of a CTA
     static constexpr int RG = THREADS / CL;    // rows at a time
-    // Rows up to which this is done: 8 per thread, 16 of narrow vectors.  Bf16 with y, once
+    // Rows up to which this is done: 8 per thread, fp32 4, and 16 of narrow vectors.  Bf16 with y, once
     // against sums in the row CTAs and a second launch: 128 x 512 2.2 and 4.2 us, 1024 x 512
     // 4.0 and 5.1, 2048 x 512 8.2 and 5.5; 512 x 500 3.4 and 5.1, 1024 x 500 5.5 and 5.1;
     // 128 x 4096 3.3 and 13.2.
-    static constexpr int ROWS = (V >= 4 ? 8 : 16) * RG;
+    static constexpr int ROWS = (V >= 4 ? 16 / (int)sizeof(T) : 16) * RG;
 };
 
 template <typename T, int V, int W>
@@ -319,49 +323,85 @@ __device__ __forceinline__ void ln_bwd_columns(const T* __restrict__ dout, const
     (i < S::C ? dgamma : dbeta)[col] = a;
 }
 
-// FEW: CTAs from row_ctas on take columns, and part is not used.
-template <typename T, int V, int E, int W, bool FEW>
+// How the rows come: from global memory row by row; the same, with CTAs from row_ctas on
+// that take columns (part is not used); or ahead of their use through a ring of stages in
+// shared memory.
+enum BwdMode { kPlain, kFew, kRing };
+constexpr int kMaxStages = 3;  // (25600 x 1024 bf16: 3 or 4 stages 33 us, 8 35 us)
+
+// Whether rows that are not few come through the ring: where they did, plain loads waited for
+// memory with 16 warps per SM (25600 x 1024 bf16 40 us, through the ring 33; 8000 x 3000 49
+// and 37; 9001 x 1001 fp32 31.4 and 28.2).  A warp per row of bf16 has rows enough in flight
+// (11264 x 512 12.8 us, with the ring 13.8), and bf16 by single elements has its instructions to
+// wait for (9001 x 1001 20.4 us and 21.1).  32 warps leave 64 registers.
+template <typename T, int V, int W>
+constexpr bool takes_ring() {
+    return W < 32 && (sizeof(T) == 4 || (V == 8 && W > 1));
+}
+
+// A stage of the ring: `rows` consecutive rows of every tensor, whose bytes are a multiple of 16.
+struct Ring {
+    int rows, stages;
+    int gamma;  // offset behind the stages
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <typename T, int V, int E, int W, int MODE>
 __global__ void __launch_bounds__(Shape<W>::THREADS, bwd_ctas<E, W>())
 ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __restrict__ y,
               const T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
-              const T* __restrict__ dres, long long rows, int d, float inv_d, T* __restrict__ dx,
-              int row_ctas, float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta) {
+              const T* __restrict__ dres, long long rows, int d, float inv_d, T* __restrict__ dx, int row_ctas,
+              float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta, Ring ring, int* status) {
     using S = Shape<W>;
     using Col = Columns<T, V, W>;
     __shared__ float2 sh[2 * S::THREADS / 32];
-    __shared__ float fold[FEW ? S::THREADS / 32 * 2 * Col::C : S::R > 1 ? S::THREADS / 2 * 2 * E : 1];
+    __shared__ __align__(8) uint64_t full[MODE == kRing ? kMaxStages : 1];
+    __shared__ int abort_word;
+    extern __shared__ __align__(128) unsigned char dynamic[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (MODE == kRing && threadIdx.x == 0) {
+        for (int s = 0; s < kMaxStages; ++s) mbar_init(&full[s], 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (FEW && (int)blockIdx.x >= row_ctas) {
-        ln_bwd_columns<T, V, W>(dout, x, y, mean, rstd, (int)rows, d, (int)blockIdx.x - row_ctas, fold, dgamma, dbeta);
+    if (MODE == kFew && (int)blockIdx.x >= row_ctas) {
+        ln_bwd_columns<T, V, W>(dout, x, y, mean, rstd, (int)rows, d, (int)blockIdx.x - row_ctas,
+                                reinterpret_cast<float*>(dynamic), dgamma, dbeta);
         return;
     }
     const int t = threadIdx.x % S::TPR, lr = threadIdx.x / S::TPR;
-    alignas(8) float dg[E], db[E], gam[E];
+    // gamma stays in registers, or in shared memory beside a ring of whole fp32 vectors (in
+    // registers it made that kernel spill, and beside the ring there is little L1 to spill to)
+    constexpr bool GAMMA_SH = MODE == kRing && sizeof(T) == 4 && V == 4 && W >= 8;
+    constexpr int G = GAMMA_SH ? V : E;
+    alignas(8) float dg[E], db[E], gam[G];
     const int left = d - t * V;
-    load_row<T, V, E, S::TPR>(gamma + t * V, left, gam);
+    T* const gamma_sh = reinterpret_cast<T*>(dynamic + ring.gamma);
+    if constexpr (GAMMA_SH) {
+        for (int i = threadIdx.x; i < d; i += S::THREADS) gamma_sh[i] = gamma[i];
+    } else {
+        load_row<T, V, E, S::TPR>(gamma + t * V, left, gam);
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.f;
     int phase = 0;
-    // where this thread's elements of its rows lie, row after row
-    const long long first = (long long)blockIdx.x * S::R + lr, step = (long long)row_ctas * S::R, hop = step * d;
-    long long at = first * d + t * V;
-    int todo = (int)(rows > (long long)blockIdx.x * S::R ? (rows - (long long)blockIdx.x * S::R + step - 1) / step : 0);
-    const float *mp = mean + first, *rp = rstd + first;
-    long long past = rows - first;  // rows from this thread's on
-    for (; todo > 0; --todo, phase ^= 1, at += hop, past -= step, mp += step, rp += step) {
-        const bool in = past > 0;
+    // One row, this thread's elements of which lie at px, pd, py, pr and go to `to`.
+    auto row = [&](const T* px, const T* pd, const T* py, const T* pr, T* to, bool in, float mu, float rs) {
         alignas(8) float xh[E], g[E];
-        float rs = 0.f;
         float2 s = both(0.f);
         if (in) {
-            const float mu = *mp;
-            rs = *rp;
-            load_row<T, V, E, S::TPR>(x + at, left, xh);
-            load_row<T, V, E, S::TPR>(dout + at, left, g);
+            load_row<T, V, E, S::TPR>(px, left, xh);
+            load_row<T, V, E, S::TPR>(pd, left, g);
             if (y) {
                 alignas(8) float b[E];
-                load_row<T, V, E, S::TPR>(y + at, left, b);
+                load_row<T, V, E, S::TPR>(py, left, b);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) pair(xh, e) = __fadd2_rn(pair(xh, e), pair(b, e));
             }
@@ -373,11 +413,13 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 float2& h = pair(xh, e);
                 float2& q = pair(g, e);
                 h = __fmul2_rn(__fadd2_rn(h, both(-mu)), both(rs));
-                if (!FEW) {
+                if (MODE != kFew) {
                     pair(dg, e) = __ffma2_rn(q, h, pair(dg, e));
                     pair(db, e) = __fadd2_rn(pair(db, e), q);
                 }
-                q = __fmul2_rn(q, pair(gam, e));
+                if (GAMMA_SH && 2 * e % G == 0)
+                    load_row<T, V, G, S::TPR>(gamma_sh + (t + S::TPR * (2 * e / V)) * V, left - S::TPR * (2 * e / V) * V, gam);
+                q = __fmul2_rn(q, pair(gam, e % (G / 2)));
                 s1 = __fadd2_rn(s1, q);
                 s2 = __ffma2_rn(q, h, s2);
             }
@@ -386,7 +428,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
             // no registers of their own through it
             if (dres) {
                 alignas(8) float a[E];
-                load_row<T, V, E, S::TPR>(dres + at, left, a);
+                load_row<T, V, E, S::TPR>(pr, left, a);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) pair(g, e) = __ffma2_rn(pair(g, e), both(rs), pair(a, e));
             } else {
@@ -395,19 +437,103 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
             }
         }
         s = row_sum2<W>(s, sh, phase);
-        if (!in) continue;
+        phase ^= 1;
+        if (!in) return;
         const float2 c1 = both(-rs * s.x * inv_d), c2 = both(-rs * s.y * inv_d);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) pair(g, e) = __fadd2_rn(__ffma2_rn(pair(xh, e), c2, pair(g, e)), c1);
 #pragma unroll
         for (int i = 0; i < E / V; ++i) {
             constexpr int OFF = S::TPR * V;
-            if (OFF * i < left && TXL_BOUNDS(OFF * i + V <= left, 903, at)) Vec<T, V>::store(dx + at + OFF * i, g + V * i);
+            if (OFF * i < left && TXL_BOUNDS(OFF * i + V <= left, 903, left)) Vec<T, V>::store(to + OFF * i, g + V * i);
+        }
+    };
+    if constexpr (MODE == kRing) {
+        // This CTA's stages are blockIdx.x, blockIdx.x + row_ctas, ..  Thread 0 fills a slot
+        // again when all threads are past their reads of it: with several warps per row
+        // that is known from the row's own reduction.
+        const long long n_stages = rows / ring.rows;
+        const int count = (int)(n_stages > blockIdx.x ? (n_stages - blockIdx.x + row_ctas - 1) / row_ctas : 0);
+        const uint32_t per = (uint32_t)ring.rows * d * sizeof(T), bytes = per * (2 + (y != nullptr) + (dres != nullptr));
+        const uint32_t o_y = 2 * per, o_r = o_y + (y ? per : 0);
+        auto fill = [&](int k, int slot) {
+            const long long at = ((long long)k * row_ctas + blockIdx.x) * ring.rows * d;
+            if (!TXL_BOUNDS(at + (long long)ring.rows * d <= rows * d, 905, at)) return;
+            unsigned char* const to = dynamic + slot * bytes;
+            mbar_expect_tx(&full[slot], bytes);
+            bulk_load(to, x + at, per, &full[slot]);
+            bulk_load(to + per, dout + at, per, &full[slot]);
+            if (y) bulk_load(to + o_y, y + at, per, &full[slot]);
+            if (dres) bulk_load(to + o_r, dres + at, per, &full[slot]);
+        };
+        if (threadIdx.x == 0)
+            for (int k = 0; k < ring.stages && k < count; ++k) fill(k, k);
+        __syncthreads();  // the barriers are ready
+        // The rows behind the last full stage are a stage of the CTA whose turn it is, copied
+        // by its threads.
+        const int rest = (int)(rows - n_stages * ring.rows);
+        const int total = count + (rest && (long long)blockIdx.x == n_stages % row_ctas);
+        bool ok = true;
+        int slot = 0, parity = 0;
+        long long r = (long long)blockIdx.x * ring.rows + lr;  // this thread's row
+        float mu = 0.f, rs = 0.f;
+        if (r < rows) mu = mean[r], rs = rstd[r];
+#pragma unroll 1
+        for (int k = 0; k < total; ++k) {
+            T* const st = reinterpret_cast<T*>(dynamic + slot * bytes);
+            int n = ring.rows;
+            if (k == count) {
+                n = rest;
+                const long long at = n_stages * ring.rows * d;
+                for (int i = threadIdx.x; i < n * d; i += S::THREADS) {
+                    st[i] = x[at + i];
+                    st[i + per / sizeof(T)] = dout[at + i];
+                    if (y) st[i + o_y / sizeof(T)] = y[at + i];
+                    if (dres) st[i + o_r / sizeof(T)] = dres[at + i];
+                }
+                __syncthreads();
+            } else if (ok && !mbar_wait(&full[slot], parity, kDevTimeoutProducer, &abort_word, status)) {
+                // (nothing is waited for or filled from here on; what is still on its way lands
+                // before the CTA ends)
+                ok = false;
+                for (int i = k; threadIdx.x == 0 && i < count && i < k + ring.stages; ++i) {
+                    const uint64_t t0 = globaltimer_ns();
+                    const int at = i % ring.stages, odd = (i / ring.stages) & 1;
+                    while (!mbar_try_wait(&full[at], odd) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+                }
+            }
+            const T* p = st + lr * d + t * V;
+#pragma unroll 1
+            for (int q = 0; q < n; q += S::R, p += S::R * d) {
+                const float m = mu, s = rs;
+                const bool in = q + lr < n;
+                T* const to = dx + r * d + t * V;
+                r += q + S::R >= n ? (long long)row_ctas * ring.rows - q : S::R;
+                if (r < rows) mu = mean[r], rs = rstd[r];
+                row(p, p + per / sizeof(T), p + o_y / sizeof(T), p + o_r / sizeof(T), to, in, m, s);
+            }
+            if (W == 1) __syncthreads();
+            if (threadIdx.x == 0 && ok && k + ring.stages < count) fill(k + ring.stages, slot);
+            if (++slot == ring.stages) slot = 0, parity ^= 1;
+        }
+    } else {
+        // where this thread's elements of its rows lie, row after row
+        const long long first = (long long)blockIdx.x * S::R + lr, step = (long long)row_ctas * S::R, hop = step * d;
+        long long at = first * d + t * V;
+        int todo =
+            (int)(rows > (long long)blockIdx.x * S::R ? (rows - (long long)blockIdx.x * S::R + step - 1) / step : 0);
+        const float *mp = mean + first, *rp = rstd + first;
+        long long past = rows - first;  // rows from this thread's on
+#pragma unroll 1
+        for (; todo > 0; --todo, at += hop, past -= step, mp += step, rp += step) {
+            const bool in = past > 0;
+            row(x + at, dout + at, y + at, dres + at, dx + at, in, in ? *mp : 0.f, in ? *rp : 0.f);
         }
     }
-    if (FEW) return;
+    if (MODE == kFew) return;
     // the CTA's rows fold in halves, into the first row's threads
     if (S::R > 1) {
+        float* const fold = reinterpret_cast<float*>(dynamic);
 #pragma unroll
         for (int half = S::R / 2; half > 0; half >>= 1) {
             __syncthreads();
@@ -469,10 +595,12 @@ __global__ void __launch_bounds__(1024) ln_bwd_sum_kernel(const float* __restric
 // Launch with programmatic stream serialisation (every kernel here waits for
 // the one before it before its first global access).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned threads, size_t dynamic, cudaStream_t stream,
+                       Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = dynamic;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -524,22 +652,34 @@ auto pick_width(int d, F f) {
 }
 
 // How the backward pass is launched: CTAs that take rows (one round of resident ones at
-// most), and CTAs that take columns (0: the row CTAs sum them, into as many parts).
+// most), CTAs that take columns (0: the row CTAs sum them, into as many parts), and the
+// rows of a ring's stage.
 struct BwdGrid {
-    int rows, columns;
+    int rows, columns, stage;
 };
 template <typename T>
 BwdGrid bwd_grid(long long rows, int d) {
     BwdGrid g = {};
     pick_bwd(d, [&](auto k) {
         constexpr int E = decltype(k)::e, W = decltype(k)::w, R = Shape<W>::R;
-        const long long want = (rows + R - 1) / R, most = (long long)bwd_ctas<E, W>() * current_sm_count();
-        g.rows = (int)(want < 1 ? 1 : (want < most ? want : most));
+        const long long most = (long long)bwd_ctas<E, W>() * current_sm_count();
+        // as many rows as fill the CTA, start at 16 bytes, and make 4 KB where there are many
+        g.stage = R;
+        while ((long long)g.stage * d * sizeof(T) % 16) g.stage *= 2;
+        while ((long long)g.stage * d * sizeof(T) < 4096 && rows / (2 * g.stage) >= 2 * most) g.stage *= 2;
+        int by = R;
         pick_width<T>(d, [&](auto v) {
-            using C = Columns<T, decltype(v)::v, W>;
-            if (rows <= C::ROWS) g.columns = (d + C::C - 1) / C::C;
+            constexpr int V = decltype(v)::v;
+            using C = Columns<T, V, W>;
+            // (two stages of four tensors may not fit: then the rows are dealt one by one)
+            if (rows <= C::ROWS)
+                g.columns = (d + C::C - 1) / C::C;
+            else if (takes_ring<T, V, W>() && (size_t)(g.stage * 4 * 2 + 1) * d * sizeof(T) <= kRingRoom / bwd_ctas<E, W>())
+                by = g.stage;
             return 0;
         });
+        const long long want = (rows + by - 1) / by;
+        g.rows = (int)(want < 1 ? 1 : (want < most ? want : most));
         return cudaSuccess;
     });
     return g;
@@ -553,7 +693,7 @@ cudaError_t ln_fwd(const void* x, const void* y, const void* gamma, const void* 
         constexpr int E = decltype(k)::e, W = decltype(k)::w;
         const long long ctas = (rows + Shape<W, 128>::R - 1) / Shape<W, 128>::R;
         if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-        return launch_pdl(ln_fwd_kernel<T, V, E, W>, (unsigned)ctas, (unsigned)Shape<W, 128>::THREADS, stream,
+        return launch_pdl(ln_fwd_kernel<T, V, E, W>, (unsigned)ctas, (unsigned)Shape<W, 128>::THREADS, 0, stream,
                           static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(gamma),
                           static_cast<const T*>(beta), rows, d, 1.f / d, eps, static_cast<T*>(out), mean, rstd);
     });
@@ -562,21 +702,42 @@ cudaError_t ln_fwd(const void* x, const void* y, const void* gamma, const void* 
 template <typename T, int V>
 cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
                    const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
-                   float* dbeta, float* part, cudaStream_t stream) {
+                   float* dbeta, float* part, int* status, cudaStream_t stream) {
     // (no rows: CTAs that add nothing write the zeros)
     const BwdGrid grid = bwd_grid<T>(rows, d);
     const cudaError_t e = pick_bwd(d, [&](auto k) {
         constexpr int E = decltype(k)::e, W = decltype(k)::w;
-        auto go = [&](auto kern) {
-            return launch_pdl(kern, (unsigned)(grid.rows + grid.columns), (unsigned)Shape<W>::THREADS, stream,
+        using S = Shape<W>;
+        auto go = [&](auto kern, size_t dynamic, Ring ring) {
+            return launch_pdl(kern, (unsigned)(grid.rows + grid.columns), (unsigned)S::THREADS, dynamic, stream,
                               static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
                               static_cast<const T*>(gamma), mean, rstd, static_cast<const T*>(dres), rows, d, 1.f / d,
-                              static_cast<T*>(dx), grid.rows, part, dgamma, dbeta);
+                              static_cast<T*>(dx), grid.rows, part, dgamma, dbeta, ring, status);
         };
-        return grid.columns ? go(ln_bwd_kernel<T, V, E, W, true>) : go(ln_bwd_kernel<T, V, E, W, false>);
+        if (grid.columns)
+            return go(ln_bwd_kernel<T, V, E, W, kFew>, S::THREADS / 32 * 2 * Columns<T, V, W>::C * sizeof(float), Ring{});
+        const size_t fold = S::R > 1 ? S::THREADS * E * sizeof(float) : 0;
+        const size_t stage = (size_t)grid.stage * d * sizeof(T) * (2 + (y != nullptr) + (dres != nullptr));
+        if constexpr (takes_ring<T, V, W>()) {
+            constexpr size_t kRoom = kRingRoom / bwd_ctas<E, W>();
+            const size_t own = (size_t)d * sizeof(T), most = kRoom > own ? (kRoom - own) / stage : 0;
+            const int stages = (int)(most < kMaxStages ? most : kMaxStages);
+            if (stages >= 2) {
+                static PerDeviceOnce attrs;
+                const cudaError_t set = attrs.run([] {
+                    return cudaFuncSetAttribute(ln_bwd_kernel<T, V, E, W, kRing>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
+                });
+                if (set != cudaSuccess) return set;
+                const size_t bytes = stage * stages + own;
+                return go(ln_bwd_kernel<T, V, E, W, kRing>, bytes > fold ? bytes : fold,
+                          Ring{grid.stage, stages, (int)(stage * stages)});
+            }
+        }
+        return go(ln_bwd_kernel<T, V, E, W, kPlain>, fold, Ring{});
     });
     if (e != cudaSuccess || grid.columns) return e;
-    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, stream, part, grid.rows, d, dgamma, dbeta);
+    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, 0, stream, part, grid.rows, d, dgamma, dbeta);
 }
 
 }  // namespace
@@ -600,13 +761,14 @@ size_t layer_norm_bwd_workspace_bytes(long long rows, int d, int bf16) {
 
 cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
                                   const float* mean, const float* rstd, const void* dres, long long rows, int d,
-                                  void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
+                                  void* dx, float* dgamma, float* dbeta, void* workspace, int bf16, int* status,
                                   cudaStream_t stream) {
     float* part = static_cast<float*>(workspace);
     auto go = [&](auto zero) {
         using T = decltype(zero);
         return pick_width<T>(d, [&](auto v) {
-            return ln_bwd<T, decltype(v)::v>(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part, stream);
+            return ln_bwd<T, decltype(v)::v>(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta, part, status,
+                                               stream);
         });
     };
     return bf16 ? go(__nv_bfloat16()) : go(float());

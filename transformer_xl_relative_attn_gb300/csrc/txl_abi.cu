@@ -38,7 +38,7 @@ cudaError_t launch_layer_norm_fwd(const void* x, const void* y, const void* gamm
 size_t layer_norm_bwd_workspace_bytes(long long rows, int d, int bf16);
 cudaError_t launch_layer_norm_bwd(const void* dout, const void* x, const void* y, const void* gamma,
                                   const float* mean, const float* rstd, const void* dres, long long rows,
-                                  int d, void* dx, float* dgamma, float* dbeta, void* workspace, int bf16,
+                                  int d, void* dx, float* dgamma, float* dbeta, void* workspace, int bf16, int* status,
                                   cudaStream_t stream);
 cudaError_t launch_attn_simt_f32(const float* q, const float* k, const float* v, const float* r,
                                  const float* ub, const float* vb, int B, int H, int L, int M,
@@ -729,8 +729,11 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
                  range_of(rstd, nr, false), range_of(dres, n, false),   range_of(dx, n, true),
                  range_of(dgamma, nd, true), range_of(dbeta, nd, true), range_of(workspace, need, true)};
     if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    int* status = dev_status_ptr();
+    if (!status) return TXL_ERR_CUDA;
     return cuda_status(txl::launch_layer_norm_bwd(dout, x, y, gamma, mean, rstd, dres, rows, d, dx, dgamma, dbeta,
-                                                  workspace, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
+                                                  workspace, dtype == TXL_BF16, status,
+                                                  static_cast<cudaStream_t>(stream)));
 }
 
 size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
