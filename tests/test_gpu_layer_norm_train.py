@@ -88,7 +88,9 @@ def check_backward(t, mean, rstd, dres, **kw):
 
 
 SIZES = [(1, 1), (3, 2), (5, 7), (1, 512), (22, 512), (130, 33), (70, 256), (64, 1000), (33, 1001), (128, 1024),
-         (17, 1536), (9, 2048), (200, 768), (7, 4100), (3, 8192), (2, 16384), (5, 16383), (2000, 64), (700, 96), (2, 3001)]
+         (17, 1536), (9, 2048), (200, 768), (7, 4100), (3, 8192), (2, 16384), (5, 16383), (2000, 64), (700, 96), (2, 3001),
+         # more rows than are few, so that they come through the ring in whole and broken stages, or row by row
+         (1100, 3000), (1201, 1024), (1030, 8192), (601, 6001), (1500, 1001), (1025, 8200)]
 
 
 @pytest.mark.parametrize("rows,d", SIZES)

@@ -161,7 +161,8 @@ assert txl.bounds_status() == (0, 0), "not the bounds-checked build, or stale re
 bf, f32 = torch.bfloat16, torch.float32
 g = torch.Generator(device="cuda").manual_seed(1)
 n = lambda *s, dt=bf: torch.empty(s, device="cuda").normal_(generator=g).to(dt)
-for rows, d, dt in [(1, 1, f32), (37, 520, bf), (9, 1001, f32), (130, 1024, bf), (5, 4099, bf), (3, 16384, f32)]:
+for rows, d, dt in [(1, 1, f32), (37, 520, bf), (9, 1001, f32), (130, 1024, bf), (5, 4099, bf), (3, 16384, f32),
+                    (2005, 1024, bf), (1501, 1001, f32), (1300, 4104, bf), (1501, 1001, bf), (1100, 12000, bf)]:
     x, y, w, b, do = n(rows, d, dt=dt), n(rows, d, dt=dt), n(d, dt=dt), n(d, dt=dt), n(rows, d, dt=dt)
     out, mean, rstd = txl.layer_norm_fwd(x, w, b, y=y)
     z = (x.double() + y.double())
