@@ -567,20 +567,30 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     }
 }
 
-// dgamma and dbeta: the CTAs' sums of 32 columns per CTA, 32 threads on each.
+// dgamma and dbeta: the CTAs' sums of 32 columns per CTA, 64 threads on each two, all of
+// whose loads are on their way together (up to 384 parts).
 __global__ void __launch_bounds__(1024) ln_bwd_sum_kernel(const float* __restrict__ part, int n_part, int d,
                                                           float* __restrict__ dgamma, float* __restrict__ dbeta) {
     __shared__ float sh[32][33];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float a = 0.f;
-    if (c < 2 * d) {
-#pragma unroll 4
-        for (int p = w; p < n_part; p += 32) a += part[(size_t)p * 2 * d + c];
+    const int c = blockIdx.x * 32 + (lane & 15) * 2;  // (2 d is even)
+    float2 a = both(0.f);
+    for (int p0 = threadIdx.x >> 4; c < 2 * d && p0 < n_part; p0 += 6 * 64) {
+        float2 v[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            v[i] = p0 + 64 * i < n_part ? *reinterpret_cast<const float2*>(part + (size_t)(p0 + 64 * i) * 2 * d + c) : both(0.f);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) a = __fadd2_rn(a, v[i]);
     }
-    sh[w][lane] = a;
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+    if (lane < 16) {
+        sh[w][2 * lane] = a.x;
+        sh[w][2 * lane + 1] = a.y;
+    }
     __syncthreads();
     const float s = warp_sum(sh[lane][w]);  // column w of this CTA's 32
     const int cw = blockIdx.x * 32 + w;
