@@ -150,6 +150,36 @@ def test_a_training_step_in_a_graph(bits):
     assert all(torch.equal(v, opt.master[a:a + v.numel()].view(v.shape).to(BF)) for v, a in zip(p.values(), opt.starts))
 
 
+def test_calls_on_several_streams_at_once():
+    """Two blocks' gradients and an attention forward, each on a stream of its own and all
+    at once: what they give one after the other."""
+    d, di = 512, 1024
+    p = [parameters(d, di, 50), parameters(d, di, 60)]
+    x, dh = [rnd(8, 256, d, seed=70 + i) for i in range(2)], [rnd(8, 256, d, std=0.1, seed=72 + i) for i in range(2)]
+    q, k, v, r = rnd(4, 8, 256, 64, seed=74), rnd(4, 8, 512, 64, seed=75), rnd(4, 8, 512, 64, seed=76), rnd(512, 8, 64, seed=77)
+    u = rnd(8, 64, std=0.3, seed=78)
+    saved = [feed_forward(p[i], x[i])[1] for i in range(2)]
+
+    def grads_of(i):
+        g = {n: torch.empty(t.shape, device="cuda") for n, t in p[i].items()}
+        dx = feed_forward_bwd(p[i], dh[i], saved[i], g)
+        return [*g.values(), *(dx if isinstance(dx, (tuple, list)) else (dx,))]
+
+    jobs = [lambda: grads_of(0), lambda: grads_of(1), lambda: [txl.attn_fwd(q, k, v, r, u, u)]]
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = []
+        for job, st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                got.append([job() for _ in range(3)][-1])
+        torch.cuda.synchronize()
+        assert txl.sync_status() == 0
+        for a, b in zip(want, got):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
 CHILD = r'''
 import sys
 import torch
