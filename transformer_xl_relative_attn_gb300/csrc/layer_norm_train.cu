@@ -13,8 +13,8 @@
 // arithmetic, statistics and parameter gradients.
 //
 // Both passes are bound by memory: a row is read once, held in registers (E
-// elements per lane, W warps per row), reduced by shuffles and, with several
-// warps, through shared memory, and written once.  Rows of a multiple of 16
+// elements per lane, L lanes per row), reduced by shuffles and, with several
+// warps per row, through shared memory, and written once.  Rows of a multiple of 16
 // bytes move as 16-byte vectors, others by 4 or 2 bytes with the same code.
 // The backward pass is persistent: bulk copies bring rows ahead into a ring of stages in
 // shared memory, and each thread keeps its columns' sums of dout xh and dout in registers
@@ -110,50 +110,52 @@ __device__ __forceinline__ float inv_sqrt(float a) {
     return a > 0.f && a < INFINITY ? fmaf(r, fmaf(-h, r, 0.5f), r) : r;
 }
 
+// Over a warp, or its L lanes of a row.
+template <int L = 32>
 __device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
-// A CTA's threads: R rows side by side, W warps on each; T threads if they hold a row.
+// A CTA's threads: R rows side by side, L lanes on each; T threads if they hold a row.
 // The forward pass takes 128 (25600 x 1024 bf16: 19.8 us, with 256 21.1 us: its CTAs are
 // short, and smaller ones leave and follow more evenly), the backward pass, whose CTAs
 // stay and fold their sums at the end, 256 (11264 x 512 bf16: 13.8 us, with 128 15.0 us).
-template <int W, int T = 256>
+template <int L, int T = 256>
 struct Shape {
-    static constexpr int THREADS = 32 * W < T ? T : 32 * W;
-    static constexpr int R = THREADS / (32 * W);
-    static constexpr int TPR = 32 * W;  // threads per row
+    static constexpr int THREADS = L < T ? T : L;
+    static constexpr int R = THREADS / L;
+    static constexpr int TPR = L;  // threads per row
 };
 
-// Sum over the W warps of a row.  sh: [2][THREADS / 32], `phase` alternates from
+// Sum over the L lanes of a row.  sh: [2][THREADS / 32], `phase` alternates from
 // call to call, so one barrier per call is enough.
-template <int W>
+template <int L>
 __device__ __forceinline__ float row_sum(float s, float* sh, int phase) {
-    s = warp_sum(s);
-    if (W == 1) return s;
-    constexpr int N = Shape<W, 128>::THREADS / 32;
+    s = warp_sum<L>(s);
+    if (L <= 32) return s;
+    constexpr int N = Shape<L, 128>::THREADS / 32;
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) sh[phase * N + warp] = s;
     __syncthreads();
     float a = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) a += sh[phase * N + warp / W * W + w];
+    for (int w = 0; w < L / 32; ++w) a += sh[phase * N + warp / (L / 32) * (L / 32) + w];
     return a;
 }
-template <int W>
+template <int L>
 __device__ __forceinline__ float2 row_sum2(float2 s, float2* sh, int phase) {
-    s = make_float2(warp_sum(s.x), warp_sum(s.y));
-    if (W == 1) return s;
-    constexpr int N = Shape<W>::THREADS / 32;
+    s = make_float2(warp_sum<L>(s.x), warp_sum<L>(s.y));
+    if (L <= 32) return s;
+    constexpr int N = Shape<L>::THREADS / 32;
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) sh[phase * N + warp] = s;
     __syncthreads();
     float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const float2 t = sh[phase * N + warp / W * W + w];
+    for (int w = 0; w < L / 32; ++w) {
+        const float2 t = sh[phase * N + warp / (L / 32) * (L / 32) + w];
         a.x += t.x, a.y += t.y;
     }
     return a;
@@ -174,12 +176,19 @@ __device__ __forceinline__ void load_row(const T* p, int left, float (&f)[E]) {
     }
 }
 
-template <typename T, int V, int E, int W>
-__global__ void __launch_bounds__(Shape<W, 128>::THREADS)
+// Threads of a forward CTA.  Rows of 8 elements per lane make many and short CTAs, which cost
+// more to start than to run (400000 x 64 bf16: 256 threads 21.3 us, 128 26.4, 512 22.2).
+template <int E>
+constexpr int fwd_threads() {
+    return E <= 8 ? 256 : 128;
+}
+
+template <typename T, int V, int E, int L>
+__global__ void __launch_bounds__(Shape<L, fwd_threads<E>()>::THREADS)
 ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restrict__ gamma,
               const T* __restrict__ beta, long long rows, int d, float inv_d, float eps, T* __restrict__ out,
               float* __restrict__ mean_out, float* __restrict__ rstd_out) {
-    using S = Shape<W, 128>;
+    using S = Shape<L, fwd_threads<E>()>;
     __shared__ float sh[2 * S::THREADS / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -204,7 +213,7 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     float2 s = both(0.f);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) s = __fadd2_rn(s, pair(z, e));
-    const float mean = row_sum<W>(s.x + s.y, sh, 0) * inv_d;
+    const float mean = row_sum<L>(s.x + s.y, sh, 0) * inv_d;
     // (behind the row's end z is 0 and stays so)
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
@@ -218,7 +227,7 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
     float2 q = both(0.f);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) q = __ffma2_rn(pair(z, e), pair(z, e), q);
-    const float rstd = inv_sqrt(fmaf(row_sum<W>(q.x + q.y, sh, 1), inv_d, eps));
+    const float rstd = inv_sqrt(fmaf(row_sum<L>(q.x + q.y, sh, 1), inv_d, eps));
     if (!in) return;
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
@@ -246,16 +255,16 @@ ln_fwd_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restr
 constexpr size_t kRingRoom = 220 * 1024;
 
 // CTAs per SM that the backward kernel is compiled for.
-template <int E, int W>
+template <int E, int L>
 constexpr int bwd_ctas() {
-    return Shape<W>::THREADS > 256 ? 1 : (E <= 8 ? 3 : 2);
+    return Shape<L>::THREADS > 256 ? 1 : (E <= 8 ? 3 : 2);
 }
 
 // dgamma and dbeta of a few columns by one CTA: CL lanes of V columns side by side, at least
 // 32 bytes of a row, and as many threads below one another as the CTA has.
-template <typename T, int V, int W>
+template <typename T, int V, int L>
 struct Columns {
-    static constexpr int THREADS = Shape<W>::THREADS;
+    static constexpr int THREADS = Shape<L>::THREADS;
     static constexpr int SECTOR = 32 / (int)sizeof(T) / V;
     static constexpr int CL = SECTOR > THREADS / 128 ? SECTOR : THREADS / 128;
     static constexpr int C = CL * V;           // columns of a CTA
@@ -267,12 +276,12 @@ struct Columns {
     static constexpr int ROWS = (V >= 4 ? 16 / (int)sizeof(T) : 16) * RG;
 };
 
-template <typename T, int V, int W>
+template <typename T, int V, int L>
 __device__ __forceinline__ void ln_bwd_columns(const T* __restrict__ dout, const T* __restrict__ x,
                                                const T* __restrict__ y, const float* __restrict__ mean,
                                                const float* __restrict__ rstd, int rows, int d, int cta, float* sh,
                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    using S = Columns<T, V, W>;
+    using S = Columns<T, V, L>;
     const int cl = threadIdx.x % S::CL, c = cta * S::C + cl * V;
     float dg[V], db[V];
 #pragma unroll
@@ -334,9 +343,9 @@ constexpr int kMaxStages = 3;  // (25600 x 1024 bf16: 3 or 4 stages 33 us, 8 35 
 // and 37; 9001 x 1001 fp32 31.4 and 28.2).  A warp per row of bf16 has rows enough in flight
 // (11264 x 512 12.8 us, with the ring 13.8), and bf16 by single elements has its instructions to
 // wait for (9001 x 1001 20.4 us and 21.1).  32 warps leave 64 registers.
-template <typename T, int V, int W>
+template <typename T, int V, int L>
 constexpr bool takes_ring() {
-    return W < 32 && (sizeof(T) == 4 || (V == 8 && W > 1));
+    return L < 1024 && (sizeof(T) == 4 || (V == 8 && L > 32));
 }
 
 // A stage of the ring: `rows` consecutive rows of every tensor, whose bytes are a multiple of 16.
@@ -352,14 +361,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-template <typename T, int V, int E, int W, int MODE>
-__global__ void __launch_bounds__(Shape<W>::THREADS, bwd_ctas<E, W>())
+template <typename T, int V, int E, int L, int MODE>
+__global__ void __launch_bounds__(Shape<L>::THREADS, bwd_ctas<E, L>())
 ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __restrict__ y,
               const T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
               const T* __restrict__ dres, long long rows, int d, float inv_d, T* __restrict__ dx, int row_ctas,
               float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta, Ring ring, int* status) {
-    using S = Shape<W>;
-    using Col = Columns<T, V, W>;
+    using S = Shape<L>;
+    using Col = Columns<T, V, L>;
     __shared__ float2 sh[2 * S::THREADS / 32];
     __shared__ __align__(8) uint64_t full[MODE == kRing ? kMaxStages : 1];
     __shared__ int abort_word;
@@ -372,14 +381,14 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (MODE == kFew && (int)blockIdx.x >= row_ctas) {
-        ln_bwd_columns<T, V, W>(dout, x, y, mean, rstd, (int)rows, d, (int)blockIdx.x - row_ctas,
+        ln_bwd_columns<T, V, L>(dout, x, y, mean, rstd, (int)rows, d, (int)blockIdx.x - row_ctas,
                                 reinterpret_cast<float*>(dynamic), dgamma, dbeta);
         return;
     }
     const int t = threadIdx.x % S::TPR, lr = threadIdx.x / S::TPR;
     // gamma stays in registers, or in shared memory beside a ring of whole fp32 vectors (in
     // registers it made that kernel spill, and beside the ring there is little L1 to spill to)
-    constexpr bool GAMMA_SH = MODE == kRing && sizeof(T) == 4 && V == 4 && W >= 8;
+    constexpr bool GAMMA_SH = MODE == kRing && sizeof(T) == 4 && V == 4 && L >= 256;
     constexpr int G = GAMMA_SH ? V : E;
     alignas(8) float dg[E], db[E], gam[G];
     const int left = d - t * V;
@@ -436,7 +445,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 for (int e = 0; e < E / 2; ++e) pair(g, e) = __fmul2_rn(pair(g, e), both(rs));
             }
         }
-        s = row_sum2<W>(s, sh, phase);
+        s = row_sum2<L>(s, sh, phase);
         phase ^= 1;
         if (!in) return;
         const float2 c1 = both(-rs * s.x * inv_d), c2 = both(-rs * s.y * inv_d);
@@ -512,7 +521,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 if (r < rows) mu = mean[r], rs = rstd[r];
                 row(p, p + per / sizeof(T), p + o_y / sizeof(T), p + o_r / sizeof(T), to, in, m, s);
             }
-            if (W == 1) __syncthreads();
+            if (L <= 32) __syncthreads();
             if (threadIdx.x == 0 && ok && k + ring.stages < count) fill(k + ring.stages, slot);
             if (++slot == ring.stages) slot = 0, parity ^= 1;
         }
@@ -620,32 +629,37 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// Calls f with the element and warp counts that a row of d elements takes: as
-// few warps as hold it at 32 elements per lane (forward) or 16 (backward, which
-// keeps two sums per element besides).
-template <int E, int W>
+// Calls f with the element and lane counts that a row of d elements takes: as few lanes as
+// hold it at 32 elements each (forward) or 16 (backward, which keeps two sums per element
+// besides), and short rows several to a warp (400000 x 64 bf16: forward 26 us, backward 37,
+// with a warp to each row 102 and 115).
+template <int E, int L>
 struct Pick {
-    static constexpr int e = E, w = W;
+    static constexpr int e = E, l = L;
 };
 template <typename F>
 cudaError_t pick_fwd(int d, F f) {
-    if (d <= 256) return f(Pick<8, 1>());
-    if (d <= 512) return f(Pick<16, 1>());
-    if (d <= 1024) return f(Pick<32, 1>());
-    if (d <= 2048) return f(Pick<32, 2>());
-    if (d <= 4096) return f(Pick<32, 4>());
-    if (d <= 8192) return f(Pick<32, 8>());
-    return f(Pick<32, 16>());
+    if (d <= 64) return f(Pick<8, 8>());
+    if (d <= 128) return f(Pick<8, 16>());
+    if (d <= 256) return f(Pick<8, 32>());
+    if (d <= 512) return f(Pick<16, 32>());
+    if (d <= 1024) return f(Pick<32, 32>());
+    if (d <= 2048) return f(Pick<32, 64>());
+    if (d <= 4096) return f(Pick<32, 128>());
+    if (d <= 8192) return f(Pick<32, 256>());
+    return f(Pick<32, 512>());
 }
 template <typename F>
 cudaError_t pick_bwd(int d, F f) {
-    if (d <= 256) return f(Pick<8, 1>());
-    if (d <= 512) return f(Pick<16, 1>());
-    if (d <= 1024) return f(Pick<16, 2>());
-    if (d <= 2048) return f(Pick<16, 4>());
-    if (d <= 4096) return f(Pick<16, 8>());
-    if (d <= 8192) return f(Pick<16, 16>());
-    return f(Pick<16, 32>());
+    if (d <= 64) return f(Pick<8, 8>());
+    if (d <= 128) return f(Pick<8, 16>());
+    if (d <= 256) return f(Pick<8, 32>());
+    if (d <= 512) return f(Pick<16, 32>());
+    if (d <= 1024) return f(Pick<16, 64>());
+    if (d <= 2048) return f(Pick<16, 128>());
+    if (d <= 4096) return f(Pick<16, 256>());
+    if (d <= 8192) return f(Pick<16, 512>());
+    return f(Pick<16, 1024>());
 }
 
 // Calls f with the vector length of rows of d elements.
@@ -671,8 +685,8 @@ template <typename T>
 BwdGrid bwd_grid(long long rows, int d) {
     BwdGrid g = {};
     pick_bwd(d, [&](auto k) {
-        constexpr int E = decltype(k)::e, W = decltype(k)::w, R = Shape<W>::R;
-        const long long most = (long long)bwd_ctas<E, W>() * current_sm_count();
+        constexpr int E = decltype(k)::e, L = decltype(k)::l, R = Shape<L>::R;
+        const long long most = (long long)bwd_ctas<E, L>() * current_sm_count();
         // as many rows as fill the CTA, start at 16 bytes, and make 4 KB where there are many
         g.stage = R;
         while ((long long)g.stage * d * sizeof(T) % 16) g.stage *= 2;
@@ -680,11 +694,11 @@ BwdGrid bwd_grid(long long rows, int d) {
         int by = R;
         pick_width<T>(d, [&](auto v) {
             constexpr int V = decltype(v)::v;
-            using C = Columns<T, V, W>;
+            using C = Columns<T, V, L>;
             // (two stages of four tensors may not fit: then the rows are dealt one by one)
             if (rows <= C::ROWS)
                 g.columns = (d + C::C - 1) / C::C;
-            else if (takes_ring<T, V, W>() && (size_t)(g.stage * 4 * 2 + 1) * d * sizeof(T) <= kRingRoom / bwd_ctas<E, W>())
+            else if (takes_ring<T, V, L>() && (size_t)(g.stage * 4 * 2 + 1) * d * sizeof(T) <= kRingRoom / bwd_ctas<E, L>())
                 by = g.stage;
             return 0;
         });
@@ -700,10 +714,11 @@ cudaError_t ln_fwd(const void* x, const void* y, const void* gamma, const void* 
                    float eps, void* out, float* mean, float* rstd, cudaStream_t stream) {
     if (rows <= 0) return cudaSuccess;
     return pick_fwd(d, [&](auto k) {
-        constexpr int E = decltype(k)::e, W = decltype(k)::w;
-        const long long ctas = (rows + Shape<W, 128>::R - 1) / Shape<W, 128>::R;
+        constexpr int E = decltype(k)::e, L = decltype(k)::l;
+        using S = Shape<L, fwd_threads<E>()>;
+        const long long ctas = (rows + S::R - 1) / S::R;
         if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-        return launch_pdl(ln_fwd_kernel<T, V, E, W>, (unsigned)ctas, (unsigned)Shape<W, 128>::THREADS, 0, stream,
+        return launch_pdl(ln_fwd_kernel<T, V, E, L>, (unsigned)ctas, (unsigned)S::THREADS, 0, stream,
                           static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(gamma),
                           static_cast<const T*>(beta), rows, d, 1.f / d, eps, static_cast<T*>(out), mean, rstd);
     });
@@ -716,8 +731,8 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
     // (no rows: CTAs that add nothing write the zeros)
     const BwdGrid grid = bwd_grid<T>(rows, d);
     const cudaError_t e = pick_bwd(d, [&](auto k) {
-        constexpr int E = decltype(k)::e, W = decltype(k)::w;
-        using S = Shape<W>;
+        constexpr int E = decltype(k)::e, L = decltype(k)::l;
+        using S = Shape<L>;
         auto go = [&](auto kern, size_t dynamic, Ring ring) {
             return launch_pdl(kern, (unsigned)(grid.rows + grid.columns), (unsigned)S::THREADS, dynamic, stream,
                               static_cast<const T*>(dout), static_cast<const T*>(x), static_cast<const T*>(y),
@@ -725,26 +740,26 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
                               static_cast<T*>(dx), grid.rows, part, dgamma, dbeta, ring, status);
         };
         if (grid.columns)
-            return go(ln_bwd_kernel<T, V, E, W, kFew>, S::THREADS / 32 * 2 * Columns<T, V, W>::C * sizeof(float), Ring{});
+            return go(ln_bwd_kernel<T, V, E, L, kFew>, S::THREADS / 32 * 2 * Columns<T, V, L>::C * sizeof(float), Ring{});
         const size_t fold = S::R > 1 ? S::THREADS * E * sizeof(float) : 0;
         const size_t stage = (size_t)grid.stage * d * sizeof(T) * (2 + (y != nullptr) + (dres != nullptr));
-        if constexpr (takes_ring<T, V, W>()) {
-            constexpr size_t kRoom = kRingRoom / bwd_ctas<E, W>();
+        if constexpr (takes_ring<T, V, L>()) {
+            constexpr size_t kRoom = kRingRoom / bwd_ctas<E, L>();
             const size_t own = (size_t)d * sizeof(T), most = kRoom > own ? (kRoom - own) / stage : 0;
             const int stages = (int)(most < kMaxStages ? most : kMaxStages);
             if (stages >= 2) {
                 static PerDeviceOnce attrs;
                 const cudaError_t set = attrs.run([] {
-                    return cudaFuncSetAttribute(ln_bwd_kernel<T, V, E, W, kRing>,
+                    return cudaFuncSetAttribute(ln_bwd_kernel<T, V, E, L, kRing>,
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
                 });
                 if (set != cudaSuccess) return set;
                 const size_t bytes = stage * stages + own;
-                return go(ln_bwd_kernel<T, V, E, W, kRing>, bytes > fold ? bytes : fold,
+                return go(ln_bwd_kernel<T, V, E, L, kRing>, bytes > fold ? bytes : fold,
                           Ring{grid.stage, stages, (int)(stage * stages)});
             }
         }
-        return go(ln_bwd_kernel<T, V, E, W, kPlain>, fold, Ring{});
+        return go(ln_bwd_kernel<T, V, E, L, kPlain>, fold, Ring{});
     });
     if (e != cudaSuccess || grid.columns) return e;
     return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, 0, stream, part, grid.rows, d, dgamma, dbeta);
