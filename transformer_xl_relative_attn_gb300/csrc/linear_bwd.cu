@@ -301,6 +301,16 @@ __device__ __forceinline__ uint4 lb_ld_shared_v4(uint32_t addr) {
     return v;
 }
 
+// 16 bytes that are read once, past L1: beside 230 KB of shared memory L1 is too small for
+// the loads on their way to wait in (base512's second feed-forward layer 49.5 us through L1,
+// 47.9 past it).
+__device__ __forceinline__ uint4 lb_load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 // Eight bf16 onto eight sums; eight sums to memory.
 __device__ __forceinline__ void lb_add8(float (&a)[8], const uint4& v) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
@@ -487,7 +497,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
 #pragma unroll 8
                     for (long long r = r0; r < r1; ++r) {
                         if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.dy + r * p.N + n));
+                        const uint4 v = lb_load_once(p.dy + r * p.N + n);
                         lb_add8(a, v);
                     }
                     lb_put8(p.db + (size_t)part * p.N + n, a);
@@ -503,7 +513,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             v[i] = r + 16 * i < end && TXL_BOUNDS(n + 8 <= p.N, 804, n)
-                                       ? __ldg(reinterpret_cast<const uint4*>(p.dy + (long long)(r + 16 * i) * p.N + n))
+                                       ? lb_load_once(p.dy + (long long)(r + 16 * i) * p.N + n)
                                        : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) lb_add8(a, v[i]);
@@ -621,8 +631,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
         auto fetch = [&](uint4 (&x4)[8], const Lines& l, int sl) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                x4[i] = line_in(l, sl, i) ? __ldg(reinterpret_cast<const uint4*>(
-                                                p.x + l.at + sl * slice_stride + (long long)(4 * i) * row_stride))
+                x4[i] = line_in(l, sl, i) ? lb_load_once(p.x + l.at + sl * slice_stride + (long long)(4 * i) * row_stride)
                                           : make_uint4(0, 0, 0, 0);
         };
         auto mask_of = [&](uint4 (&x4)[8], uint32_t (&keep)[2]) {
