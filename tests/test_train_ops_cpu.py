@@ -73,6 +73,8 @@ def test_linear_bwd_rejects_bad_arguments(lib):
     assert call(B=1 << 20, T=1 << 10) == -2 and call(K=1 << 21) == -2
     assert call(dx=addr(1)) == -4 and call(dw=addr(4), db=addr(4) + 64) == -4 and call(dw=addr(2)) == -4
     assert lib.txl_linear_bwd_workspace_bytes(0, 2, 100, 132, 136, 1, 1, 1) == 0
+    for want in ((0, 0, 0), (0, 0, 1), (1, 0, 0)):                           # no row is reduced over
+        assert lib.txl_linear_bwd_workspace_bytes(0, 2, 5000, 128, 136, *want) == 0, want
 
 
 def table(*entries):

@@ -738,7 +738,7 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
 
 size_t txl_linear_bwd_workspace_bytes(int x_layout, int B, int T, int K, int N, int want_dx, int want_dw,
                                       int want_db) {
-    if (linear_bwd_sizes(x_layout, B, T, K, N) != TXL_OK) return 0;
+    if (linear_bwd_sizes(x_layout, B, T, K, N) != TXL_OK || (!want_dx && !want_dw)) return 0;
     return txl::linear_bwd_workspace_bytes(
         txl::linear_bwd_plan(x_layout == TXL_LAYOUT_HEADS, B, T, K, N, want_dx != 0, want_dw != 0), want_dw && want_db);
 }
