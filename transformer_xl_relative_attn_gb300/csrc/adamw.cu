@@ -436,8 +436,8 @@ __device__ __forceinline__ void adamw_update(const AdamwRaw<P, G, EIGHT>& r, con
 // are issued before it.
 template <typename P, typename G, bool EIGHT, int CAP>
 __global__ void __launch_bounds__(256, EIGHT ? kCtas8 : kCtas32)
-adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks, unsigned per, unsigned first, const AdamwFlat flat,
-             float b1, float b1c, float b2, float b2c, float eps, const AdamwCoef* __restrict__ coef) {
+adamw_kernel(const __grid_constant__ AdamwTable<CAP> t, unsigned n_blocks, unsigned per, unsigned first,
+             const AdamwFlat flat, float b1, float b1c, float b2, float b2c, float eps, const AdamwCoef* __restrict__ coef) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const unsigned warp = threadIdx.x >> 5, b0 = blockIdx.x * per;
@@ -518,8 +518,8 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
         e = each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned) {
             float* to = part + n_part;
             n_part += ctas(n, per);
-            return a.bf16_grad ? launch_pdl(adamw_norm_kernel<__nv_bfloat16, CAP>, ctas(n, per), 256u, stream, t, n, per, to)
-                               : launch_pdl(adamw_norm_kernel<float, CAP>, ctas(n, per), 256u, stream, t, n, per, to);
+            auto go = [&](auto kern) { return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, to); };
+            return a.bf16_grad ? go(adamw_norm_kernel<__nv_bfloat16, CAP>) : go(adamw_norm_kernel<float, CAP>);
         });
         if (e != cudaSuccess) return e;
     }
@@ -530,7 +530,8 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
     return each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned first) {
         auto go = [&](auto kern) {
-            return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, first, flat, b1, b1c, b2, b2c, (float)a.eps, coef);
+            return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, first, flat, b1, b1c, b2, b2c, (float)a.eps,
+                              coef);
         };
         using B = __nv_bfloat16;
         if (a.eight_bit) {

@@ -16,13 +16,13 @@
 // elements per lane, L lanes per row), reduced by shuffles and, with several
 // warps per row, through shared memory, and written once.  Rows of a multiple of 16
 // bytes move as 16-byte vectors, others by 4 or 2 bytes with the same code.
-// The backward pass is persistent: bulk copies bring rows ahead into a ring of stages in
-// shared memory, and each thread keeps its columns' sums of dout xh and dout in registers
-// over all rows of its CTA, so dgamma and dbeta cost no
-// second pass over the rows; the CTAs' sums go to the workspace and a second
-// launch adds them, in a fixed order (the same inputs give the same bits).  With
-// few rows other CTAs of the same launch read the rows again for these sums, column
-// by column, and there is neither second launch nor workspace.
+// The backward pass is persistent: bulk copies bring rows ahead into a ring of
+// stages in shared memory, and each thread keeps its columns' sums of dout xh and
+// dout in registers over all rows of its CTA, so dgamma and dbeta cost no second
+// pass over the rows; the CTAs' sums go to the workspace and a second launch adds
+// them, in a fixed order (the same inputs give the same bits).  With few rows other
+// CTAs of the same launch read the rows again for these sums, column by column, and
+// there is neither second launch nor workspace.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -427,7 +427,8 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                     pair(db, e) = __fadd2_rn(pair(db, e), q);
                 }
                 if (GAMMA_SH && 2 * e % G == 0)
-                    load_row<T, V, G, S::TPR>(gamma_sh + (t + S::TPR * (2 * e / V)) * V, left - S::TPR * (2 * e / V) * V, gam);
+                    load_row<T, V, G, S::TPR>(gamma_sh + (t + S::TPR * (2 * e / V)) * V, left - S::TPR * (2 * e / V) * V,
+                                              gam);
                 q = __fmul2_rn(q, pair(gam, e % (G / 2)));
                 s1 = __fadd2_rn(s1, q);
                 s2 = __ffma2_rn(q, h, s2);
@@ -463,7 +464,8 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
         // that is known from the row's own reduction.
         const long long n_stages = rows / ring.rows;
         const int count = (int)(n_stages > blockIdx.x ? (n_stages - blockIdx.x + row_ctas - 1) / row_ctas : 0);
-        const uint32_t per = (uint32_t)ring.rows * d * sizeof(T), bytes = per * (2 + (y != nullptr) + (dres != nullptr));
+        const uint32_t per = (uint32_t)ring.rows * d * sizeof(T);
+        const uint32_t bytes = per * (2 + (y != nullptr) + (dres != nullptr));
         const uint32_t o_y = 2 * per, o_r = o_y + (y ? per : 0);
         auto fill = [&](int k, int slot) {
             const long long at = ((long long)k * row_ctas + blockIdx.x) * ring.rows * d;
@@ -590,7 +592,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_sum_kernel(const float* __restric
         float2 v[6];
 #pragma unroll
         for (int i = 0; i < 6; ++i)
-            v[i] = p0 + 64 * i < n_part ? *reinterpret_cast<const float2*>(part + (size_t)(p0 + 64 * i) * 2 * d + c) : both(0.f);
+            v[i] = p0 + 64 * i < n_part ? *reinterpret_cast<const float2*>(part + (size_t)(p0 + 64 * i) * 2 * d + c)
+                                        : both(0.f);
 #pragma unroll
         for (int i = 0; i < 6; ++i) a = __fadd2_rn(a, v[i]);
     }
@@ -698,7 +701,8 @@ BwdGrid bwd_grid(long long rows, int d) {
             // (two stages of four tensors may not fit: then the rows are dealt one by one)
             if (rows <= C::ROWS)
                 g.columns = (d + C::C - 1) / C::C;
-            else if (takes_ring<T, V, L>() && (size_t)(g.stage * 4 * 2 + 1) * d * sizeof(T) <= kRingRoom / bwd_ctas<E, L>())
+            else if (takes_ring<T, V, L>() &&
+                     (size_t)(g.stage * 4 * 2 + 1) * d * sizeof(T) <= kRingRoom / bwd_ctas<E, L>())
                 by = g.stage;
             return 0;
         });
@@ -740,7 +744,8 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
                               static_cast<T*>(dx), grid.rows, part, dgamma, dbeta, ring, status);
         };
         if (grid.columns)
-            return go(ln_bwd_kernel<T, V, E, L, kFew>, S::THREADS / 32 * 2 * Columns<T, V, L>::C * sizeof(float), Ring{});
+            return go(ln_bwd_kernel<T, V, E, L, kFew>, S::THREADS / 32 * 2 * Columns<T, V, L>::C * sizeof(float),
+                      Ring{});
         const size_t fold = S::R > 1 ? S::THREADS * E * sizeof(float) : 0;
         const size_t stage = (size_t)grid.stage * d * sizeof(T) * (2 + (y != nullptr) + (dres != nullptr));
         if constexpr (takes_ring<T, V, L>()) {
@@ -762,7 +767,8 @@ cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* g
         return go(ln_bwd_kernel<T, V, E, L, kPlain>, fold, Ring{});
     });
     if (e != cudaSuccess || grid.columns) return e;
-    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, 0, stream, part, grid.rows, d, dgamma, dbeta);
+    return launch_pdl(ln_bwd_sum_kernel, (unsigned)((2 * d + 31) / 32), 1024u, 0, stream, part, grid.rows, d, dgamma,
+                      dbeta);
 }
 
 }  // namespace

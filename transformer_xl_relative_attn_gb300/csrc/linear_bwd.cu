@@ -403,7 +403,8 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     const int m = it.m0 + BM * rank, k = it.k0 + 128 * rank;  // this CTA's share
                     uint32_t a, b, bar;
                     if (dw) {
-                        const int m_el = n64 ? 0 : m, m_sl = n64 ? m >> 6 : 0, k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
+                        const int m_el = n64 ? 0 : m, m_sl = n64 ? m >> 6 : 0;
+                        const int k_el = k64 ? 0 : k, k_sl = k64 ? k >> 6 : 0;
                         int bt = it.s0 / p.t_steps, t = (it.s0 - bt * p.t_steps) * BR;
                         const int T = p.T;
                         for (int n = it.s1 - it.s0; n > 0 && next_slot(a, b, bar); --n) {
@@ -866,7 +867,8 @@ LbPlan linear_bwd_plan(int heads, int B, int T, int K, int N, bool want_dx, bool
     }
     // row ranges of db: as many as give each of the two summing warps per CTA one
     const long long rows = (long long)B * T, groups = (N + 255) / 256;
-    p.db_rows = rows <= (p.splits > 1 ? kDbOnceSplit : kDbOnce) ? 0 : (int)std::max(1ll, std::min(2ll * pl.grid / groups, rows / 16));
+    const long long parts = std::max(1ll, std::min(2ll * pl.grid / groups, rows / 16));
+    p.db_rows = rows <= (p.splits > 1 ? kDbOnceSplit : kDbOnce) ? 0 : (int)parts;
     return pl;
 }
 
