@@ -194,9 +194,12 @@ def _stream(stream, device) -> int:
 def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device=None) -> None:
     """Type, device, dtype, shape and contiguity of one argument.  ``device``:
     the device every tensor of the call must share (the kernels run there)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and
-            (device is None or t.device == device)):
-        return
+    try:  # the few attributes that tell (a CPU tensor's get_device is -1)
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+                (t.is_cuda if device is None else t.get_device() == device.index)):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if device is not None and t.device != device:
