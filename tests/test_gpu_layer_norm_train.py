@@ -223,3 +223,20 @@ def test_nothing_behind_the_rows_is_written():
     txl.layer_norm_bwd(t["dout"], t["x"], t["gamma"], torch.zeros(rows, device="cuda"),
                        torch.ones(rows, device="cuda"), grads=grads)
     assert bool((big[rows * d:] == 7).all())
+
+
+def test_workspace_of_many_rows_is_checked():
+    """Many rows need a workspace: a given one is used up to its end and not beyond, and a
+    smaller one is refused."""
+    t = to_gpu(make(3001, 260, F32, True, seed=13))
+    need = txl.layer_norm_bwd_workspace_bytes(3001, 260, F32)
+    assert need > 0
+    _, mean, rstd = txl.layer_norm_fwd(t["x"], t["gamma"], t["beta"], y=t["y"])
+    want = txl.layer_norm_bwd(t["dout"], t["x"], t["gamma"], mean, rstd, y=t["y"])
+    ws = torch.full((need + 256,), 7, dtype=torch.uint8, device="cuda")
+    got = txl.layer_norm_bwd(t["dout"], t["x"], t["gamma"], mean, rstd, y=t["y"], workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[k], got[k]) for k in want) and bool((ws[need:] == 7).all())
+    with pytest.raises(txl.TxlError) as e:
+        txl.layer_norm_bwd(t["dout"], t["x"], t["gamma"], mean, rstd, y=t["y"], workspace=ws[:need - 256])
+    assert e.value.code == -7
