@@ -356,8 +356,8 @@ int txl_layer_norm(const void* x, const void* y, const void* gamma, const void* 
  *   dgamma, dbeta [d], summed over the rows in a fixed order (the same inputs
  *   give the same bits; zeros when rows = 0).
  *
- * All pointers 16-byte aligned (TXL_ERR_MISALIGNED; with rows = 0 those of
- * row data are not looked at).  Outputs overlap neither inputs nor each other
+ * All pointers 16-byte aligned (TXL_ERR_MISALIGNED; with rows = 0 only those of
+ * dgamma and dbeta are looked at).  Outputs overlap neither inputs nor each other
  * (TXL_ERR_ALIAS).  workspace: device memory, 256-byte aligned, at least
  * txl_layer_norm_bwd_workspace_bytes(...) bytes (TXL_ERR_WORKSPACE), overlapping
  * no other argument (TXL_ERR_ALIAS); concurrent calls use distinct ones.  0 bytes:

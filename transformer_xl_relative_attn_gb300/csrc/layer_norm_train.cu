@@ -679,8 +679,8 @@ auto pick_width(int d, F f) {
 }
 
 // How the backward pass is launched: CTAs that take rows (one round of resident ones at
-// most), CTAs that take columns (0: the row CTAs sum them, into as many parts), and the
-// rows of a ring's stage.
+// most; none without rows, as a row CTA reads gamma before its first row), CTAs that take
+// columns (0: the row CTAs sum them, into as many parts), and the rows of a ring's stage.
 struct BwdGrid {
     int rows, columns, stage;
 };
@@ -707,7 +707,7 @@ BwdGrid bwd_grid(long long rows, int d) {
             return 0;
         });
         const long long want = (rows + by - 1) / by;
-        g.rows = (int)(want < 1 ? 1 : (want < most ? want : most));
+        g.rows = (int)(want < most ? want : most);
         return cudaSuccess;
     });
     return g;
@@ -732,7 +732,7 @@ template <typename T, int V>
 cudaError_t ln_bwd(const void* dout, const void* x, const void* y, const void* gamma, const float* mean,
                    const float* rstd, const void* dres, long long rows, int d, void* dx, float* dgamma,
                    float* dbeta, float* part, int* status, cudaStream_t stream) {
-    // (no rows: CTAs that add nothing write the zeros)
+    // (no rows: column CTAs that add nothing write the zeros)
     const BwdGrid grid = bwd_grid<T>(rows, d);
     const cudaError_t e = pick_bwd(d, [&](auto k) {
         constexpr int E = decltype(k)::e, L = decltype(k)::l;
