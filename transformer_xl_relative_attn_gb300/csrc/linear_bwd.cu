@@ -54,6 +54,7 @@ namespace lb {
 constexpr int BM = 128;  // rows of a CTA's accumulator
 constexpr int BR = 64;   // reduction per stage
 constexpr int CHAIN = 16;  // stages that one dw accumulator takes
+constexpr int DB_CHAIN = 1024;  // rows that one accumulator of db takes
 constexpr int NTHREADS = 384;
 constexpr uint32_t SZ_BOX = 64 * 64 * 2;  // 64 rows of 64 bf16: 8 KB
 constexpr uint32_t SZ_A = 2 * SZ_BOX;     // 128 of M
@@ -494,14 +495,22 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     const int part = u / groups, n = (u - part * groups) * 256 + lane * 8;  // N is a multiple of 8
                     if (n >= p.N) continue;
                     const long long r0 = rows * part / p.db_rows, r1 = rows * (part + 1) / p.db_rows;
-                    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    // (a wide dy has few ranges, of many rows: a chain of additions ends after
+                    // DB_CHAIN, so that its roundings stay those of DB_CHAIN + rows / DB_CHAIN)
+                    for (long long r = r0; r < r1;) {
+                        const long long end = min(r1, r + DB_CHAIN);
+                        float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-                    for (long long r = r0; r < r1; ++r) {
-                        if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
-                        const uint4 v = lb_load_once(p.dy + r * p.N + n);
-                        lb_add8(a, v);
+                        for (; r < end; ++r) {
+                            if (!TXL_BOUNDS(r < rows && n + 8 <= p.N, 801, r * p.N + n)) continue;
+                            const uint4 v = lb_load_once(p.dy + r * p.N + n);
+                            lb_add8(a, v);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sum[e] += a[e];
                     }
-                    lb_put8(p.db + (size_t)part * p.N + n, a);
+                    lb_put8(p.db + (size_t)part * p.N + n, sum);
                 }
             } else if (p.db) {
                 const int rows = p.B * p.T;
