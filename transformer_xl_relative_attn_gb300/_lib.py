@@ -162,6 +162,13 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}: bf16 or fp32 only")
 
 
+def _index(device):
+    """Ordinal of a device that is neither an int nor a torch.device with one: a name
+    ("cuda:1"); None where it has none, which stands for the current device."""
+    device = torch.device(device) if isinstance(device, str) else device
+    return device.index if isinstance(device, torch.device) and device.type == "cuda" else None
+
+
 def _invoke(device, name: str, *args):
     """Calls C entry point ``name`` with ``device`` current, so that the
     library's launches, its status word and its static scratch are those of
@@ -171,6 +178,8 @@ def _invoke(device, name: str, *args):
         fn = _functions[name] = getattr(load(), name)
     # entering the device's context costs more than the call where it is current already
     index = device if type(device) is int else getattr(device, "index", None)
+    if type(index) is not int:
+        index = _index(device)
     if index is not None and index == torch.cuda.current_device():
         return fn(*args)
     with torch.cuda.device(device):
@@ -185,6 +194,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(stream, device) -> int:
     if stream is None:
         index = device if type(device) is int else getattr(device, "index", None)
+        if type(index) is not int:
+            index = _index(device)
         if _raw_stream is not None and index is not None:
             return _raw_stream(index)
         stream = torch.cuda.current_stream(device)
