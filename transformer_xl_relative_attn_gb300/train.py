@@ -252,7 +252,11 @@ class AdamW:
     the moments as e4m3 codes with one scale per 256 elements, rounded at random
     from ``seed``.  ``stream``: the stream of the steps (default: the current one
     of each call); what is enqueued on the current stream when the optimizer is made
-    is waited for.
+    is waited for.  A first step on a further stream waits for what the constructor
+    enqueued, and the memory of the optimizer is not handed out again before that
+    stream has done with it; gradients, parameters and steps on several streams are the
+    caller's to order.  A captured step waits for nothing outside its graph, and its
+    graph is replayed only while the optimizer lives.
 
     Device values: ``lr`` [1] fp32 (set_lr), ``steps`` [1] int64 (steps done), the
     flat ``master`` (None for fp32 parameters) and states(); parameter i's part of
@@ -314,6 +318,10 @@ class AdamW:
             self.exp_avg_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
             self.exp_avg_sq_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
             self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            made_on = torch.cuda.current_stream(dev)
+            # (made in a capture, the fills run with its replay: no event outside stands for them)
+            self._ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+        self._joined = {made_on.cuda_stream}  # streams whose steps come after the fills above
         self._args = (self._table, n, self._param_dtype, self._grad_dtype, state_bits, _ptr(self.master),
                       self.exp_avg.data_ptr(), _ptr(self.exp_avg_scale), self.exp_avg_sq.data_ptr(),
                       _ptr(self.exp_avg_sq_scale), self.steps.data_ptr(), self.lr.data_ptr(), *self.betas, self.eps,
@@ -324,11 +332,29 @@ class AdamW:
             for p, a in zip(self.params, self.starts):
                 self.master[a:a + p.numel()].copy_(p.reshape(-1))
 
+    def _join(self, handle: int) -> None:
+        """Puts the steps on a further stream behind the constructor's fills, and the
+        release of all memory that they use behind them."""
+        with _on(handle, self.device):
+            if torch.cuda.is_current_stream_capturing():
+                return  # a graph cannot wait for what is outside of it
+            st = torch.cuda.current_stream(self.device)
+        if self._ready is not None:
+            st.wait_event(self._ready)
+        own = [self.lr, self.steps, self.grad_norm, self.master, self._workspace, *self.states()]
+        bound = [torch.empty(0, dtype=torch.uint8, device=self.device).set_(x) for x in self._storages]
+        for t in own + bound:
+            if t is not None:
+                t.record_stream(st)
+        self._joined.add(handle)
+
     def step(self, stream=None) -> None:
         """One step from the gradients as they stand, on ``stream`` (default:
         the constructor's, else the current one)."""
-        st = stream if stream is not None else self._fixed_stream
-        rc = _invoke(self.device, "txl_adamw_step", *self._args, _stream(st, self.device))
+        handle = _stream(stream if stream is not None else self._fixed_stream, self.device)
+        if handle not in self._joined:
+            self._join(handle)
+        rc = _invoke(self.device, "txl_adamw_step", *self._args, handle)
         if rc != 0:
             raise TxlError(rc, "txl_adamw_step")
 
