@@ -89,3 +89,28 @@ def test_an_optimizer_made_in_a_capture():
     opt.step(stream=st)
     torch.cuda.synchronize()
     assert int(opt.steps) == 2 and float((p - 1.0).abs().max()) <= 2 * (16 * U * 2 + 1e-8)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_autograd_notices_a_step(dtype):
+    """Between a forward and its backward pass a step changes the values that the gradient is
+    made from: autograd has to refuse, as after torch's own in-place operations."""
+    p, x = torch.ones(64, dtype=dtype, device="cuda", requires_grad=True), torch.ones(64, dtype=dtype, device="cuda", requires_grad=True)
+    opt = txl.AdamW([p], [torch.ones(64, device="cuda")], lr=0.5)
+    y = (p * x).sum()
+    before = p._version
+    opt.step()
+    assert p._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    (p * x).sum().backward()
+    assert torch.equal(x.grad, p.detach())
+
+
+def test_parameters_made_in_inference_mode():
+    """They have no version counter that counts; steps work on them as before."""
+    with torch.inference_mode():
+        p = torch.ones(64, device="cuda")
+    opt = txl.AdamW([p], [torch.ones(64, device="cuda")], lr=0.5)
+    opt.step()
+    assert float((p - 0.5).abs().max()) <= 16 * U
