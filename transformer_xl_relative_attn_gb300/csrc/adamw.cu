@@ -235,12 +235,13 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
     }
 }
 
-// The step's coefficients, from the partial sums of g g (max_norm = 0: no clipping).
+// The step's coefficients, from the partial sums of g g (clipped = 0: no clipping; max_norm
+// may be 0 all the same, where it is below fp32's range).
 // 1 - b^t = -expm1(t ln b) with ln b from the host: fp32 keeps it to 2^-22 however
 // small, and double precision's pow alone took longer than a small update.
 __global__ void __launch_bounds__(1024) adamw_coef_kernel(const float* __restrict__ part, unsigned n_part,
-                                                          double ln_beta1, double ln_beta2, float max_norm,
-                                                          unsigned seed, const float* lr, long long* steps,
+                                                          double ln_beta1, double ln_beta2, int clipped,
+                                                          float max_norm, unsigned seed, const float* lr, long long* steps,
                                                           float* grad_norm, AdamwCoef* coef) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(1024) adamw_coef_kernel(const float* __restric
     const long long t = *steps + 1;
     const float rate = *lr;
     float s = 0.f;
-    if (max_norm > 0.f) {
+    if (clipped) {
         for (unsigned i = threadIdx.x; i < n_part; i += blockDim.x) s += part[i];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(1024) adamw_coef_kernel(const float* __restric
     }
     if (threadIdx.x != 0) return;
     AdamwCoef c = {1.f, 0.f, 0.f, rate, mix32(seed + (unsigned)t * 0x9E3779B1u), 0};
-    if (max_norm > 0.f) {
+    if (clipped) {
         const float norm = sqrtf(s);
         if (grad_norm) *grad_norm = norm;
         c.skip = !(norm < INFINITY);
@@ -524,7 +525,7 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     e = launch_pdl(adamw_coef_kernel, 1, a.max_norm > 0 ? 1024u : 32u, stream, part, n_part, std::log(a.beta1),
-                   std::log(a.beta2), (float)a.max_norm, a.seed, a.lr, a.steps, a.grad_norm, coef);
+                   std::log(a.beta2), (int)(a.max_norm > 0), (float)a.max_norm, a.seed, a.lr, a.steps, a.grad_norm, coef);
     if (e != cudaSuccess) return e;
     const AdamwFlat flat = {(unsigned)blocks, a.master, a.exp_avg, a.exp_avg_scale, a.exp_avg_sq, a.exp_avg_sq_scale};
     const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
