@@ -428,7 +428,8 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
  * (TXL_ERR_MISALIGNED).  What is written overlaps nothing else
  * (TXL_ERR_ALIAS); gradients may share memory.  workspace as for
  * txl_layer_norm_bwd, of txl_adamw_workspace_bytes(...) bytes.  betas in
- * [0, 1), eps >= 0, max_norm >= 0 and finite (TXL_ERR_INVALID_ARG).
+ * [0, 1), eps 0 or at least 2^-126, max_norm >= 0, both finite
+ * (TXL_ERR_INVALID_ARG).
  */
 typedef struct txl_adamw_tensor {
     void* param;

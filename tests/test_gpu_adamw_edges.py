@@ -32,3 +32,15 @@ def test_max_norm_above_the_range_of_fp32(max_norm):
     opt = txl.AdamW([p], [g], lr=0.5, max_norm=max_norm)
     opt.step()
     assert float((p - 1.5).abs().max()) <= 16 * U * 2 + 1e-8 and int(opt.steps) == 1
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_smallest_eps(bits):
+    """2^-126, the smallest one taken: elements whose gradient is 0 stay, the others move by lr."""
+    p, g = torch.full((1000,), 2.0, device="cuda"), torch.ones(1000, device="cuda")
+    g[::2] = 0.0
+    txl.AdamW([p], [g], lr=0.5, eps=2.0 ** -126, state_bits=bits).step()
+    assert bool((p[::2] == 2.0).all()) and float((p[1::2] - 1.5).abs().max()) <= 16 * U * 2
+    with pytest.raises(txl.TxlError) as e:
+        txl.AdamW([p], [g], lr=0.5, eps=1e-40, state_bits=bits).step()
+    assert e.value.code == -1

@@ -2,6 +2,7 @@
 // argument validation on the host, then one asynchronous launch on the
 // caller's stream.  Nothing here allocates device memory.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -792,6 +793,8 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
         !(max_norm >= 0.0) || !std::isfinite(max_norm))
         return TXL_ERR_INVALID_ARG;
+    // (the update's reciprocal counts an operand below 2^-126 as 0: 0 / eps would be NaN)
+    if (eps > 0.0 && (float)eps < FLT_MIN) return TXL_ERR_INVALID_ARG;
     const long long total = txl_adamw_state_elements(tensors, n_tensors);
     if (total < 0 || !steps || !lr) return TXL_ERR_INVALID_ARG;
     const bool eight = state_bits == 8, bf16 = param_dtype == TXL_BF16;
