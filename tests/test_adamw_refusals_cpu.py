@@ -28,3 +28,16 @@ def test_eps_below_the_normal_numbers_of_fp32(lib, eps):
                                   0.0, 0, None, None, 0, None)
     assert call(eps) == -1
     assert call(0.0) == -7 and call(2.0 ** -126) == -7 and call(1e-8) == -7
+
+
+@pytest.mark.parametrize("pd,bits", [(F32, 32), (BF, 32), (F32, 8), (BF, 8)])
+def test_flat_buffers_of_no_elements_may_be_null(lib, pd, bits):
+    """A list of empty tensors has no state: every type and width passes its checks (here on to
+    the missing workspace), and buffers that the form does not have are still refused."""
+    t = (_lib.AdamwTensor * 2)(_lib.AdamwTensor(None, None, 0, 0.0, 0), _lib.AdamwTensor(None, None, 0, 0.0, 0))
+
+    def call(master=None, ms=None):
+        return lib.txl_adamw_step(t, 2, pd, F32, bits, master, None, ms, None, None, addr(4), addr(5), 0.9, 0.999, 1e-8,
+                                  0.0, 0, None, None, 0, None)
+    assert call() == -7
+    assert call(master=addr(2)) == (-7 if pd == BF else -1) and call(ms=addr(3)) == (-7 if bits == 8 else -1)

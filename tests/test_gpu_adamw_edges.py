@@ -44,3 +44,16 @@ def test_smallest_eps(bits):
     with pytest.raises(txl.TxlError) as e:
         txl.AdamW([p], [g], lr=0.5, eps=1e-40, state_bits=bits).step()
     assert e.value.code == -1
+
+
+@pytest.mark.parametrize("pd", [F32, BF])
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+def test_nothing_but_empty_parameters(pd, bits, max_norm):
+    p = [torch.empty(0, dtype=pd, device="cuda"), torch.empty(3, 0, dtype=pd, device="cuda")]
+    opt = txl.AdamW(p, [torch.empty(0, device="cuda"), torch.empty(3, 0, device="cuda")], lr=0.5, state_bits=bits, max_norm=max_norm)
+    opt.step()
+    opt.load_state_dict(opt.state_dict())
+    opt.step()
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 2 and (max_norm is None or float(opt.grad_norm) == 0.0)

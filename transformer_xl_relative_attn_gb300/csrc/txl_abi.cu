@@ -798,8 +798,9 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
     const long long total = txl_adamw_state_elements(tensors, n_tensors);
     if (total < 0 || !steps || !lr) return TXL_ERR_INVALID_ARG;
     const bool eight = state_bits == 8, bf16 = param_dtype == TXL_BF16;
-    if ((master != nullptr) != bf16 || (exp_avg_scale != nullptr) != eight || (exp_avg_sq_scale != nullptr) != eight ||
-        (total && (!exp_avg || !exp_avg_sq)))
+    // (flat buffers of no elements may be null)
+    if ((master && !bf16) || ((exp_avg_scale || exp_avg_sq_scale) && !eight)) return TXL_ERR_INVALID_ARG;
+    if (total && (!exp_avg || !exp_avg_sq || (bf16 && !master) || (eight && (!exp_avg_scale || !exp_avg_sq_scale))))
         return TXL_ERR_INVALID_ARG;
     for (const void* p : {(const void*)master, (const void*)exp_avg, (const void*)exp_avg_scale,
                           (const void*)exp_avg_sq, (const void*)exp_avg_sq_scale})
