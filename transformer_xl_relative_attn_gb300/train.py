@@ -17,6 +17,7 @@ from ._lib import TXL_BF16, TXL_F32, AdamwTensor, TxlError, _dtype_code, _invoke
 _HERE = contextlib.nullcontext()
 _LINEAR_GRADS = frozenset(("dx", "dw", "db"))
 STATE_BLOCK = 256  # elements of one block of a flat optimizer state
+_INT_MAX = 0x7FFFFFFF  # ctypes cuts a larger size to its low 32 bits without a word
 
 
 def _on(stream, device):
@@ -57,6 +58,8 @@ def _scratch(workspace, need: int, device) -> int:
 @functools.lru_cache(maxsize=1024)
 def _workspace_need(index: int, name: str, *sizes) -> int:
     """Workspace of a call of these sizes on device ``index``: a function of both alone."""
+    if max(sizes) > _INT_MAX:
+        raise TxlError(-2, name)
     return int(_invoke(index, name, *sizes))
 
 
@@ -70,6 +73,8 @@ def _row_args(x, y, gamma):
     d = shape[-1]
     if d == 0:
         raise ValueError("x must have a last axis of at least one element")
+    if d > _INT_MAX:
+        raise TxlError(-2, "last axis of x")
     _need(x, "x", shape, dt)
     if y is not None:
         _need(y, "y", shape, dt, dev)
@@ -114,6 +119,8 @@ def layer_norm_bwd_workspace_bytes(rows, d, dtype=torch.bfloat16, device=None) -
     current one)."""
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
+    if max(rows, d) > _INT_MAX:
+        return 0  # as for every size that the call refuses
     code = TXL_BF16 if dtype is torch.bfloat16 else TXL_F32
     dev = device if device is not None else torch.cuda.current_device()
     return int(_invoke(dev, "txl_layer_norm_bwd_workspace_bytes", rows, d, code))
@@ -178,6 +185,8 @@ def linear_bwd_workspace_bytes(x_shape, N, want=("dx", "dw", "db"), device=None)
     [B, K/64, T, 64] and N output columns, on ``device`` (default: the current
     one; the split depends on its SM count)."""
     layout, B, T, K = _linear_shape(torch.empty(x_shape, device="meta"))
+    if max(B, T, K, N) > _INT_MAX:
+        return 0  # as for every size that the call refuses
     dev = device if device is not None else torch.cuda.current_device()
     return int(_invoke(dev, "txl_linear_bwd_workspace_bytes", layout, B, T, K, N, *("dx" in want, "dw" in want, "db" in want)))
 
