@@ -2,7 +2,7 @@
 
 Each .cu under csrc/ compiles to an object in _build/ in parallel; the objects
 link into transformer_xl_relative_attn_gb300/libtxl.so.  The bounds-checked
-variant (every computed kernel index checked, -DTXL_CHECKED) builds the same
+variant (computed kernel indexes checked, -DTXL_CHECKED) builds the same
 sources into _build/checked/ and libtxl_checked.so.  Rebuilds only what
 changed (object older than its source or any header).
 """

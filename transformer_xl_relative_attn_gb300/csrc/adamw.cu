@@ -165,24 +165,26 @@ __device__ __forceinline__ void store1(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 
 // Elements 0 .. 3 of p, of which `left` are the tensor's (0 behind its end).
-// `full`: the whole block is the tensor's.
+// `full`: the whole block is the tensor's.  at, n: the index of p in its tensor and the
+// tensor's length, for the bounds-checked build alone.
 template <typename T>
-__device__ __forceinline__ void load4_tail(const T* p, bool full, int left, float (&f)[4]) {
-    if (full && TXL_BOUNDS(left >= 4, 1001, left)) {
-        load4(p, f);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = k < left ? load1(p + k) : 0.f;
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store4_tail(T* p, bool full, int left, const float (&f)[4]) {
-    if (full && TXL_BOUNDS(left >= 4, 1002, left)) {
-        store4(p, f);
+__device__ __forceinline__ void load4_tail(const T* p, bool full, int left, long long at, long long n, float (&f)[4]) {
+    if (full) {
+        if (TXL_BOUNDS(at >= 0 && at + 4 <= n, 1001, at)) load4(p, f);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (k < left) store1(p + k, f[k]);
+            f[k] = k < left && TXL_BOUNDS(at >= 0 && at + k < n, 1004, at) ? load1(p + k) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4_tail(T* p, bool full, int left, long long at, long long n, const float (&f)[4]) {
+    if (full) {
+        if (TXL_BOUNDS(at >= 0 && at + 4 <= n, 1002, at)) store4(p, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < left && TXL_BOUNDS(at >= 0 && at + k < n, 1005, at)) store1(p + k, f[k]);
     }
 }
 
@@ -200,11 +202,11 @@ __device__ __forceinline__ int find_entry(const AdamwTable<CAP>& t, unsigned b) 
     return lo;
 }
 
-// Sum of g g over each CTA's blocks: part[blockIdx.x].
+// Sum of g g over each CTA's blocks: part[blockIdx.x] (of n_part left in the workspace).
 template <typename G, int CAP>
 __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__ AdamwTable<CAP> t,
                                                          unsigned n_blocks, unsigned per,
-                                                         float* __restrict__ part) {
+                                                         float* __restrict__ part, unsigned n_part) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sh[8];
@@ -219,8 +221,9 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
         const int left = full ? kAdamwBlock : (int)n - lane * 4;
         const G* const gp = static_cast<const G*>(t.e[e].g) + i + lane * 4;
         float g[2][4];
-        load4_tail(gp, full, left, g[0]);
-        load4_tail(gp + 128, full, left - 128, g[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            load4_tail(gp + 128 * h, full, left - 128 * h, i + lane * 4 + 128 * h, t.e[e].n, g[h]);
 #pragma unroll
         for (int x = 0; x < 8; ++x) s = fmaf(g[x >> 2][x & 3], g[x >> 2][x & 3], s);
     }
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
     if (threadIdx.x == 0) {
         float a = 0.f;
         for (int w = 0; w < 8; ++w) a += sh[w];
-        part[blockIdx.x] = a;
+        if (TXL_BOUNDS(blockIdx.x < n_part, 1006, blockIdx.x)) part[blockIdx.x] = a;
     }
 }
 
@@ -321,6 +324,7 @@ template <typename P, typename G, bool EIGHT>
 struct AdamwRaw {
     P* p;       // the lane's first element
     int left;   // elements of the tensor from there on, kAdamwBlock where the whole block is its
+    long long i, n;  // index of p in its tensor, whose length is n (bounds-checked build)
     float wd;
     unsigned blk;  // block of the flat buffers
     float g[8], w[8];
@@ -339,6 +343,8 @@ __device__ __forceinline__ void adamw_load(const AdamwTable<CAP>& t, int& e, uns
     const bool full = n >= kAdamwBlock;
     r.left = full ? kAdamwBlock : (int)n - lane * 4;
     r.p = static_cast<P*>(t.e[e].p) + i + lane * 4;
+    r.i = i + lane * 4;
+    r.n = t.e[e].n;
     r.wd = t.e[e].wd;
     r.blk = first + b;
     if (!TXL_BOUNDS(r.blk < flat.blocks, 1003, r.blk)) r.blk = 0;
@@ -346,11 +352,11 @@ __device__ __forceinline__ void adamw_load(const AdamwTable<CAP>& t, int& e, uns
     const size_t at = (size_t)r.blk * kAdamwBlock + lane * 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        load4_tail(gp + 128 * h, full, r.left - 128 * h, *reinterpret_cast<float(*)[4]>(r.g + 4 * h));
+        load4_tail(gp + 128 * h, full, r.left - 128 * h, r.i + 128 * h, r.n, *reinterpret_cast<float(*)[4]>(r.g + 4 * h));
         if (MASTER)
             load4(flat.master + at + 128 * h, *reinterpret_cast<float(*)[4]>(r.w + 4 * h));
         else
-            load4_tail(reinterpret_cast<const float*>(r.p) + 128 * h, full, r.left - 128 * h,
+            load4_tail(reinterpret_cast<const float*>(r.p) + 128 * h, full, r.left - 128 * h, r.i + 128 * h, r.n,
                        *reinterpret_cast<float(*)[4]>(r.w + 4 * h));
         if constexpr (EIGHT) {
             r.mc[h] = *reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(flat.m) + at + 128 * h);
@@ -403,7 +409,7 @@ __device__ __forceinline__ void adamw_update(const AdamwRaw<P, G, EIGHT>& r, con
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float(&p4)[4] = *reinterpret_cast<const float(*)[4]>(p + 4 * h);
-        store4_tail(r.p + 128 * h, full, r.left - 128 * h, p4);
+        store4_tail(r.p + 128 * h, full, r.left - 128 * h, r.i + 128 * h, r.n, p4);
         if (MASTER) store4(flat.master + at + 128 * h, p4);
     }
     if constexpr (EIGHT) {
@@ -508,6 +514,12 @@ cudaError_t each_group(const AdamwArgs& a, F f) {
     return err;
 }
 
+constexpr int kSmallTable = 32, kLargeTable = 480;
+
+// One partial sum per CTA of each group of tensors (a group's last CTA may be partly
+// filled: one more per group at most).
+long long part_count(long long blocks) { return blocks / 8 + blocks / kSmallTable + 2; }
+
 template <int CAP>
 cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     AdamwCoef* coef = static_cast<AdamwCoef*>(a.workspace);
@@ -518,8 +530,9 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     if (a.max_norm > 0) {
         e = each_group<CAP>(a, [&](const AdamwTable<CAP>& t, unsigned n, unsigned) {
             float* to = part + n_part;
+            const unsigned room = (unsigned)(part_count(blocks) - n_part);
             n_part += ctas(n, per);
-            auto go = [&](auto kern) { return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, to); };
+            auto go = [&](auto kern) { return launch_pdl(kern, ctas(n, per), 256u, stream, t, n, per, to, room); };
             return a.bf16_grad ? go(adamw_norm_kernel<__nv_bfloat16, CAP>) : go(adamw_norm_kernel<float, CAP>);
         });
         if (e != cudaSuccess) return e;
@@ -544,8 +557,6 @@ cudaError_t run(const AdamwArgs& a, long long blocks, cudaStream_t stream) {
     });
 }
 
-constexpr int kSmallTable = 32, kLargeTable = 480;
-
 }  // namespace
 
 long long adamw_blocks(const txl_adamw_tensor* tensors, int n_tensors) {
@@ -555,11 +566,7 @@ long long adamw_blocks(const txl_adamw_tensor* tensors, int n_tensors) {
     return b;
 }
 
-// Coefficients, and one partial sum per CTA of each group of tensors (a group's
-// last CTA may be partly filled: one more per group at most).
-size_t adamw_workspace_bytes(long long blocks) {
-    return coef_bytes() + (size_t)(blocks / 8 + blocks / kSmallTable + 2) * sizeof(float);
-}
+size_t adamw_workspace_bytes(long long blocks) { return coef_bytes() + (size_t)part_count(blocks) * sizeof(float); }
 
 cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream) {
     const long long blocks = adamw_blocks(a.tensors, a.n_tensors);

@@ -97,6 +97,13 @@ __device__ __forceinline__ void store_sums(float* p, const float* f) {
     }
 }
 
+// Dynamic shared memory of this launch (bounds-checked build).
+[[maybe_unused]] __device__ __forceinline__ uint32_t dynamic_bytes() {
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
+}
+
 // Two fp32 operations per instruction: the rows' arithmetic, not memory, bounded these
 // kernels one element at a time (forward, bf16: 18 instructions per element, 68 % of the
 // issue slots).  Arrays of E floats are taken as pairs.
@@ -316,7 +323,8 @@ __device__ __forceinline__ void ln_bwd_columns(const T* __restrict__ dout, const
         }
     }
     const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) < S::CL) {
+    if ((threadIdx.x & 31) < S::CL &&
+        TXL_BOUNDS((warp + 1) * 2 * S::C * sizeof(float) <= dynamic_bytes() && cl * V + V <= S::C, 912, warp)) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             sh[warp * 2 * S::C + cl * V + k] = dg[k];
@@ -394,7 +402,8 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
     const int left = d - t * V;
     T* const gamma_sh = reinterpret_cast<T*>(dynamic + ring.gamma);
     if constexpr (GAMMA_SH) {
-        for (int i = threadIdx.x; i < d; i += S::THREADS) gamma_sh[i] = gamma[i];
+        for (int i = threadIdx.x; i < d; i += S::THREADS)
+            if (TXL_BOUNDS(ring.gamma + (i + 1) * sizeof(T) <= dynamic_bytes(), 911, i)) gamma_sh[i] = gamma[i];
     } else {
         load_row<T, V, E, S::TPR>(gamma + t * V, left, gam);
     }
@@ -469,7 +478,9 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
         const uint32_t o_y = 2 * per, o_r = o_y + (y ? per : 0);
         auto fill = [&](int k, int slot) {
             const long long at = ((long long)k * row_ctas + blockIdx.x) * ring.rows * d;
-            if (!TXL_BOUNDS(at + (long long)ring.rows * d <= rows * d, 905, at)) return;
+            if (!TXL_BOUNDS(at + (long long)ring.rows * d <= rows * d, 905, at) ||
+                !TXL_BOUNDS((slot + 1) * bytes <= dynamic_bytes(), 909, slot))
+                return;
             unsigned char* const to = dynamic + slot * bytes;
             mbar_expect_tx(&full[slot], bytes);
             bulk_load(to, x + at, per, &full[slot]);
@@ -497,6 +508,9 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 n = rest;
                 const long long at = n_stages * ring.rows * d;
                 for (int i = threadIdx.x; i < n * d; i += S::THREADS) {
+                    if (!TXL_BOUNDS(at + i < rows * d && (i + 1) * sizeof(T) <= per && (slot + 1) * bytes <= dynamic_bytes(), 910,
+                                    at + i))
+                        continue;
                     st[i] = x[at + i];
                     st[i + per / sizeof(T)] = dout[at + i];
                     if (y) st[i + o_y / sizeof(T)] = y[at + i];
@@ -549,7 +563,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
         for (int half = S::R / 2; half > 0; half >>= 1) {
             __syncthreads();
             const int n = half * S::TPR;
-            if (lr >= half && lr < 2 * half) {
+            if (lr >= half && lr < 2 * half && TXL_BOUNDS(2 * E * n * sizeof(float) <= dynamic_bytes(), 907, n)) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     fold[(2 * e) * n + threadIdx.x - n] = dg[e];
@@ -557,7 +571,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
                 }
             }
             __syncthreads();
-            if (lr < half) {
+            if (lr < half && TXL_BOUNDS(2 * E * n * sizeof(float) <= dynamic_bytes(), 908, n)) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     dg[e] += fold[(2 * e) * n + threadIdx.x];
@@ -571,7 +585,7 @@ ln_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ x, const T* __re
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
         const int c = (t + S::TPR * i) * V;
-        if (c < d) {
+        if (c < d && TXL_BOUNDS(c + V <= d && (int)blockIdx.x < row_ctas, 906, c)) {
             store_sums<V>(to + c, dg + V * i);
             store_sums<V>(to + d + c, db + V * i);
         }
@@ -592,8 +606,9 @@ __global__ void __launch_bounds__(1024) ln_bwd_sum_kernel(const float* __restric
         float2 v[6];
 #pragma unroll
         for (int i = 0; i < 6; ++i)
-            v[i] = p0 + 64 * i < n_part ? *reinterpret_cast<const float2*>(part + (size_t)(p0 + 64 * i) * 2 * d + c)
-                                        : both(0.f);
+            v[i] = p0 + 64 * i < n_part && TXL_BOUNDS(c + 2 <= 2 * d, 913, c)
+                       ? *reinterpret_cast<const float2*>(part + (size_t)(p0 + 64 * i) * 2 * d + c)
+                       : both(0.f);
 #pragma unroll
         for (int i = 0; i < 6; ++i) a = __fadd2_rn(a, v[i]);
     }

@@ -510,7 +510,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) sum[e] += a[e];
                     }
-                    lb_put8(p.db + (size_t)part * p.N + n, sum);
+                    if (TXL_BOUNDS(n + 8 <= p.N && part < p.db_rows, 805, n)) lb_put8(p.db + (size_t)part * p.N + n, sum);
                 }
             } else if (p.db) {
                 const int rows = p.B * p.T;
@@ -532,7 +532,7 @@ linear_bwd_kernel(const __grid_constant__ LbMaps maps, const LbParams p) {
                     for (int o = 2; o < 32; o <<= 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
-                    if (lane < 2 && n < p.N) lb_put8(p.db + n, a);
+                    if (lane < 2 && n < p.N && TXL_BOUNDS(n + 8 <= p.N, 806, n)) lb_put8(p.db + n, a);
                 }
             }
         }
@@ -756,6 +756,7 @@ __global__ void __launch_bounds__(256) linear_bwd_sum_kernel(const float* __rest
         float4 a = q[0];
 #pragma unroll 4
         for (int s = 1; s < splits; ++s) {
+            if (!TXL_BOUNDS(i + s * n4 < n4 * splits, 807, i + s * n4)) continue;
             const float4 b = q[s * n4];
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
@@ -767,7 +768,8 @@ __global__ void __launch_bounds__(256) linear_bwd_sum_kernel(const float* __rest
     float a = 0.f;
     if (n < N) {
 #pragma unroll 8
-        for (int r = w; r < db_rows; r += 8) a += db_part[(size_t)r * N + n];
+        for (int r = w; r < db_rows; r += 8)
+            if (TXL_BOUNDS((long long)r * N + n < (long long)db_rows * N, 808, n)) a += db_part[(size_t)r * N + n];
     }
     sh[w][lane] = a;
     __syncthreads();

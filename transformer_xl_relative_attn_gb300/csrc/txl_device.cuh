@@ -13,9 +13,10 @@
 namespace txl {
 
 // ---------------------------------------------------------------- bounds checks
-// Built with -DTXL_CHECKED, every computed global index and every computed
-// shared-memory address of the kernels goes through TXL_BOUNDS(cond, site,
-// index): an access whose condition fails is skipped (no trap) and the first
+// Built with -DTXL_CHECKED, the computed global indexes and shared-memory
+// addresses of the kernels go through TXL_BOUNDS(cond, site, index), but for those
+// that the code itself compares with the same bound just before the access (a row
+// below the row count) and those fixed by the thread's index alone: an access whose condition fails is skipped (no trap) and the first
 // violation of the translation unit is recorded as (1 << 63) | (site << 40)
 // | (index & (2^40 - 1)) in a device word that txl_bounds_status() reads and
 // clears.  Without the flag the macro is the constant true and compiles away.
