@@ -376,7 +376,8 @@ int txl_layer_norm_bwd(const void* dout, const void* x, const void* y, const voi
  * [B, T, K] (TXL_LAYOUT_ROWS) or [B, K/64, T, 64] (TXL_LAYOUT_HEADS), w [N, K]:
  *   dx = dy W, bf16 in x's layout (an attention output's gradient comes out in
  *        the layout txl_attn_bwd takes as dout); with relu_in, where x is the
- *        output of a ReLU, times [x > 0]: the gradient of the ReLU's input
+ *        output of a ReLU, the gradient of the ReLU's input: exactly 0 where x
+ *        is not above 0 (a NaN among them), whatever dy and W hold
  *   dw = dy^T x, fp32 [N, K];  db = sum of dy over the rows, fp32 [N]
  * dx may be null, db may be null, dw may be null if db is (TXL_ERR_INVALID_ARG:
  * db without dw, or nothing asked for).  Sums over rows are added in a fixed

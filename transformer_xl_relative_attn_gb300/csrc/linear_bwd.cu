@@ -1,7 +1,7 @@
 // Gradients of a Linear layer out = x W^T + b on the sm_103a tensor cores, bf16
 // in, fp32 accumulation:
 //
-//   dx = dy W          [T, K] = [T, N] [N, K]   bf16 (where x came out of a ReLU: times [x > 0])
+//   dx = dy W          [T, K] = [T, N] [N, K]   bf16 (where x came out of a ReLU: 0 unless x > 0)
 //   dw = dy^T x        [N, K] = [N, T] [T, K]   fp32
 //   db = sum over rows of dy                    fp32
 //
@@ -13,8 +13,8 @@
 // Two CTAs of a cluster share a 256 x 256 tile (cta_group::2), or one CTA takes 128 x
 // 128 where the larger tiles would leave SMs idle.
 //
-// The ReLU mask is a factor of the epilogue of dx, read from x before the tile's
-// MMAs end.  db is summed by two warps of every CTA that have no part in the products,
+// The ReLU mask is applied in the epilogue of dx (by bits: a masked element is 0 also where
+// the product is not finite), read from x before the tile's MMAs end.  db is summed by two warps of every CTA that have no part in the products,
 // from dy in global memory (L2 mostly: the products read it at the same time).
 //
 // dw has few tiles and a long reduction (base512's second feed-forward layer: 16

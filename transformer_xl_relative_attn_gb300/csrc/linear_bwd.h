@@ -32,7 +32,7 @@ struct LbPlan {
     LbParams p;
 };
 
-// dx = dy W (times [x > 0] if relu), dw = dy^T x, db = column sums of dy.  x and
+// dx = dy W (0 unless x > 0 if relu), dw = dy^T x, db = column sums of dy.  x and
 // dx [B, T, K] (heads = 0) or [B, K / 64, T, 64]; dy [B, T, N]; w [N, K].  dx, or
 // dw with db, may be null; db alone may be null.  K and N multiples of 8, of 64 for
 // K with heads.  cudaErrorInvalidValue: a tensor map could not be encoded.
