@@ -114,3 +114,18 @@ def test_parameters_made_in_inference_mode():
     opt = txl.AdamW([p], [torch.ones(64, device="cuda")], lr=0.5)
     opt.step()
     assert float((p - 0.5).abs().max()) <= 16 * U
+
+
+def test_made_on_a_side_stream_and_stepped_on_the_default_one():
+    n = 1 << 16
+    big, st = torch.empty(1 << 28, device="cuda"), torch.cuda.Stream()
+    p, g = torch.full((n,), 2.0, dtype=BF, device="cuda"), torch.ones(n, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        busy(big)
+        opt = txl.AdamW([p], [g], lr=0.5)
+    opt.step()
+    opt.step(stream=torch.cuda.default_stream())
+    opt.step(stream=0)
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 3 and float((opt.master - 0.5).abs().max()) <= 3 * (16 * U * 2 + 1e-8)

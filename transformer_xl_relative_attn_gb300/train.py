@@ -27,7 +27,9 @@ def _on(stream, device):
     if stream is None:
         return _HERE
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # (torch takes a null handle for none given, and makes a stream of its own for it)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 
