@@ -262,7 +262,8 @@ class AdamW:
     was computed from the old values (a graph's replay moves none).  ``weight_decay``: one
     number, or one per parameter.  ``max_norm``: gradients are scaled by
     min(1, max_norm / norm), norm the 2-norm of all of them, kept in ``grad_norm``
-    [1]; a norm that is not finite makes the step change nothing.  ``state_bits`` 8:
+    [1]; a norm that is not finite makes the step change nothing.  ``eps``: 0, or at
+    least 2^-126.  ``state_bits`` 8:
     the moments as e4m3 codes with one scale per 256 elements, rounded at random
     from ``seed``.  ``stream``: the stream of the steps (default: the current one
     of each call); what is enqueued on the current stream when the optimizer is made
