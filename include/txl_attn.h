@@ -396,6 +396,40 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
                    int relu_in, void* dx, float* dw, float* db, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * txl_token_logprobs: from logits x of `rows` rows of V (row r at logits + r ld, in
+ * elements, ld >= V) and a token per row (int64; negative: the row has none),
+ *   lse[r] = ln sum e^x,  logprob[r] = x_token - lse (0 without a token, NaN for a
+ *   token >= V),  entropy[r] = -sum p ln p with p = e^(x - lse);
+ *   with 0 < top <= min(V, 32): top_index[r, i], the indexes of the `top` largest
+ *   logits in their order, of equal ones the lower index first (NaN above all others),
+ *   and top_logprob[r, i] = x - lse.  top = 0: both null.
+ * fp32 arithmetic, each logit read once; logits of dtype TXL_BF16 or TXL_F32, results
+ * fp32, indexes int64.  A row of nothing but -inf: lse, logprob and top_logprob -inf,
+ * entropy 0.  A row that holds a NaN or +inf: lse, logprob (of a token), entropy and
+ * top_logprob NaN.
+ * txl_token_logprobs_bwd: with the gradients of logprob, lse and entropy (fp32 [rows],
+ * each may be null: zeros, but not all three),
+ *   dx_j = dlogprob (delta_j,token - p_j) + dlse p_j - dentropy p_j ((x_j - lse) + entropy),
+ * dlogprob taken as 0 where there is no token.  lse and entropy (null without dentropy)
+ * as the forward call gave them.  dlogits (rows ldd elements apart) may be logits with
+ * the same distance of rows: the gradient then takes their place.  A row whose gradients
+ * are all 0 gets zeros whatever its logits hold, as does a row of nothing but -inf;
+ * dlogprob other than 0 at a token >= V makes the row NaN.  What lies between the rows
+ * is left as it was.
+ *
+ * 0 <= rows < 2^31, 1 <= V <= 2^30, rows * max(ld, ldd) <= 2^40 (TXL_ERR_UNSUPPORTED
+ * beyond, as for top > 32; top > V is TXL_ERR_INVALID_ARG).  Pointers need the alignment
+ * of their elements (TXL_ERR_MISALIGNED).  What is written overlaps nothing else
+ * (TXL_ERR_ALIAS), but for dlogits as said.
+ */
+int txl_token_logprobs(const void* logits, long long ld, const long long* tokens, long long rows, int V, int top,
+                       float* logprob, float* lse, float* entropy, long long* top_index, float* top_logprob,
+                       int dtype, void* stream);
+int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* tokens, const float* lse,
+                           const float* entropy, const float* dlogprob, const float* dlse, const float* dentropy,
+                           long long rows, int V, void* dlogits, long long ldd, int dtype, void* stream);
+
+/*
  * txl_adamw_step: one AdamW step over n_tensors tensors.  `tensors` is an array
  * in HOST memory, read during the call; tensor i has n elements (0: skipped),
  * a parameter, a gradient and a weight decay of its own.  With g the gradient

@@ -119,6 +119,10 @@ def load() -> ctypes.CDLL:
         lib.txl_adamw_step.argtypes = ([table] + [i] * 4 + [vp] * 7 + [dbl] * 4 + [ctypes.c_uint] +
                                        [vp, vp, sz, vp])
         lib.txl_adamw_step.restype = i
+        lib.txl_token_logprobs.argtypes = [vp, ll, vp, ll, i, i] + [vp] * 5 + [i, vp]
+        lib.txl_token_logprobs.restype = i
+        lib.txl_token_logprobs_bwd.argtypes = [vp, ll] + [vp] * 6 + [ll, i, vp, ll, i, vp]
+        lib.txl_token_logprobs_bwd.restype = i
         lib.txl_mem_update_ext.argtypes = [vp, vp] + [i] * 6 + [vp]
         lib.txl_mem_update_ext.restype = i
         lib.txl_mem_reset.argtypes = [vp, vp] + [i] * 4 + [vp]

@@ -14,6 +14,7 @@
 #include "adamw.h"
 #include "linear_bwd.h"
 #include "proj_gemm.h"
+#include "token_logprobs.h"
 #include "txl_attn.h"
 #include "txl_device.cuh"
 
@@ -70,6 +71,7 @@ unsigned long long bounds_word_proj_gemm();
 unsigned long long bounds_word_layer_norm_train();
 unsigned long long bounds_word_adamw();
 unsigned long long bounds_word_linear_bwd();
+unsigned long long bounds_word_token_logprobs();
 
 }  // namespace txl
 
@@ -682,6 +684,16 @@ int linear_bwd_sizes(int x_layout, int B, int T, int K, int N) {
     return TXL_OK;
 }
 
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Logits: 2^31 - 1 rows, 2^30 columns and 2^40 elements at most.
+bool logit_rows_too_large(long long rows, int V, long long ld) {
+    return V > (1 << 30) || rows > 0x7FFFFFFFll || ld > (1ll << 40) || rows > (1ll << 40) / ld;
+}
+
+// Bytes from the first row's begin to the last one's end.
+size_t row_span(long long rows, int V, long long ld, int es) { return ((size_t)(rows - 1) * ld + V) * es; }
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_LAUNCH; }
 
 }  // namespace
@@ -765,6 +777,55 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
     if (!status) return TXL_ERR_CUDA;
     return launch_status(txl::launch_linear_bwd(plan, dy, x, w, relu_in != 0, dx, dw, db, workspace, status,
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int txl_token_logprobs(const void* logits, long long ld, const long long* tokens, long long rows, int V, int top,
+                       float* logprob, float* lse, float* entropy, long long* top_index, float* top_logprob,
+                       int dtype, void* stream) {
+    const int es = elem_size(dtype);
+    if (!es || rows < 0 || V <= 0 || ld < V || top < 0 || top > V) return TXL_ERR_INVALID_ARG;
+    if (logit_rows_too_large(rows, V, ld) || top > txl::kTopMost) return TXL_ERR_UNSUPPORTED;
+    if (rows == 0) return TXL_OK;
+    if (!logits || !tokens || !logprob || !lse || !entropy || (top != 0) != (top_index != nullptr) ||
+        (top != 0) != (top_logprob != nullptr))
+        return TXL_ERR_INVALID_ARG;
+    if (!aligned_to(logits, es) || !aligned_to(tokens, 8) || !aligned_to(logprob, 4) || !aligned_to(lse, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(top_index, 8) || !aligned_to(top_logprob, 4))
+        return TXL_ERR_MISALIGNED;
+    const size_t nr = (size_t)rows * sizeof(float);
+    Range r[] = {range_of(logits, row_span(rows, V, ld, es), false), range_of(tokens, 2 * nr, false),
+                 range_of(logprob, nr, true), range_of(lse, nr, true), range_of(entropy, nr, true),
+                 range_of(top_index, 2 * nr * top, true), range_of(top_logprob, nr * top, true)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    const txl::TokenLogprobs a = {logits, ld, tokens, rows, V, top, logprob, lse, entropy, top_index, top_logprob};
+    return cuda_status(txl::launch_token_logprobs(a, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* tokens, const float* lse,
+                           const float* entropy, const float* dlogprob, const float* dlse, const float* dentropy,
+                           long long rows, int V, void* dlogits, long long ldd, int dtype, void* stream) {
+    const int es = elem_size(dtype);
+    if (!es || rows < 0 || V <= 0 || ld < V || ldd < V) return TXL_ERR_INVALID_ARG;
+    if ((!dlogprob && !dlse && !dentropy && rows > 0) || (entropy && !dentropy)) return TXL_ERR_INVALID_ARG;
+    if (logit_rows_too_large(rows, V, std::max(ld, ldd))) return TXL_ERR_UNSUPPORTED;
+    if (rows == 0) return TXL_OK;
+    if (!logits || !tokens || !lse || !dlogits || (dentropy && !entropy)) return TXL_ERR_INVALID_ARG;
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(tokens, 8)) return TXL_ERR_MISALIGNED;
+    for (const float* p : {lse, entropy, dlogprob, dlse, dentropy})
+        if (!aligned_to(p, 4)) return TXL_ERR_MISALIGNED;
+    const size_t nr = (size_t)rows * sizeof(float);
+    const bool in_place = dlogits == logits && (ldd == ld || rows == 1);
+    Range r[] = {range_of(in_place ? nullptr : logits, row_span(rows, V, ld, es), false),
+                 range_of(dlogits, row_span(rows, V, ldd, es), true),
+                 range_of(tokens, 2 * nr, false),
+                 range_of(lse, nr, false),
+                 range_of(entropy, nr, false),
+                 range_of(dlogprob, nr, false),
+                 range_of(dlse, nr, false),
+                 range_of(dentropy, nr, false)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    const txl::TokenLogprobsBwd a = {logits, ld, tokens, lse, entropy, dlogprob, dlse, dentropy, rows, V, dlogits, ldd};
+    return cuda_status(txl::launch_token_logprobs_bwd(a, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors) {
@@ -872,7 +933,8 @@ int txl_bounds_status(unsigned long long* first) {
                                          txl::bounds_word_attn_bwd(),    txl::bounds_word_attn_bwd_tc(),
                                          txl::bounds_word_mem_update(),  txl::bounds_word_layer_norm(),
                                          txl::bounds_word_proj_gemm(),   txl::bounds_word_layer_norm_train(),
-                                         txl::bounds_word_adamw(),       txl::bounds_word_linear_bwd()};
+                                         txl::bounds_word_adamw(),       txl::bounds_word_linear_bwd(),
+                                         txl::bounds_word_token_logprobs()};
     unsigned long long w = 0;
     for (unsigned long long x : words) {
         if (x == ~0ull) return TXL_ERR_CUDA;

@@ -1,0 +1,143 @@
+"""Log probabilities of given tokens, behind a decoder's last layer: from logits,
+with each row's log-sum-exp, entropy and best alternatives, and their gradient.
+Argument marshalling and buffers only: every step of the computation runs in
+libtxl.so's CUDA kernels."""
+from __future__ import annotations
+
+import torch
+from torch.autograd.graph import increment_version
+
+from ._lib import TXL_BF16, TXL_F32, TxlError, _invoke, _need, _stream
+from .train import _INT_MAX, _on, _ptr
+
+_F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
+
+
+def _rows(t, name: str):
+    """(rows, V, distance of the rows in elements) of logits [..., V]: each row
+    contiguous, all rows at one distance (a slice of a wider, padded buffer is fine)."""
+    if not isinstance(t, torch.Tensor) or t.dim() < 1:
+        raise ValueError(f"{name} must be a tensor [..., V]")
+    V = t.shape[-1]
+    if V == 0:
+        raise ValueError(f"{name} must have a last axis of at least one element")
+    rows = t.numel() // V
+    if t.is_contiguous():
+        return rows, V, V
+    ld, size = None, 1  # elements between rows, rows of the axes seen so far
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError(f"each row of {name} must be contiguous")
+    for n, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = step
+        if step != ld * size or ld < V:
+            raise ValueError(f"the rows of {name} must lie at one distance of at least their length")
+        size *= n
+    return rows, V, V if ld is None else ld
+
+
+def _type_of(t, name: str) -> int:
+    if t.dtype is _BF16:
+        return TXL_BF16
+    if t.dtype is _F32:
+        return TXL_F32
+    raise TypeError(f"unsupported dtype {t.dtype} of {name}: bf16 or fp32 only")
+
+
+def _on_gpu(t, name: str, device=None) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+
+
+def _statistics(shape, dev, outs):
+    """logprob, lse, entropy: the caller's, or three parts of one buffer."""
+    if outs is None:
+        return torch.empty((3, *shape), dtype=_F32, device=dev).unbind(0)
+    for n in ("logprob", "lse", "entropy"):
+        _need(outs[n], n, shape, _F32, dev)
+    return outs["logprob"], outs["lse"], outs["entropy"]
+
+
+def token_logprobs(logits, tokens, top=0, stream=None, outs=None):
+    """txl_token_logprobs: of each row of logits [..., V] (bf16 or fp32; rows
+    contiguous, at one distance) and its token (int64 [...], negative: none) a dict of
+    logprob, lse, entropy (fp32 [...]): ln p of the token (0 without one, NaN for a
+    token of V or more), ln sum e^x, -sum p ln p; with top > 0 (at most 32) also
+    top_index (int64) and top_logprob (fp32) [..., top]: the largest logits, of equal
+    ones the lower index first, and their ln p.  outs: a dict of preallocated tensors
+    to fill.  A row of nothing but -inf: lse, ln p -inf, entropy 0; a row with NaN or
+    +inf: NaN."""
+    rows, V, ld = _rows(logits, "logits")
+    code, dev, shape = _type_of(logits, "logits"), logits.device, logits.shape[:-1]
+    _on_gpu(logits, "logits")
+    _need(tokens, "tokens", shape, _I64, dev)
+    if not isinstance(top, int) or top < 0:
+        raise ValueError("top must be a count")
+    if max(V, rows, top) > _INT_MAX:
+        raise TxlError(-2, "txl_token_logprobs")
+    index = value = None
+    with _on(stream, dev):
+        logprob, lse, entropy = _statistics(shape, dev, outs)
+        if top:
+            if outs is None:
+                index = torch.empty((*shape, top), dtype=_I64, device=dev)
+                value = torch.empty((*shape, top), dtype=_F32, device=dev)
+            else:
+                index, value = outs["top_index"], outs["top_logprob"]
+                _need(index, "top_index", (*shape, top), _I64, dev)
+                _need(value, "top_logprob", (*shape, top), _F32, dev)
+    rc = _invoke(dev, "txl_token_logprobs", logits.data_ptr(), ld, tokens.data_ptr(), rows, V, top, logprob.data_ptr(),
+                 lse.data_ptr(), entropy.data_ptr(), _ptr(index), _ptr(value), code, _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_token_logprobs")
+    if outs is not None:
+        return outs
+    outs = {"logprob": logprob, "lse": lse, "entropy": entropy}
+    if top:
+        outs["top_index"], outs["top_logprob"] = index, value
+    return outs
+
+
+def token_logprobs_bwd(logits, tokens, lse, dlogprob=None, dlse=None, dentropy=None, entropy=None, out=None, stream=None):
+    """txl_token_logprobs_bwd: the gradient of logits (their type) from those of
+    token_logprobs' logprob, lse and entropy (fp32 [...], None: zeros; one at least).
+    lse, and with dentropy also entropy, as it returned them.  out: like logits, may be
+    logits itself, whose place the gradient then takes.  A row without a token takes
+    nothing from dlogprob; a row whose gradients are all 0 gets zeros whatever its
+    logits hold."""
+    rows, V, ld = _rows(logits, "logits")
+    code, dev, shape = _type_of(logits, "logits"), logits.device, logits.shape[:-1]
+    _on_gpu(logits, "logits")
+    _need(tokens, "tokens", shape, _I64, dev)
+    _need(lse, "lse", shape, _F32, dev)
+    if dlogprob is None and dlse is None and dentropy is None:
+        raise ValueError("need at least one of dlogprob, dlse, dentropy")
+    if dlogprob is not None:
+        _need(dlogprob, "dlogprob", shape, _F32, dev)
+    if dlse is not None:
+        _need(dlse, "dlse", shape, _F32, dev)
+    if dentropy is not None:
+        _need(dentropy, "dentropy", shape, _F32, dev)
+        _need(entropy, "entropy", shape, _F32, dev)
+    if max(V, rows) > _INT_MAX:
+        raise TxlError(-2, "txl_token_logprobs_bwd")
+    if out is None:
+        with _on(stream, dev):
+            out, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=dev), V
+    else:
+        if not isinstance(out, torch.Tensor) or out.shape != logits.shape or out.dtype is not logits.dtype:
+            raise ValueError(f"out must be a tensor {tuple(logits.shape)} of {logits.dtype}")
+        _on_gpu(out, "out", dev)
+        _, _, ldd = _rows(out, "out")
+    rc = _invoke(dev, "txl_token_logprobs_bwd", logits.data_ptr(), ld, tokens.data_ptr(), lse.data_ptr(),
+                 entropy.data_ptr() if dentropy is not None else 0, _ptr(dlogprob), _ptr(dlse), _ptr(dentropy), rows, V,
+                 out.data_ptr(), ldd, code, _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_token_logprobs_bwd")
+    if out.data_ptr() == logits.data_ptr():
+        increment_version([out])  # what was computed from the logits is not differentiated any more
+    return out
