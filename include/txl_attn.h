@@ -482,6 +482,34 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
                    size_t ws_bytes, void* stream);
 
 /*
+ * txl_grad_norm: the 2-norm of n_tensors tensors together (norm, device fp32 [1]), that
+ * of each one (norms, fp32 [n_tensors], may be null) and, with max_norm > 0, their scaling
+ * in place by max_norm / norm where norm > max_norm.  `tensors` is an array in HOST memory,
+ * read during the call; tensor i has n elements (0: its norm is 0) of type dtype (TXL_F32
+ * or TXL_BF16, which may differ from tensor to tensor).  Products and sums in fp32 over
+ * values scaled by powers of two where their squares would leave its range, added in a
+ * fixed order (the same inputs give the same bits); a scaled value is rounded once.
+ * norm and norms are those before the scaling.  A norm that is not finite in fp32 leaves
+ * the tensors as they were, as does one of at most max_norm.  max_norm = 0: nothing is
+ * scaled, and tensors may overlap each other.
+ *
+ * Tensors 16-byte aligned, norm and norms 4-byte (TXL_ERR_MISALIGNED); what is written
+ * overlaps nothing else (TXL_ERR_ALIAS).  At most 2^38 elements per tensor, 2^40 in all
+ * (TXL_ERR_UNSUPPORTED).  workspace as for txl_layer_norm_bwd, of
+ * txl_grad_norm_workspace_bytes(...) bytes.  max_norm >= 0 and finite, and 0 or at least
+ * 2^-126 (TXL_ERR_INVALID_ARG).
+ */
+typedef struct txl_grad_tensor {
+    void* grad;
+    long long n;
+    int dtype;
+    int reserved; /* 0 */
+} txl_grad_tensor;
+size_t txl_grad_norm_workspace_bytes(const txl_grad_tensor* tensors, int n_tensors);
+int txl_grad_norm(const txl_grad_tensor* tensors, int n_tensors, double max_norm, float* norm, float* norms,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Tail_M memory roll, in place ("Transformer-XL" notes, section
  * "Segment-Level Recurrence": M_{tau+1} = Tail_M([M_tau; H_tau]); source notes
  * MemTransformerLM._update_mems with ext_len = 0 and a full memory).

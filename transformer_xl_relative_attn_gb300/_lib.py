@@ -40,6 +40,11 @@ class AdamwTensor(ctypes.Structure):
                 ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int)]
 
 
+class GradTensor(ctypes.Structure):
+    """txl_grad_tensor: one tensor of txl_grad_norm's table."""
+    _fields_ = [("grad", ctypes.c_void_p), ("n", ctypes.c_longlong), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -123,6 +128,11 @@ def load() -> ctypes.CDLL:
         lib.txl_token_logprobs.restype = i
         lib.txl_token_logprobs_bwd.argtypes = [vp, ll] + [vp] * 6 + [ll, i, vp, ll, i, vp]
         lib.txl_token_logprobs_bwd.restype = i
+        grads = ctypes.POINTER(GradTensor)
+        lib.txl_grad_norm_workspace_bytes.argtypes = [grads, i]
+        lib.txl_grad_norm_workspace_bytes.restype = sz
+        lib.txl_grad_norm.argtypes = [grads, i, dbl, vp, vp, vp, sz, vp]
+        lib.txl_grad_norm.restype = i
         lib.txl_mem_update_ext.argtypes = [vp, vp] + [i] * 6 + [vp]
         lib.txl_mem_update_ext.restype = i
         lib.txl_mem_reset.argtypes = [vp, vp] + [i] * 4 + [vp]

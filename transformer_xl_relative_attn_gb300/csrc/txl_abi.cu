@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "adamw.h"
+#include "grad_norm.h"
 #include "linear_bwd.h"
 #include "proj_gemm.h"
 #include "token_logprobs.h"
@@ -72,6 +73,7 @@ unsigned long long bounds_word_layer_norm_train();
 unsigned long long bounds_word_adamw();
 unsigned long long bounds_word_linear_bwd();
 unsigned long long bounds_word_token_logprobs();
+unsigned long long bounds_word_grad_norm();
 
 }  // namespace txl
 
@@ -694,6 +696,17 @@ bool logit_rows_too_large(long long rows, int V, long long ld) {
 // Bytes from the first row's begin to the last one's end.
 size_t row_span(long long rows, int V, long long ld, int es) { return ((size_t)(rows - 1) * ld + V) * es; }
 
+int grad_tensors_status(const txl_grad_tensor* tensors, int n_tensors) {
+    if (!tensors || n_tensors <= 0) return TXL_ERR_INVALID_ARG;
+    long long total = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        if (tensors[i].n < 0 || !elem_size(tensors[i].dtype)) return TXL_ERR_INVALID_ARG;
+        if (tensors[i].n > (1ll << 38) || total > (1ll << 40) - tensors[i].n) return TXL_ERR_UNSUPPORTED;
+        total += tensors[i].n;
+    }
+    return TXL_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? TXL_OK : TXL_ERR_LAUNCH; }
 
 }  // namespace
@@ -904,6 +917,43 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
     return cuda_status(txl::launch_adamw(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t txl_grad_norm_workspace_bytes(const txl_grad_tensor* tensors, int n_tensors) {
+    return grad_tensors_status(tensors, n_tensors) == TXL_OK
+               ? txl::grad_norm_workspace_bytes(txl::grad_norm_pieces(tensors, n_tensors))
+               : 0;
+}
+
+int txl_grad_norm(const txl_grad_tensor* tensors, int n_tensors, double max_norm, float* norm, float* norms,
+                  void* workspace, size_t ws_bytes, void* stream) {
+    if (!(max_norm >= 0.0) || !std::isfinite(max_norm) || (max_norm > 0.0 && max_norm < FLT_MIN) || max_norm > FLT_MAX ||
+        !norm)
+        return TXL_ERR_INVALID_ARG;
+    const int rc = grad_tensors_status(tensors, n_tensors);
+    if (rc != TXL_OK) return rc;
+    if (!aligned_to(norm, 4) || !aligned_to(norms, 4)) return TXL_ERR_MISALIGNED;
+    const size_t need = txl_grad_norm_workspace_bytes(tensors, n_tensors);
+    if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
+    std::vector<Range> r;
+    try {
+        r.reserve((size_t)n_tensors + 3);
+    } catch (const std::bad_alloc&) {
+        return TXL_ERR_UNSUPPORTED;
+    }
+    for (int i = 0; i < n_tensors; ++i) {
+        const txl_grad_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        if (!t.grad) return TXL_ERR_INVALID_ARG;
+        if (!aligned16(t.grad)) return TXL_ERR_MISALIGNED;
+        r.push_back(range_of(t.grad, (size_t)t.n * elem_size(t.dtype), max_norm > 0.0));
+    }
+    r.push_back(range_of(norm, sizeof(float), true));
+    r.push_back(range_of(norms, (size_t)n_tensors * sizeof(float), true));
+    r.push_back(range_of(workspace, need, true));
+    if (any_written_overlap(r.data(), r.size())) return TXL_ERR_ALIAS;
+    const txl::GradNormArgs a = {tensors, n_tensors, max_norm, norm, norms, workspace};
+    return cuda_status(txl::launch_grad_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
 const char* txl_status_string(int status) {
     switch (status) {
         case TXL_OK: return "ok";
@@ -934,7 +984,7 @@ int txl_bounds_status(unsigned long long* first) {
                                          txl::bounds_word_mem_update(),  txl::bounds_word_layer_norm(),
                                          txl::bounds_word_proj_gemm(),   txl::bounds_word_layer_norm_train(),
                                          txl::bounds_word_adamw(),       txl::bounds_word_linear_bwd(),
-                                         txl::bounds_word_token_logprobs()};
+                                         txl::bounds_word_token_logprobs(), txl::bounds_word_grad_norm()};
     unsigned long long w = 0;
     for (unsigned long long x : words) {
         if (x == ~0ull) return TXL_ERR_CUDA;

@@ -12,7 +12,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from ._lib import TXL_BF16, TXL_F32, AdamwTensor, TxlError, _dtype_code, _invoke, _need, _stream
+from ._lib import TXL_BF16, TXL_F32, AdamwTensor, GradTensor, TxlError, _dtype_code, _invoke, _need, _stream
 
 _HERE = contextlib.nullcontext()
 _LINEAR_GRADS = frozenset(("dx", "dw", "db"))
@@ -246,7 +246,34 @@ def linear_bwd(dy, x, w, relu_in=False, want=("dx", "dw", "db"), stream=None, wo
     return grads
 
 
-class AdamW:
+class _Bound:
+    """What is bound to tensors once and then called on streams: ``device``, ``_storages``
+    (the bound memory) and _own() (tensors of its own, made on the stream that _made
+    records)."""
+
+    def _made(self) -> None:
+        made_on = torch.cuda.current_stream(self.device)
+        # (made in a capture, the fills run with its replay: no event outside stands for them)
+        self._ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+        self._joined = {made_on.cuda_stream}  # streams whose calls come after the fills
+
+    def _join(self, handle: int) -> None:
+        """Puts the calls on a further stream behind the constructor's fills, and the
+        release of all memory that they use behind them."""
+        with _on(handle, self.device):
+            if torch.cuda.is_current_stream_capturing():
+                return  # a graph cannot wait for what is outside of it
+            st = torch.cuda.current_stream(self.device)
+        if self._ready is not None:
+            st.wait_event(self._ready)
+        bound = [torch.empty(0, dtype=torch.uint8, device=self.device).set_(x) for x in self._storages]
+        for t in self._own() + bound:
+            if t is not None:
+                t.record_stream(st)
+        self._joined.add(handle)
+
+
+class AdamW(_Bound):
     """AdamW over a list of parameters in one launch sequence (txl_adamw_step),
     with the moments in fp32 or in 8 bits.
 
@@ -333,10 +360,7 @@ class AdamW:
             self.exp_avg_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
             self.exp_avg_sq_scale = torch.zeros(blocks, **f32) if state_bits == 8 else None
             self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            made_on = torch.cuda.current_stream(dev)
-            # (made in a capture, the fills run with its replay: no event outside stands for them)
-            self._ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
-        self._joined = {made_on.cuda_stream}  # streams whose steps come after the fills above
+            self._made()
         args = (self._table, n, self._param_dtype, self._grad_dtype, state_bits, _ptr(self.master),
                 self.exp_avg.data_ptr(), _ptr(self.exp_avg_scale), self.exp_avg_sq.data_ptr(),
                 _ptr(self.exp_avg_sq_scale), self.steps.data_ptr(), self.lr.data_ptr(), *self.betas, self.eps,
@@ -350,21 +374,8 @@ class AdamW:
             for p, a in zip(self.params, self.starts):
                 self.master[a:a + p.numel()].copy_(p.reshape(-1))
 
-    def _join(self, handle: int) -> None:
-        """Puts the steps on a further stream behind the constructor's fills, and the
-        release of all memory that they use behind them."""
-        with _on(handle, self.device):
-            if torch.cuda.is_current_stream_capturing():
-                return  # a graph cannot wait for what is outside of it
-            st = torch.cuda.current_stream(self.device)
-        if self._ready is not None:
-            st.wait_event(self._ready)
-        own = [self.lr, self.steps, self.grad_norm, self.master, self._workspace, *self.states()]
-        bound = [torch.empty(0, dtype=torch.uint8, device=self.device).set_(x) for x in self._storages]
-        for t in own + bound:
-            if t is not None:
-                t.record_stream(st)
-        self._joined.add(handle)
+    def _own(self) -> list:
+        return [self.lr, self.steps, self.grad_norm, self.master, self._workspace, *self.states()]
 
     def step(self, stream=None) -> None:
         """One step from the gradients as they stand, on ``stream`` (default:
@@ -414,3 +425,63 @@ class AdamW:
             if self.master is not None:
                 for p, a in zip(self.params, self.starts):
                     p.copy_(self.master[a:a + p.numel()].view(p.shape))
+
+
+class GradNorm(_Bound):
+    """The norms of many gradients, and their clipping, in two launches (txl_grad_norm).
+
+    ``grads``: contiguous CUDA tensors, fp32 or bf16, of both types if need be; their memory
+    is bound here, as AdamW binds it (which clips by itself where it is given a max_norm:
+    this is for gradients that something else reads, or that are to be watched).  Device
+    values: ``norm`` [1], the 2-norm of all, and ``norms`` [n], that of each, fp32; both
+    written by measure() and, before the scaling, by clip().  Calls on several streams are
+    the caller's to order; the first on a further stream waits for the constructor."""
+
+    def __init__(self, grads: Sequence[torch.Tensor]):
+        self.grads = list(grads)
+        n = len(self.grads)
+        if n == 0:
+            raise ValueError("need at least one gradient")
+        self._table, dev = (GradTensor * n)(), None
+        for i, g in enumerate(self.grads):
+            if not isinstance(g, torch.Tensor):
+                raise TypeError("grads must be torch.Tensors")
+            code = _dtype_code(g)
+            _need(g, f"grads[{i}]", g.shape, g.dtype, dev)
+            dev = g.device
+            self._table[i] = GradTensor(g.data_ptr(), g.numel(), code, 0)
+        self.device = dev
+        self._storages = [t.untyped_storage() for t in self.grads]
+        need = int(_invoke(dev, "txl_grad_norm_workspace_bytes", self._table, n))
+        self.norm = torch.empty(1, dtype=torch.float32, device=dev)
+        self.norms = torch.empty(n, dtype=torch.float32, device=dev)
+        self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev):
+            self._made()
+        types = _lib.load().txl_grad_norm.argtypes
+        args = (self.norm.data_ptr(), self.norms.data_ptr(), self._workspace.data_ptr(), need)
+        self._args = tuple(of(a) for of, a in zip(types[3:], args))
+
+    def _own(self) -> list:
+        return [self.norm, self.norms, self._workspace]
+
+    def _call(self, max_norm: float, stream) -> None:
+        handle = _stream(stream, self.device)
+        if handle not in self._joined:
+            self._join(handle)
+        rc = _invoke(self.device, "txl_grad_norm", self._table, len(self._table), max_norm, *self._args, handle)
+        if rc != 0:
+            raise TxlError(rc, "txl_grad_norm")
+
+    def measure(self, stream=None) -> None:
+        """Norms of the gradients as they stand, on ``stream`` (default: the current one)."""
+        self._call(0.0, stream)
+
+    def clip(self, max_norm: float, stream=None) -> None:
+        """measure(), and gradients scaled in place by max_norm / norm where norm is above
+        max_norm and finite.  Moves the gradients' version counters, as AdamW's step the
+        parameters'."""
+        if not max_norm > 0:
+            raise ValueError("max_norm must be positive")
+        self._call(float(max_norm), stream)
+        increment_version(self.grads)
