@@ -430,6 +430,24 @@ int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* to
                            long long rows, int V, void* dlogits, long long ldd, int dtype, void* stream);
 
 /*
+ * txl_linear_logprobs: txl_token_logprobs of the logits z = x W^T + bias without the
+ * logits: x [rows, K], w [V, K] and bias [V] (may be null) bf16, products on the tensor
+ * cores with fp32 accumulation, z never rounded to fewer bits; the row statistics lse,
+ * logprob and entropy (fp32 [rows]) and their special cases are those of
+ * txl_token_logprobs (a bias of -inf masks a column).  For scoring; the gradient goes over
+ * txl_linear's logits and txl_token_logprobs_bwd.  The same inputs give the same bits.
+ *
+ * 0 <= rows <= 2^28, K a multiple of 8 up to 2^20, 1 <= V <= 2^30, rows * V <= 2^40
+ * (TXL_ERR_UNSUPPORTED beyond).  x and w 16-byte aligned, the others to their elements
+ * (TXL_ERR_MISALIGNED); outputs overlap neither inputs nor each other (TXL_ERR_ALIAS).
+ * workspace as for txl_layer_norm_bwd, of txl_linear_logprobs_workspace_bytes(...) bytes.
+ */
+size_t txl_linear_logprobs_workspace_bytes(long long rows, int K, int V);
+int txl_linear_logprobs(const void* x, const void* w, const void* bias, const long long* tokens, long long rows, int K,
+                        int V, float* logprob, float* lse, float* entropy, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/*
  * txl_adamw_step: one AdamW step over n_tensors tensors.  `tensors` is an array
  * in HOST memory, read during the call; tensor i has n elements (0: skipped),
  * a parameter, a gradient and a weight decay of its own.  With g the gradient

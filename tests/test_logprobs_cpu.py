@@ -95,3 +95,37 @@ def test_sizes_of_2_to_31(monkeypatch, axis, big):
         with pytest.raises(txl.TxlError) as e:
             call()
         assert e.value.code == -2
+
+
+def test_linear_logprobs_rejects_bad_arguments(lib):
+    need = lib.txl_linear_logprobs_workspace_bytes(100, 64, 500)
+    assert need > 0
+
+    def call(x=addr(0), w=addr(1), b=addr(2), t=addr(3), rows=100, K=64, V=500, lp=addr(4), lse=addr(5), ent=addr(6),
+             ws=addr(7), ws_bytes=need):
+        return lib.txl_linear_logprobs(x, w, b, t, rows, K, V, lp, lse, ent, ws, ws_bytes, None)
+    for name in ("x", "w", "t", "lp", "lse", "ent"):
+        assert call(**{name: None}) == -1, name
+    for name in ("x", "w"):
+        assert call(**{name: addr(8) + 8}) == -3, name
+    for name in ("b", "t", "lp", "lse", "ent"):
+        assert call(**{name: addr(8) + 1}) == -3, name
+    assert call(rows=-1) == -1 and call(K=0) == -1 and call(V=0) == -1
+    assert call(K=60) == -2 and call(K=(1 << 20) + 8) == -2 and call(V=(1 << 30) + 1) == -2
+    assert call(rows=(1 << 28) + 1) == -2 and call(rows=1 << 27, V=1 << 14) == -2
+    assert call(ws=None) == -7 and call(ws=addr(7) + 128) == -7 and call(ws_bytes=need - 1) == -7
+    assert call(lp=addr(5)) == -4 and call(lse=addr(1) + 64) == -4 and call(ws=addr(0)) == -4 and call(ent=addr(7) + 16) == -4
+    assert call(rows=0, x=None, w=None, t=None, ws=None) == 0
+    for rows, K, V in ((0, 64, 500), (-1, 64, 500), (100, 60, 500), (100, 64, 0)):
+        assert lib.txl_linear_logprobs_workspace_bytes(rows, K, V) == 0
+
+
+def test_linear_binding_refuses_what_it_can_see():
+    x, w, t = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(9, 8, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        txl.linear_logprobs(x, w, t)
+    with pytest.raises(ValueError, match="w must be"):
+        txl.linear_logprobs(x, w[0], t)
+    with pytest.raises(ValueError, match="last axis"):
+        txl.linear_logprobs(x[:, :0], w, t)
+    assert txl.linear_logprobs_workspace_bytes(2 ** 31, 64, 64, device=0) == 0

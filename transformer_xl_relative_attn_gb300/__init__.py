@@ -17,6 +17,8 @@ Public API (all computation runs in libtxl.so's CUDA kernels):
     AdamW                                         AdamW over many tensors, 32-bit or 8-bit states
     GradNorm                                      norms of many gradients and of all, clipping in place
     token_logprobs, token_logprobs_bwd            log probabilities of given tokens, entropy, alternatives; their gradient
+    linear_logprobs                               the same from hidden states and output weights (tensor cores), no logits
+    linear_logprobs_workspace_bytes               scratch of the latter
     sync_status, check_status                     device status word
     bounds_status                                 first out-of-range access (bounds-checked build)
     SegmentDriver                                 multi-segment, multi-layer driver (caller's projections)
@@ -29,7 +31,7 @@ from ._lib import (TXL_BF16, TXL_F32, TxlError, attn_bwd, attn_bwd_workspace_byt
                    status_string,
                    sync_status, version, LIB_PATH)
 from .driver import AttnStack, DecoderStack, SegmentDriver
-from .logprobs import token_logprobs, token_logprobs_bwd
+from .logprobs import linear_logprobs, linear_logprobs_workspace_bytes, token_logprobs, token_logprobs_bwd
 from .train import AdamW, GradNorm, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd, linear_bwd, linear_bwd_workspace_bytes
 
 __all__ = ["TXL_BF16", "TXL_F32", "TxlError", "attn_bwd", "attn_bwd_workspace_bytes", "attn_fwd", "attn_fwd_lse", "attn_fwd_noalloc", "attn_fwd_ws",
@@ -37,4 +39,5 @@ __all__ = ["TXL_BF16", "TXL_F32", "TxlError", "attn_bwd", "attn_bwd_workspace_by
            "check_status", "debug_inject", "header_functions", "layer_norm", "linear", "load", "mem_reset", "mem_ring_push", "mem_update", "qkv_proj", "qkvr_proj", "r_proj",
            "status_string", "sync_status", "version", "SegmentDriver", "AttnStack", "DecoderStack", "AdamW", "GradNorm", "layer_norm_fwd",
            "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
-           "linear_bwd", "linear_bwd_workspace_bytes", "token_logprobs", "token_logprobs_bwd", "LIB_PATH"]
+           "linear_bwd", "linear_bwd_workspace_bytes", "token_logprobs", "token_logprobs_bwd",
+           "linear_logprobs", "linear_logprobs_workspace_bytes", "LIB_PATH"]

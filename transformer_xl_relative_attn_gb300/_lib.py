@@ -128,6 +128,10 @@ def load() -> ctypes.CDLL:
         lib.txl_token_logprobs.restype = i
         lib.txl_token_logprobs_bwd.argtypes = [vp, ll] + [vp] * 6 + [ll, i, vp, ll, i, vp]
         lib.txl_token_logprobs_bwd.restype = i
+        lib.txl_linear_logprobs_workspace_bytes.argtypes = [ll, i, i]
+        lib.txl_linear_logprobs_workspace_bytes.restype = sz
+        lib.txl_linear_logprobs.argtypes = [vp] * 4 + [ll, i, i] + [vp] * 4 + [sz, vp]
+        lib.txl_linear_logprobs.restype = i
         grads = ctypes.POINTER(GradTensor)
         lib.txl_grad_norm_workspace_bytes.argtypes = [grads, i]
         lib.txl_grad_norm_workspace_bytes.restype = sz

@@ -1,0 +1,35 @@
+// Internal interface of the log probabilities from hidden states (linear_logprobs.cu) for the ABI layer.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace txl {
+
+struct LpParams {
+    int rows, V;
+    int ksteps;            // 64-element steps of K
+    int n_rt, n_vt;        // tiles of rows and of columns
+    int per, chunks;       // column tiles of an item; items per row tile
+    long long ld;          // rows of the partial sums, whole tiles
+    const long long* tokens;
+    const __nv_bfloat16* bias;  // [V] or null
+    float* part;           // [2 chunks][3][ld]: m, s, t of each half of an item's columns
+    float* given;          // [ld]: the token's logit
+    int* status;
+};
+
+struct LpPlan {
+    bool pair;
+    int grid;
+    LpParams p;
+};
+
+LpPlan linear_logprobs_plan(int rows, int K, int V);
+size_t linear_logprobs_workspace_bytes(const LpPlan& plan);
+// Of x [rows, K], w [V, K] and bias [V] (may be null), bf16, K a multiple of 8.
+// cudaErrorInvalidValue: a tensor map could not be encoded.
+cudaError_t launch_linear_logprobs(LpPlan plan, const void* x, const void* w, const void* bias, int K, const long long* tokens,
+                                   float* logprob, float* lse, float* entropy, void* workspace, int* status,
+                                   cudaStream_t stream);
+
+}  // namespace txl

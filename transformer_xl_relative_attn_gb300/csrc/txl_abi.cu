@@ -14,6 +14,7 @@
 #include "adamw.h"
 #include "grad_norm.h"
 #include "linear_bwd.h"
+#include "linear_logprobs.h"
 #include "proj_gemm.h"
 #include "token_logprobs.h"
 #include "txl_attn.h"
@@ -74,6 +75,7 @@ unsigned long long bounds_word_adamw();
 unsigned long long bounds_word_linear_bwd();
 unsigned long long bounds_word_token_logprobs();
 unsigned long long bounds_word_grad_norm();
+unsigned long long bounds_word_linear_logprobs();
 
 }  // namespace txl
 
@@ -696,6 +698,12 @@ bool logit_rows_too_large(long long rows, int V, long long ld) {
 // Bytes from the first row's begin to the last one's end.
 size_t row_span(long long rows, int V, long long ld, int es) { return ((size_t)(rows - 1) * ld + V) * es; }
 
+int linear_logprobs_sizes(long long rows, int K, int V) {
+    if (rows < 0 || K <= 0 || V <= 0) return TXL_ERR_INVALID_ARG;
+    if (K % 8 != 0 || K > (1 << 20) || V > (1 << 30) || rows > (1ll << 28) || rows > (1ll << 40) / V) return TXL_ERR_UNSUPPORTED;
+    return TXL_OK;
+}
+
 int grad_tensors_status(const txl_grad_tensor* tensors, int n_tensors) {
     if (!tensors || n_tensors <= 0) return TXL_ERR_INVALID_ARG;
     long long total = 0;
@@ -841,6 +849,36 @@ int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* to
     return cuda_status(txl::launch_token_logprobs_bwd(a, dtype == TXL_BF16, static_cast<cudaStream_t>(stream)));
 }
 
+size_t txl_linear_logprobs_workspace_bytes(long long rows, int K, int V) {
+    if (linear_logprobs_sizes(rows, K, V) != TXL_OK || rows == 0) return 0;
+    return txl::linear_logprobs_workspace_bytes(txl::linear_logprobs_plan((int)rows, K, V));
+}
+
+int txl_linear_logprobs(const void* x, const void* w, const void* bias, const long long* tokens, long long rows, int K,
+                        int V, float* logprob, float* lse, float* entropy, void* workspace, size_t ws_bytes,
+                        void* stream) {
+    const int rc = linear_logprobs_sizes(rows, K, V);
+    if (rc != TXL_OK) return rc;
+    if (rows == 0) return TXL_OK;
+    if (!x || !w || !tokens || !logprob || !lse || !entropy) return TXL_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned_to(bias, 2) || !aligned_to(tokens, 8) || !aligned_to(logprob, 4) ||
+        !aligned_to(lse, 4) || !aligned_to(entropy, 4))
+        return TXL_ERR_MISALIGNED;
+    const txl::LpPlan plan = txl::linear_logprobs_plan((int)rows, K, V);
+    const size_t need = txl::linear_logprobs_workspace_bytes(plan);
+    if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
+    const size_t nr = (size_t)rows * sizeof(float);
+    Range r[] = {range_of(x, (size_t)rows * K * 2, false), range_of(w, (size_t)V * K * 2, false),
+                 range_of(bias, (size_t)V * 2, false),     range_of(tokens, 2 * nr, false),
+                 range_of(logprob, nr, true),              range_of(lse, nr, true),
+                 range_of(entropy, nr, true),              range_of(workspace, need, true)};
+    if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
+    int* status = dev_status_ptr();
+    if (!status) return TXL_ERR_CUDA;
+    return launch_status(txl::launch_linear_logprobs(plan, x, w, bias, K, tokens, logprob, lse, entropy, workspace, status,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
 long long txl_adamw_state_elements(const txl_adamw_tensor* tensors, int n_tensors) {
     if (!tensors || n_tensors <= 0) return -1;
     long long blocks = 0;
@@ -984,7 +1022,8 @@ int txl_bounds_status(unsigned long long* first) {
                                          txl::bounds_word_mem_update(),  txl::bounds_word_layer_norm(),
                                          txl::bounds_word_proj_gemm(),   txl::bounds_word_layer_norm_train(),
                                          txl::bounds_word_adamw(),       txl::bounds_word_linear_bwd(),
-                                         txl::bounds_word_token_logprobs(), txl::bounds_word_grad_norm()};
+                                         txl::bounds_word_token_logprobs(), txl::bounds_word_grad_norm(),
+                                         txl::bounds_word_linear_logprobs()};
     unsigned long long w = 0;
     for (unsigned long long x : words) {
         if (x == ~0ull) return TXL_ERR_CUDA;

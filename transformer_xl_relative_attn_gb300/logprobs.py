@@ -1,5 +1,6 @@
 """Log probabilities of given tokens, behind a decoder's last layer: from logits,
-with each row's log-sum-exp, entropy and best alternatives, and their gradient.
+with each row's log-sum-exp, entropy and best alternatives, and their gradient; or
+straight from hidden states and the output weights, without the logits.
 Argument marshalling and buffers only: every step of the computation runs in
 libtxl.so's CUDA kernels."""
 from __future__ import annotations
@@ -8,7 +9,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from ._lib import TXL_BF16, TXL_F32, TxlError, _invoke, _need, _stream
-from .train import _INT_MAX, _on, _ptr
+from .train import _INT_MAX, _on, _ptr, _scratch, _workspace_need
 
 _F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
 
@@ -141,3 +142,48 @@ def token_logprobs_bwd(logits, tokens, lse, dlogprob=None, dlse=None, dentropy=N
     if out.data_ptr() == logits.data_ptr():
         increment_version([out])  # what was computed from the logits is not differentiated any more
     return out
+
+
+def linear_logprobs_workspace_bytes(rows, K, V, device=None) -> int:
+    """txl_linear_logprobs_workspace_bytes for a call on ``device`` (default: the current
+    one; the split depends on its SM count)."""
+    if max(rows, K, V) > _INT_MAX:
+        return 0  # as for every size that the call refuses
+    dev = device if device is not None else torch.cuda.current_device()
+    return int(_invoke(dev, "txl_linear_logprobs_workspace_bytes", rows, K, V))
+
+
+def linear_logprobs(x, w, tokens, bias=None, stream=None, workspace=None, outs=None):
+    """txl_linear_logprobs: token_logprobs' logprob, lse and entropy (a dict, fp32 [...])
+    of the logits x w^T + bias, which are never written: x [..., K], w [V, K], bias [V]
+    (or None) bf16, K a multiple of 8; tokens int64 [...] as there.  outs: a dict of
+    preallocated tensors to fill; workspace: a uint8 tensor of at least
+    linear_logprobs_workspace_bytes(...) bytes (allocated here when None)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a tensor [..., K]")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be [V, K]")
+    K, V, dev, shape = x.shape[-1], w.shape[0], x.device, x.shape[:-1]
+    if K == 0:
+        raise ValueError("x must have a last axis of at least one element")
+    _need(x, "x", x.shape, _BF16)
+    _need(w, "w", (V, K), _BF16, dev)
+    if bias is not None:
+        _need(bias, "bias", (V,), _BF16, dev)
+    _need(tokens, "tokens", shape, _I64, dev)
+    rows = x.numel() // K
+    need = _workspace_need(dev.index, "txl_linear_logprobs_workspace_bytes", rows, K, V)
+    with _on(stream, dev):
+        logprob, lse, entropy = _statistics(shape, dev, outs)
+        if workspace is not None:
+            at = _scratch(workspace, need, dev)
+        elif need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            at = workspace.data_ptr()
+        else:
+            at = 0
+    rc = _invoke(dev, "txl_linear_logprobs", x.data_ptr(), w.data_ptr(), _ptr(bias), tokens.data_ptr(), rows, K, V,
+                 logprob.data_ptr(), lse.data_ptr(), entropy.data_ptr(), at, need, _stream(stream, dev))
+    if rc != 0:
+        raise TxlError(rc, "txl_linear_logprobs")
+    return {"logprob": logprob, "lse": lse, "entropy": entropy} if outs is None else outs
