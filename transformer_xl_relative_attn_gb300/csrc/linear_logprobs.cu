@@ -12,10 +12,11 @@
 // the runs.  What bounds it: the MMAs with many rows (an accumulator of 128 x 256 takes the
 // epilogue less time than 512 elements of K the tensor cores), the read of W with few.
 //
-// Two CTAs of a cluster share a 256 x 256 tile (cta_group::2), or one CTA takes 128 x 128
-// where there are few rows.  Both operands are K-major, 128 rows of 64 elements per stage
-// and CTA: two TMA instructions of 16 KB.  Rows, columns and K need not fill their tiles:
-// TMA fills with zeros behind the ends, and columns behind V count as -inf.
+// Two CTAs of a cluster share a tile of 256 rows (cta_group::2), or one CTA takes 128.  A
+// tile has 256 columns, or fewer (a multiple of 64) where that fills the units more evenly.
+// Both operands are K-major, 64 elements of K per stage: two TMA instructions a CTA.  Rows,
+// columns and K need not fill their tiles: TMA fills with zeros behind the ends, and columns
+// behind V count as -inf.
 //
 // Roles (384 threads, one CTA per SM): warp 0 lane 0 issues the TMA loads, warp 1 the
 // MMAs, warps 4-11 the epilogue; two accumulators let an epilogue overlap the next tile's
@@ -36,33 +37,37 @@ namespace txl {
 namespace lp {
 constexpr int BM = 128;  // rows of a CTA's accumulator
 constexpr int BK = 64;   // K per stage
+constexpr int MAX_BN = 256;
 constexpr int NTHREADS = 384;
-constexpr uint32_t SZ_A = BM * BK * 2;  // 16 KB
-constexpr uint32_t SZ_B = 128 * BK * 2;  // of a pair's 256 columns, each CTA holds half
-constexpr int STAGES = 6;
-constexpr uint32_t OFF_A = 0;
-constexpr uint32_t OFF_B = STAGES * SZ_A;
-constexpr uint32_t OFF_BAR = OFF_B + STAGES * SZ_B;
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget of one sm_103a CTA");
+constexpr uint32_t SZ_A = BM * BK * 2;  // 16 KB; the second operand's slot: 128 bytes per column of the CTA's
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t TMEM_COLS = 2 * MAX_BN;
 
-template <bool PAIR>
+// A tile's width is known at compile time: with the width, the stages and the descriptors'
+// steps as variables the MMAs' issuing loop took 7 % longer (11264 rows, 512 -> 32768: 241
+// us as constants, 260).
+template <bool PAIR, int BN>
 struct Cfg {
     static constexpr int CTAS = PAIR ? 2 : 1;
-    static constexpr int TM = BM * CTAS;  // tile
-    static constexpr int BN = PAIR ? 256 : 128;
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static constexpr int TM = BM * CTAS;                      // rows of a tile
+    static constexpr uint32_t SZ_B = BN / CTAS * BK * 2;      // of a pair's columns each CTA holds half
+    static constexpr int FIT = 220 * 1024 / (SZ_A + SZ_B);
+    static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+    static constexpr uint32_t OFF_B = STAGES * SZ_A;
+    static constexpr uint32_t OFF_BAR = OFF_B + STAGES * SZ_B;
+    static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
     static constexpr uint32_t IDESC = idesc_bf16_f32(TM, BN, 0, 0);
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget of one sm_103a CTA");
 };
 }  // namespace lp
 
 struct LpMaps {
-    CUtensorMap x, w;  // (element, row), boxes of 64 x 128
+    CUtensorMap x, w;  // (element, row), boxes of 64 x 128 and of 64 x a CTA's columns
 };
 
 struct LpShared {
-    uint64_t full[lp::STAGES];  // a pair's: those of its first CTA
-    uint64_t empty[lp::STAGES];
+    uint64_t full[lp::MAX_STAGES];  // a pair's: those of its first CTA
+    uint64_t empty[lp::MAX_STAGES];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];  // a pair's: those of its first CTA
     uint64_t drain;
@@ -84,20 +89,29 @@ __device__ __forceinline__ LpItem lp_item(const LpParams& p, int i) {
     return it;
 }
 
-template <bool PAIR>
+// One column of an accumulator, a row per lane.
+__device__ __forceinline__ float lp_tmem_column(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+    return __uint_as_float(r);
+}
+
+// (BIAS: unused, the bias' code cost a call without one 4 %.)
+template <bool PAIR, int BN, bool BIAS>
 __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const __grid_constant__ LpMaps maps, const LpParams p) {
     using namespace lp;
-    using C = Cfg<PAIR>;
-    constexpr int BN = C::BN;
+    using C = Cfg<PAIR, BN>;
+    constexpr int CTAS = C::CTAS, TM = C::TM, STAGES = C::STAGES;
+    constexpr uint32_t SZ_B = C::SZ_B, OFF_B = C::OFF_B;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    LpShared* sh = reinterpret_cast<LpShared*>(smem + OFF_BAR);
+    LpShared* sh = reinterpret_cast<LpShared*>(smem + C::OFF_BAR);
     const uint32_t s_base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lb_cta_rank() : 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 1) lb_tmem_alloc<PAIR>(&sh->tmem_base, C::TMEM_COLS);
+    if (warp == 1) lb_tmem_alloc<PAIR>(&sh->tmem_base, TMEM_COLS);
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sh->full[s], 1);
@@ -105,7 +119,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 8 * C::CTAS);  // one arrival per epilogue warp
+            mbar_init(&sh->acc_empty[a], 8 * CTAS);  // one arrival per epilogue warp
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -120,7 +134,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = sh->tmem_base;
     volatile int* abort = &sh->abort;
-    const int unit = blockIdx.x / C::CTAS, units = gridDim.x / C::CTAS, items = p.n_rt * p.chunks;
+    const int unit = blockIdx.x / CTAS, units = gridDim.x / CTAS, items = p.n_rt * p.chunks;
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
@@ -128,23 +142,29 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
         // second's loads may land before it does (the barrier waits for the arrival).
         if (lane == 0) {
             bool ok = true;
+            // One thread's instructions per stage bound the loads, so what does not change is
+            // kept out of the loop.
             uint32_t s = 0, phase = 1;  // slot, parity of its empty barrier (a fresh one passes for 1)
             long long loads = 0;
             const uint32_t full0 = PAIR ? lb_mapa(&sh->full[0], 0) : smem_u32(&sh->full[0]);
+            const uint32_t bytes = (SZ_A + SZ_B) * CTAS;
+            uint32_t to_a = s_base, to_b = s_base + OFF_B, bar = full0;
+            const int K = p.ksteps * BK;
             for (int i = unit; ok && i < items; i += units) {
                 const LpItem it = lp_item(p, i);
-                const int r0 = it.r * C::TM + BM * rank;
+                const int r0 = it.r * TM + BM * rank;
                 for (int v = it.v0; ok && v < it.v1; ++v) {
-                    const int n0 = v * BN + 128 * rank;
-                    for (int k = 0; k < p.ksteps; ++k) {
+                    const int n0 = v * BN + BN / CTAS * rank;
+                    for (int k = 0; k < K; k += BK) {
                         if (!mbar_wait(&sh->empty[s], phase, kDevTimeoutProducer, abort, p.status)) {
                             ok = false;
                             break;
                         }
-                        if (rank == 0) mbar_expect_tx(&sh->full[s], (SZ_A + SZ_B) * C::CTAS);
-                        lb_load_2d<PAIR>(s_base + OFF_A + s * SZ_A, &maps.x, full0 + 8 * s, k * BK, r0);
-                        lb_load_2d<PAIR>(s_base + OFF_B + s * SZ_B, &maps.w, full0 + 8 * s, k * BK, n0);
-                        if (++s == STAGES) s = 0, phase ^= 1;
+                        if (rank == 0) mbar_expect_tx(&sh->full[s], bytes);
+                        lb_load_2d<PAIR>(to_a, &maps.x, bar, k, r0);
+                        lb_load_2d<PAIR>(to_b, &maps.w, bar, k, n0);
+                        to_a += SZ_A, to_b += SZ_B, bar += 8;
+                        if (++s == STAGES) s = 0, phase ^= 1, to_a = s_base, to_b = s_base + OFF_B, bar = full0;
                         ++loads;
                     }
                 }
@@ -165,7 +185,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                 if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kDevTimeoutMma, abort, p.status));
                 return ok;
             };
-            const uint64_t dA0 = smem_desc_sw128(s_base + OFF_A, 16, 1024);
+            const uint64_t dA0 = smem_desc_sw128(s_base, 16, 1024);
             const uint64_t dB0 = smem_desc_sw128(s_base + OFF_B, 16, 1024);
             uint32_t s = 0, phase = 0;  // slot, parity of its full barrier
             int j = 0;                  // accumulators filled
@@ -175,17 +195,25 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     const int acc = j & 1;
                     if (j >= 2 && !wait(&sh->acc_empty[acc], ((j >> 1) - 1) & 1)) break;
                     tc_fence_after();
-                    const uint32_t d_acc = tmem + acc * BN;
-                    for (int k = 0; k < p.ksteps; ++k) {
-                        if (!wait(&sh->full[s], phase)) break;
+                    const uint32_t d_acc = tmem + acc * MAX_BN;
+                    uint32_t more_than_first = 0;
+                    auto step = [&](int n) {
+                        if (!wait(&sh->full[s], phase)) return false;
                         tc_fence_after();
                         const uint64_t ad = dA0 + s * (SZ_A >> 4), bd = dB0 + s * (SZ_B >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            lb_mma<PAIR>(d_acc, ad + 2 * kk, bd + 2 * kk, C::IDESC, (k > 0 || kk > 0) ? 1u : 0u, leader);
+                            if (kk < n) {
+                                lb_mma<PAIR>(d_acc, ad + 2 * kk, bd + 2 * kk, C::IDESC, more_than_first, leader);
+                                more_than_first = 1;
+                            }
                         if (leader) lb_commit<PAIR>(&sh->empty[s]);
                         if (++s == STAGES) s = 0, phase ^= 1;
-                    }
+                        return true;
+                    };
+                    for (int k = 1; k < p.ksteps; ++k)
+                        if (!step(BK / 16)) break;
+                    if (ok) step(p.klast);
                     if (!ok) break;
                     if (leader) lb_commit<PAIR>(&sh->acc_full[acc]);
                     ++j;
@@ -199,30 +227,87 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
         // ---------------------------------------------------- epilogue
         const int wq = warp & 3;
         const int chalf = (warp - 4) >> 2;
-        constexpr int CPW = BN / 64;  // 32-column chunks per warp
-        const uint32_t t_row = tmem + ((uint32_t)(wq * 32) << 16) + 32 * CPW * chalf;
+        constexpr int chunks = BN / 64, half = 32 * chunks;  // 32-column chunks per warp; its columns
+        const uint32_t t_row = tmem + ((uint32_t)(wq * 32) << 16) + half * chalf;
         const uint32_t acc_empty0 = PAIR ? lb_mapa(&sh->acc_empty[0], 0) : 0;
         bool ok = true;
         int j = 0;
         for (int i = unit; ok && i < items; i += units) {
             const LpItem it = lp_item(p, i);
-            const int row = it.r * C::TM + BM * rank + 32 * wq + lane;
+            const int row = it.r * TM + BM * rank + 32 * wq + lane;
             const long long token = row < p.rows ? p.tokens[row] : -1;
-            SoftmaxSums sums;
+            SoftmaxPairs sums;
             sums.clear();
-            float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+            auto add = [&](const float (&z)[32]) {
+                float most = fmaxf(z[0], z[1]);
+#pragma unroll
+                for (int x = 2; x < 32; x += 2) most = sm_max3(most, z[x], z[x + 1]);
+                sums.raise(most);
+                if (sm_ordinary(sums.m)) {
+                    const float r = sm_reference(sums.m);
+                    const float2 was = sums.t;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) sums.add(make_float2(z[x], z[x + 1]), r);
+                    if (sums.lost()) {
+                        sums.t = was;
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) sums.add_low(make_float2(z[x], z[x + 1]), r);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) sums.add_far(z[x]);
+                }
+            };
+            // A chunk of the accumulator, columns n .. n + 31 of the logits.  (Two copies of the
+            // sums: with what the bias and the end of V change in the first, it took 2 % longer.)
+            auto take = [&](const uint32_t (&q)[32], int n) {
+                float z[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) z[x] = __uint_as_float(q[x]);
+                if (!BIAS && n + 32 <= p.V) {
+                    add(z);
+                    return;
+                }
+                float w[32];
+                if (BIAS && p.wide_bias && n + 32 <= p.V) {
+                    const uint4* const b4 = reinterpret_cast<const uint4*>(p.bias + n);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const uint4 b = __ldg(b4 + h);
+                        const uint32_t e[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            w[8 * h + 2 * x] = z[8 * h + 2 * x] + __uint_as_float(e[x] << 16);
+                            w[8 * h + 2 * x + 1] = z[8 * h + 2 * x + 1] + __uint_as_float(e[x] & 0xFFFF0000u);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        w[x] = n + x < p.V ? z[x] + (BIAS ? __bfloat162float(p.bias[n + x]) : 0.f) : -INFINITY;
+                }
+                add(w);
+            };
             for (int v = it.v0; v < it.v1; ++v, ++j) {
                 const int acc = j & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh->acc_full[acc], (j >> 1) & 1, kDevTimeoutSoftmax, abort, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                const int n0 = v * BN + 32 * CPW * chalf;
+                const int n0 = v * BN + half * chalf;
+                const uint32_t from = t_row + acc * MAX_BN;
+                // the logits of the tokens that lie in these columns, row by row (few do)
+                for (unsigned has = __ballot_sync(0xffffffffu, token >= n0 && token < n0 + half && token < p.V); has; has &= has - 1) {
+                    const int src = __ffs(has) - 1, n = __shfl_sync(0xffffffffu, (int)token, src);
+                    float g = lp_tmem_column(from + (n - n0));
+                    if (BIAS) g += __bfloat162float(p.bias[n]);
+                    if (lane == src && TXL_BOUNDS(row < p.ld, 1301, row)) p.given[row] = g;
+                }
 #pragma unroll 1
-                for (int cc = 0; cc < CPW; ++cc) {
+                for (int c = 0; c < chunks; ++c) {
                     uint32_t q[32];
-                    tmem_ld32(t_row + acc * BN + 32 * cc, q);
+                    tmem_ld32(from + 32 * c, q);
                     tmem_wait_ld();
-                    if (cc == CPW - 1) {
+                    if (c == chunks - 1) {  // the accumulator is the MMAs' again
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
@@ -232,49 +317,14 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                                 mbar_arrive(&sh->acc_empty[acc]);
                         }
                     }
-                    const int n = n0 + 32 * cc;
-                    float z[32];
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) z[x] = __uint_as_float(q[x]);
-                    if (p.bias) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (n + x < p.V) z[x] += __bfloat162float(p.bias[n + x]);
-                    }
-                    if (n + 32 > p.V) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (n + x >= p.V) z[x] = -INFINITY;
-                    }
-                    if (token >= n && token < n + 32 && token < p.V) {
-                        const int at = (int)token - n;
-                        float g = z[0];
-#pragma unroll
-                        for (int x = 1; x < 32; ++x) g = at == x ? z[x] : g;
-                        if (TXL_BOUNDS(row < p.ld, 1301, row)) p.given[row] = g;
-                    }
-                    float most = z[0];
-#pragma unroll
-                    for (int x = 1; x < 32; ++x) most = fmaxf(most, z[x]);
-                    if (most > sums.m) {
-                        const float d = fmaxf(sums.m - most, kLowest), f = sm_ex2(d * kLog2e);
-                        const float2 ff = make_float2(f, f);
-                        t = sm_mul2(ff, sm_fma2(make_float2(d, d), s, t));
-                        s = sm_mul2(ff, s);
-                        sums.m = most;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) sm_add_pair(make_float2(z[x], z[x + 1]), sums.m, s, t);
+                    take(q, n0 + 32 * c);
                 }
             }
             if (ok && row < p.rows) {
-                const long long slot = 2 * it.run + chalf;
-                if (TXL_BOUNDS(row < p.ld && slot < 2 * p.chunks, 1302, slot)) {
-                    float* const to = p.part + slot * 3 * p.ld + row;
-                    to[0] = sums.m;
-                    to[p.ld] = s.x + s.y;
-                    to[2 * p.ld] = t.x + t.y;
-                }
+                const int slot = 2 * it.run + chalf;
+                if (TXL_BOUNDS(row < p.ld && slot < 2 * p.chunks, 1302, slot))
+                    p.part[(long long)row * (2 * p.chunks) + slot] =
+                        make_float4(sums.m, sums.s.x + sums.s.y, sums.t.x + sums.t.y, 0.f);
             }
         }
     }
@@ -287,39 +337,38 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
     lb_sync<PAIR>();  // no CTA of a pair exits while the other may signal it or read its operands
     if (warp == 1) {
         tc_fence_after();
-        lb_tmem_dealloc<PAIR>(tmem, C::TMEM_COLS);
+        lb_tmem_dealloc<PAIR>(tmem, TMEM_COLS);
     }
 }
 
-// A row's results from its parts: 32 rows per CTA, a warp's lanes on a row each and its
-// parts dealt to the 32 warps.
-__global__ void __launch_bounds__(1024) linear_logprobs_join_kernel(const LpParams p, float* logprob, float* lse, float* entropy) {
-    __shared__ SoftmaxSums sh[32][33];
+// A row's results from its parts: a warp per row, its lanes on the parts.
+__global__ void __launch_bounds__(256) linear_logprobs_join_kernel(const LpParams p, float* logprob, float* lse, float* entropy) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5), n = 2 * p.chunks;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 32 + lane;
+    if (r >= p.rows) return;
+    const long long token = p.tokens[r];
+    const float4* const q = p.part + (long long)r * n;
+    const float given = token >= 0 && token < p.V ? p.given[r] : 0.f;
     SoftmaxSums a;
     a.clear();
-    if (row < p.rows) {
-#pragma unroll 4
-        for (int slot = warp; slot < 2 * p.chunks; slot += 32) {
-            const float* const q = p.part + (long long)slot * 3 * p.ld + row;
-            const SoftmaxSums b = {q[0], q[p.ld], q[2 * p.ld]};
+    for (int i = lane; i < n; i += 32 * 8) {  // 8 on their way at a time
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = i + 32 * u < n && TXL_BOUNDS(r < p.ld, 1303, r) ? q[i + 32 * u] : make_float4(-3.402823466e38f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const SoftmaxSums b = {v[u].x, v[u].y, v[u].z};
             a.merge(b);
         }
     }
-    sh[warp][lane] = a;
-    __syncthreads();
-    const int r = blockIdx.x * 32 + warp;  // now a warp per row
-    a = sh[lane][warp];
     a.merge_warp();
-    if (lane == 0 && r < p.rows) {
+    if (lane == 0) {
         const SoftmaxRow o(a);
-        const long long token = p.tokens[r];
         lse[r] = o.lse;
         entropy[r] = o.entropy;
-        logprob[r] = token < 0 ? 0.f : token < p.V ? o.logprob(p.given[r]) : __uint_as_float(0x7FFFFFFFu);
+        logprob[r] = token < 0 ? 0.f : token < p.V ? o.logprob(given) : __uint_as_float(0x7FFFFFFFu);
     }
 }
 
@@ -343,19 +392,19 @@ LpEncodeFn lp_encode_fn() {
     return fn;
 }
 
-// [rows, K] bf16 as boxes of 64 elements x 128 rows.
-bool lp_encode(CUtensorMap* map, const void* base, long long rows, int K) {
+// [rows, K] bf16 as boxes of 64 elements x `high` rows.
+bool lp_encode(CUtensorMap* map, const void* base, long long rows, int K, int high) {
     LpEncodeFn fn = lp_encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K * 2};
-    const cuuint32_t box[2] = {lp::BK, 128}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {lp::BK, (cuuint32_t)high}, es[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Microseconds that a stage takes a pair or a CTA, and that an item's end adds.
-constexpr double kStepPair = 0.36, kStepOne = 0.27, kItem = 1.0;
+// Microseconds that a stage takes at 256 columns and at least, and that an item's end adds.
+constexpr double kStepPair = 0.36, kStepOne = 0.36, kStepLeast = 0.15, kItem = 1.0;
 
 }  // namespace
 
@@ -365,48 +414,56 @@ LpPlan linear_logprobs_plan(int rows, int K, int V) {
     p.rows = rows;
     p.V = V;
     p.ksteps = (K + lp::BK - 1) / lp::BK;
+    p.klast = (K - (p.ksteps - 1) * lp::BK + 15) / 16;
     const int sms = current_sm_count();
     // The tile and the run with the least time by this model: rounds of items over the units.
     double best = -1;
     for (int ctas : {2, 1}) {
         const int most = sms / ctas, tile = lp::BM * ctas;
         if (most < 1) continue;
-        const int rt = (int)(((long long)rows + tile - 1) / tile), vt = (int)(((long long)V + tile - 1) / tile);
-        // (runs of each length that some number of rounds gives, up to 64 rounds)
-        for (int rounds = 1; rounds <= 64; ++rounds) {
-            const long long runs = std::max(1ll, (long long)most * rounds / rt);
-            const int per = (int)((vt + runs - 1) / runs), chunks = (vt + per - 1) / per;
-            const long long items = (long long)rt * chunks, units = std::min<long long>(items, most);
-            const double cost = (double)((items + units - 1) / units) * (per * p.ksteps * (ctas == 2 ? kStepPair : kStepOne) + kItem);
-            if (best >= 0 && cost >= best) continue;
-            best = cost;
-            pl.pair = ctas == 2;
-            pl.grid = (int)units * ctas;
-            p.n_rt = rt;
-            p.n_vt = vt;
-            p.per = per;
-            p.chunks = chunks;
-            p.ld = (long long)rt * tile;
+        const int rt = (int)(((long long)rows + tile - 1) / tile);
+        // (narrower tiles only where the units have few)
+        const bool few = (double)rt * ((double)V / lp::MAX_BN) < 16.0 * most;
+        for (int bn = lp::MAX_BN; bn >= (few ? 64 : lp::MAX_BN); bn -= 64) {
+            const int vt = (int)(((long long)V + bn - 1) / bn);
+            const double step = std::max(kStepLeast, (ctas == 2 ? kStepPair : kStepOne) * bn / lp::MAX_BN);
+            for (int rounds = 1; rounds <= (few ? 4 : 24); ++rounds) {
+                const int runs = (int)std::max(1ll, std::min<long long>(vt, (long long)most * rounds / rt));
+                const int per = (vt + runs - 1) / runs, chunks = (vt + per - 1) / per;
+                const long long items = (long long)rt * chunks, units = std::min<long long>(items, most);
+                const double cost = (double)((items + units - 1) / units) * (per * p.ksteps * step + kItem);
+                if (best >= 0 && cost >= best) continue;
+                best = cost;
+                pl.pair = ctas == 2;
+                pl.grid = (int)units * ctas;
+                p.bn = bn;
+                p.n_rt = rt;
+                p.n_vt = vt;
+                p.per = per;
+                p.chunks = chunks;
+                p.ld = (long long)rt * tile;
+            }
         }
     }
     return pl;
 }
 
-size_t linear_logprobs_workspace_bytes(const LpPlan& pl) { return ((size_t)pl.p.chunks * 6 + 1) * pl.p.ld * sizeof(float); }
+size_t linear_logprobs_workspace_bytes(const LpPlan& pl) { return ((size_t)pl.p.chunks * 2 * sizeof(float4) + sizeof(float)) * pl.p.ld; }
 
 namespace {
 
-template <bool PAIR>
+template <bool PAIR, int BN, bool BIAS>
 cudaError_t lp_launch(const LpMaps& maps, const LpPlan& pl, cudaStream_t stream) {
+    using C = lp::Cfg<PAIR, BN>;
     static PerDeviceOnce attrs;
     const cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(linear_logprobs_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, lp::SMEM_BYTES);
+        return cudaFuncSetAttribute(linear_logprobs_kernel<PAIR, BN, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.grid);
     cfg.blockDim = dim3(lp::NTHREADS);
-    cfg.dynamicSmemBytes = lp::SMEM_BYTES;
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -417,7 +474,17 @@ cudaError_t lp_launch(const LpMaps& maps, const LpPlan& pl, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_logprobs_kernel<PAIR>, maps, pl.p);
+    return cudaLaunchKernelEx(&cfg, linear_logprobs_kernel<PAIR, BN, BIAS>, maps, pl.p);
+}
+
+template <bool PAIR, bool BIAS>
+cudaError_t lp_launch(const LpMaps& maps, const LpPlan& pl, cudaStream_t stream) {
+    switch (pl.p.bn) {
+        case 64: return lp_launch<PAIR, 64, BIAS>(maps, pl, stream);
+        case 128: return lp_launch<PAIR, 128, BIAS>(maps, pl, stream);
+        case 192: return lp_launch<PAIR, 192, BIAS>(maps, pl, stream);
+        default: return lp_launch<PAIR, 256, BIAS>(maps, pl, stream);
+    }
 }
 
 }  // namespace
@@ -428,16 +495,18 @@ cudaError_t launch_linear_logprobs(LpPlan pl, const void* x, const void* w, cons
     LpParams& p = pl.p;
     p.tokens = tokens;
     p.bias = static_cast<const __nv_bfloat16*>(bias);
-    p.part = static_cast<float*>(workspace);
-    p.given = p.part + (size_t)p.chunks * 6 * p.ld;
+    p.wide_bias = (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
+    p.part = static_cast<float4*>(workspace);
+    p.given = reinterpret_cast<float*>(p.part + (size_t)p.chunks * 2 * p.ld);
     p.status = status;
     LpMaps maps;
-    if (!lp_encode(&maps.x, x, p.rows, K) || !lp_encode(&maps.w, w, p.V, K)) return cudaErrorInvalidValue;
-    const cudaError_t e = pl.pair ? lp_launch<true>(maps, pl, stream) : lp_launch<false>(maps, pl, stream);
+    if (!lp_encode(&maps.x, x, p.rows, K, lp::BM) || !lp_encode(&maps.w, w, p.V, K, p.bn / (pl.pair ? 2 : 1))) return cudaErrorInvalidValue;
+    const cudaError_t e = pl.pair ? (bias ? lp_launch<true, true>(maps, pl, stream) : lp_launch<true, false>(maps, pl, stream))
+                                  : (bias ? lp_launch<false, true>(maps, pl, stream) : lp_launch<false, false>(maps, pl, stream));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.rows + 31ll) / 32));
-    cfg.blockDim = dim3(1024);
+    cfg.gridDim = dim3((unsigned)((p.rows + 7ll) / 8));
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -7,13 +7,15 @@ namespace txl {
 
 struct LpParams {
     int rows, V;
-    int ksteps;            // 64-element steps of K
+    int ksteps, klast;     // 64-element steps of K; MMAs (of 16 elements) of the last one
+    int bn;                // columns of a tile, a multiple of 64 up to 256
     int n_rt, n_vt;        // tiles of rows and of columns
     int per, chunks;       // column tiles of an item; items per row tile
     long long ld;          // rows of the partial sums, whole tiles
     const long long* tokens;
     const __nv_bfloat16* bias;  // [V] or null
-    float* part;           // [2 chunks][3][ld]: m, s, t of each half of an item's columns
+    int wide_bias;         // bias is 16-byte aligned
+    float4* part;          // [ld][2 chunks]: (m, s, t) of each half of an item's columns
     float* given;          // [ld]: the token's logit
     int* status;
 };

@@ -1,21 +1,31 @@
-// The running statistics of a softmax in one pass: of the values x seen so far
+// The running statistics of a softmax in one pass: of the values x seen so far, with
+// L = log2 e as fp32 has it,
 //
-//   m = max x,   s = sum e^(x - m),   t = sum e^(x - m) (x - m)
+//   m near max x,   r = m L (rounded),   s = sum 2^(x L - r),   t = sum 2^(x L - r) (x L - r)
 //
-// all in fp32, from which log-sum-exp = m + ln s and entropy = ln s - t / s.
-// When the maximum moves from m to M, with d = m - M <= 0, the sums become
-// s e^d and e^d (t + d s).  Differences are held at or above kLowest: what a value of
-// -inf adds to t is then 0 times a finite number (e^kLowest is 0, and kLowest times 2^30
-// values is finite), not 0 times -inf;
-// and m starts at the lowest finite number, so that x - m of x = -inf is not NaN.
-// A NaN or +inf among the values makes s and t NaN.
+// all in fp32, from which log-sum-exp = (r + log2 s) / L and entropy = (log2 s - t / s) ln 2.
+// The reference is r itself, so that its rounding is no error, and a term costs one fused
+// product before its power of two; that L is off by 1.3e-8 of itself is a temperature off
+// by as much.  When the reference moves from m to M, with d = r(m) - r(M) <= 0, the sums
+// become s 2^d and 2^d (t + d s).  m need not be the maximum itself: it follows once a value
+// is kSlack above it (moved each time, some lane of a warp had to in most of the steps).
+//
+// What is not ordinary: a value of -inf, or one so low that x L - r is, would make t NaN (0
+// times -inf).  Either nothing below kLow is added, whose power is 0 and whose product with
+// it too, or t is taken once more so for a batch that made it NaN (in linear_logprobs, where
+// an instruction for each logit cost a tenth of the time).  A reference beyond +-kHuge is the
+// maximum: numbers lie 1e28 and more apart there, and s counts those equal to it.  m starts at
+// the lowest finite number, which is beyond -kHuge and equals no -inf.  A NaN or +inf among
+// the values makes s and t NaN.
 #pragma once
 #include <cuda_bf16.h>
 
 namespace txl {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLowest = -1e20f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLow = -1e38f, kHuge = 1e36f;
+constexpr float kSlack = 4.f;
+constexpr float kLowest = -1e20f;  // differences of references are held at or above it (times 2^30 terms it is finite)
 
 __device__ __forceinline__ float sm_ex2(float x) {
     float y;
@@ -26,6 +36,12 @@ __device__ __forceinline__ float sm_ex2(float x) {
 __device__ __forceinline__ float sm_max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// The largest of three, a NaN left out.
+__device__ __forceinline__ float sm_max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 // Packed fp32 pairs, each half rounded as the scalar operation.
@@ -52,62 +68,112 @@ __device__ __forceinline__ float2 sm_fma2(float2 a, float2 b, float2 c) {
     return *reinterpret_cast<float2*>(&r);
 }
 
+__device__ __forceinline__ bool sm_ordinary(float m) { return fabsf(m) < kHuge; }
+__device__ __forceinline__ float sm_reference(float m) { return __fmul_rn(m, kLog2e); }
+
+// What sums against the maximum m are worth against M >= m: the factor, and d of the above.
+__device__ __forceinline__ float sm_factor(float m, float M, float& d) {
+    d = fmaxf(sm_reference(m) - sm_reference(M), kLowest);
+    if (sm_ordinary(M)) return sm_ex2(d);
+    d = 0.f;
+    return m == M ? 1.f : 0.f;
+}
+
 struct SoftmaxSums {
     float m, s, t;
     __device__ __forceinline__ void clear() { m = -3.402823466e38f, s = 0.f, t = 0.f; }
-    // The maximum becomes `to` where that is larger.
-    __device__ __forceinline__ void raise(float to) {
-        if (to > m) {
-            const float d = fmaxf(m - to, kLowest), f = sm_ex2(d * kLog2e);
+    // One more value.
+    __device__ __forceinline__ void add(float x) {
+        float d;
+        if (x > m) {
+            const float f = sm_factor(m, x, d);
             t = f * fmaf(d, s, t);
             s = f * s;
-            m = to;
+            m = x;
+        }
+        if (sm_ordinary(m)) {
+            const float y = fmaf(sm_max_nan(x, kLow), kLog2e, -sm_reference(m)), e = sm_ex2(y);
+            s += e;
+            t = fmaf(e, y, t);
+        } else {
+            s += x == m ? (x - x) + 1.f : x != x ? x : 0.f;
         }
     }
     __device__ __forceinline__ void merge(const SoftmaxSums& o) {
         const float M = fmaxf(m, o.m);
-        const float d = fmaxf(m - M, kLowest), e = fmaxf(o.m - M, kLowest);
-        const float f = sm_ex2(d * kLog2e), g = sm_ex2(e * kLog2e);
+        float d, e;
+        const float f = sm_factor(m, M, d), g = sm_factor(o.m, M, e);
         t = fmaf(f, fmaf(d, s, t), g * fmaf(e, o.s, o.t));
         s = fmaf(f, s, g * o.s);
         m = M;
     }
-    // Over the warp, every lane with the same result (the same order of additions).
+    // Over the warp, every lane with the same result.
     __device__ __forceinline__ void merge_warp() {
+        float M, d;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
+        const float f = sm_factor(m, M, d);
+        t = f * fmaf(d, s, t);
+        s = f * s;
+        m = M;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            SoftmaxSums b;
-            b.m = __shfl_xor_sync(0xffffffffu, m, o);
-            b.s = __shfl_xor_sync(0xffffffffu, s, o);
-            b.t = __shfl_xor_sync(0xffffffffu, t, o);
-            merge(b);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            t += __shfl_xor_sync(0xffffffffu, t, o);
         }
     }
 };
 
-// Two values, neither above m, onto pairs of sums.
-__device__ __forceinline__ void sm_add_pair(float2 x, float m, float2& s, float2& t) {
-    float2 d = sm_add2(x, make_float2(-m, -m));
-    d.x = sm_max_nan(d.x, kLowest);
-    d.y = sm_max_nan(d.y, kLowest);
-    const float2 y = sm_mul2(d, make_float2(kLog2e, kLog2e));
-    const float2 e = make_float2(sm_ex2(y.x), sm_ex2(y.y));
-    s = sm_add2(s, e);
-    t = sm_fma2(e, d, t);
-}
+// Sums of many values in pairs; SoftmaxSums once they are folded.
+struct SoftmaxPairs {
+    float m;
+    float2 s, t;
+    __device__ __forceinline__ void clear() { m = -3.402823466e38f, s = t = make_float2(0.f, 0.f); }
+    // Ahead of values of which `to` is the largest.
+    __device__ __forceinline__ void raise(float to) {
+        if (to > m + kSlack) {
+            float d;
+            const float f = sm_factor(m, to, d);
+            const float2 ff = make_float2(f, f);
+            t = sm_mul2(ff, sm_fma2(make_float2(d, d), s, t));
+            s = sm_mul2(ff, s);
+            m = to;
+        }
+    }
+    // Two values up to m + kSlack, or NaN; m ordinary, r = sm_reference(m).
+    __device__ __forceinline__ void add(float2 x, float r) {
+        const float2 y = sm_fma2(x, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
+        const float2 e = make_float2(sm_ex2(y.x), sm_ex2(y.y));
+        s = sm_add2(s, e);
+        t = sm_fma2(e, y, t);
+    }
+    // Whether t has to be taken again, from what it was, by add_low over the same values.
+    __device__ __forceinline__ bool lost() const { return t.x != t.x || t.y != t.y; }
+    __device__ __forceinline__ void add_low(float2 x, float r) {
+        x = make_float2(sm_max_nan(x.x, kLow), sm_max_nan(x.y, kLow));
+        const float2 y = sm_fma2(x, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
+        t = sm_fma2(make_float2(sm_ex2(y.x), sm_ex2(y.y)), y, t);
+    }
+    // One value not above m (or NaN), where m is not ordinary.
+    __device__ __forceinline__ void add_far(float x) { s.x += x == m ? (x - x) + 1.f : x != x ? x : 0.f; }
+    __device__ __forceinline__ SoftmaxSums fold() const { return {m, s.x + s.y, t.x + t.y}; }
+};
 
 // What a row's sums say: log-sum-exp, entropy, and log p of a value of the row.  A row
 // of nothing but -inf has no probabilities: log-sum-exp and log p are -inf, its entropy 0.
 struct SoftmaxRow {
-    float m, log_s, lse, entropy;
+    float m, log_s, lse, entropy;  // log_s: log2 s
     __device__ __forceinline__ explicit SoftmaxRow(const SoftmaxSums& a) {
         m = a.m;
-        log_s = logf(a.s);  // -inf where s is 0
-        lse = a.m + log_s;
-        const float h = log_s - a.t / a.s;
+        log_s = log2f(a.s);  // -inf where s is 0
+        lse = sm_ordinary(m) ? (sm_reference(m) + log_s) * (1.f / kLog2e) : m + log_s * kLn2;
+        const float h = (log_s - a.t / a.s) * kLn2;
         entropy = a.s == 0.f || h < 0.f ? 0.f : h;
     }
-    __device__ __forceinline__ float logprob(float x) const { return log_s == -INFINITY ? -INFINITY : (x - m) - log_s; }
+    __device__ __forceinline__ float logprob(float x) const {
+        if (log_s == -INFINITY) return -INFINITY;
+        // (x L may leave the range below kLow, where ln s is nothing beside x)
+        return sm_ordinary(m) && !(x < kLow) ? (fmaf(x, kLog2e, -sm_reference(m)) - log_s) * kLn2 : (x - m) - log_s * kLn2;
+    }
 };
 
 }  // namespace txl

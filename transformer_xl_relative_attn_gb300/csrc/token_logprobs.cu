@@ -10,11 +10,16 @@
 // bounds it is that read.  A row goes to a warp where it is short, to a CTA, or, where
 // rows are few, to a cluster of CTAs, each with a part of the row: the parts meet in the
 // first CTA's shared memory, so there is one launch, no workspace, and the order of the
-// additions depends on the sizes alone.
+// additions depends on sizes and alignment alone.
 //
-// The best `top` of a warp lie sorted in its lanes, one each, as 64-bit keys (the value's
-// order, then the complement of the index: no two are alike).  A vector of logits whose
-// maximum is below the last of them costs one comparison and a vote.
+// Alternatives are ordered as 64-bit keys: the value's order, then the complement of the
+// index, so that no two are alike.  In the pass over the row a thread only notes which two
+// of its 16-byte vectors have the largest values, and the largest of the others (14
+// instructions a vector; keeping the best in order as they come took the kernel twice its
+// time).  Behind it the threads' best elements are put in order, by sorting within warps
+// and by rank among the warps' lists, and the k-th of them is a bar: a second element of a
+// thread can only count where one reaches it.  Then its warp looks at its two vectors each
+// again, and at its whole part where some third vector reaches the bar too.
 //
 // The gradient is a pass of its own, read once and written once, in place where the
 // caller wants it.
@@ -49,6 +54,12 @@ struct Vec<__nv_bfloat16> {
     __device__ __forceinline__ float2 pair(int i) const {  // i known at compile time
         return halves(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
     }
+    // the same with nothing below kLow
+    __device__ __forceinline__ float2 pair_from_low(int i) const {
+        const unsigned w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w, low = 0xFE96FE96u;  // kLow, cut to bf16
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&low));
+        return halves(*reinterpret_cast<const unsigned*>(&m));
+    }
     __device__ __forceinline__ float max() const {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
         const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
@@ -68,6 +79,10 @@ struct Vec<float> {
     __device__ __forceinline__ float2 pair(int i) const {
         return i == 0 ? make_float2(__uint_as_float(q.x), __uint_as_float(q.y))
                       : make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+    __device__ __forceinline__ float2 pair_from_low(int i) const {
+        const float2 p = pair(i);
+        return make_float2(sm_max_nan(p.x, kLow), sm_max_nan(p.y, kLow));
     }
     __device__ __forceinline__ float max() const {
         return sm_max_nan(sm_max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
@@ -117,113 +132,290 @@ __device__ __forceinline__ float value_of(unsigned o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// The best keys that a warp has seen, lane i with the i-th; `last` is the k-th.
+__device__ __forceinline__ unsigned long long key_of(float x, unsigned index) {
+    return (unsigned long long)order_of(x) << 32 | (unsigned)~index;
+}
+
+// The larger of each two lanes `apart` goes to the one whose `down` is false.
+__device__ __forceinline__ unsigned long long exchange(unsigned long long a, int apart, bool down) {
+    const unsigned long long b = __shfl_xor_sync(kAll, a, apart);
+    return (a > b) == down ? b : a;
+}
+// The best 32 of a falling list (a key per lane) and of one candidate per lane, falling.
+// (A call: inlined where it is needed, code of several times the size missed its cache.)
+__device__ __noinline__ unsigned long long merge_all(unsigned long long key, unsigned long long c) {
+    const int lane = threadIdx.x & 31;
+    // sorted upwards, so that against the list's order each lane keeps the larger of two:
+    // the best 32 of both, rising and then falling, to be sorted downwards
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int apart = size / 2; apart > 0; apart /= 2)
+            c = exchange(c, apart, ((lane & apart) == 0) == ((lane & size) == 0));
+    key = c > key ? c : key;
+#pragma unroll
+    for (int apart = 16; apart > 0; apart /= 2) key = exchange(key, apart, (lane & apart) != 0);
+    return key;
+}
+
+// The keys of a warp's lanes in falling order, the first k of them at least (0: none).
+__device__ __forceinline__ unsigned long long in_order(unsigned long long c, int k) {
+    if (k > 8) return merge_all(0ull, c);
+    // one by one: a round takes fewer instructions than two steps of the sort
+    const int lane = threadIdx.x & 31;
+    unsigned long long key = 0;
+#pragma unroll 1
+    for (int i = 0; i < k; ++i) {
+        const unsigned hi = (unsigned)(c >> 32), top = __reduce_max_sync(kAll, hi);
+        const unsigned low = __reduce_max_sync(kAll, hi == top ? (unsigned)c : 0u);
+        const unsigned long long n = (unsigned long long)top << 32 | low;
+        if (lane == i) key = n;
+        if (c == n) c = 0;
+    }
+    return key;
+}
+
+// The best keys that a warp has seen, lane i with the i-th.
 struct Best {
-    unsigned long long key, last;
-    float bar;  // value of the k-th, -inf while there are fewer
-    __device__ __forceinline__ void clear() { key = last = 0, bar = -INFINITY; }
-    // One candidate per lane (0: none).
-    __device__ __forceinline__ void offer(unsigned long long c, int k) {
+    unsigned long long key, last;  // `last`: the k-th, or what a key has to be above to count
+    float bar;                     // its value, -inf where there is none
+    __device__ __forceinline__ void settle(int k, unsigned long long floor) {
+        const unsigned long long n = __shfl_sync(kAll, key, k - 1);
+        last = n > floor ? n : floor;
+        bar = last ? value_of((unsigned)(last >> 32)) : -INFINITY;
+    }
+    // One candidate per lane (0: none), no key twice; all lanes of the warp together.
+    __device__ __forceinline__ void offer(unsigned long long c, int k, unsigned long long floor) {
         const int lane = threadIdx.x & 31;
         unsigned more = __ballot_sync(kAll, c > last);
         if (!more) return;
+        if (__popc(more) > kSingly) {
+            key = merge_all(key, c);
+            settle(k, floor);
+            return;
+        }
+#pragma unroll 1
         do {
             const int src = __ffs(more) - 1;
             const unsigned long long n = __shfl_sync(kAll, c, src);
             const unsigned long long up = __shfl_up_sync(kAll, key, 1);
             const int at = __popc(__ballot_sync(kAll, key > n));
             key = lane < at ? key : lane == at ? n : up;
-            last = __shfl_sync(kAll, key, k - 1);
+            settle(k, floor);
             if (lane == src) c = 0;
             more = __ballot_sync(kAll, c > last);
         } while (more);
-        bar = last ? value_of((unsigned)(last >> 32)) : -INFINITY;
-    }
-    __device__ __forceinline__ void offer(bool valid, float x, unsigned index, int k) {
-        offer(valid ? (unsigned long long)order_of(x) << 32 | (unsigned)~index : 0ull, k);
     }
     // Whether a vector of this maximum may hold one of the best.
     __device__ __forceinline__ bool worth(float max) const { return !(max < bar); }
+
+    // Candidates are taken one by one up to this many at a time, sorted together beyond: an
+    // insertion is a chain of some 110 cycles, a sort and merge one of 700.
+    static constexpr int kSingly = 4;
 };
 
+// How many of a falling list of k keys are above `key`.
+__device__ __forceinline__ int above(const unsigned long long* list, int k, unsigned long long key) {
+    int n = 0;
+#pragma unroll
+    for (int step = kTopMost; step > 0; step /= 2)
+        if (n + step <= k && list[n + step - 1] > key) n += step;
+    return n;
+}
+
 // ------------------------------------------------------------ one warp's share of a row
-// Vectors first + 32 warp + lane + i step, i = 0, 1, .., below `end`, and, with `loose`,
-// the elements outside the vectors.
+// What a thread notes for the alternatives: the orders of its vectors' three largest
+// values, and the vectors of the first two (of equal ones the first that came).
+struct Noted {
+    unsigned most, next, third;
+    int at, at2;
+    __device__ __forceinline__ void clear() { most = next = third = 0, at = at2 = -1; }
+    __device__ __forceinline__ void see(float max, int vec) {
+        const unsigned o = order_of(max);
+        third = ::max(third, ::min(o, next));
+        at2 = o > most ? at : o > next ? vec : at2;
+        next = ::max(next, ::min(o, most));
+        at = o > most ? vec : at;
+        most = ::max(o, most);
+    }
+};
+
+// A warp's vectors are first + lane + i step, i = 0, 1, .., below `end`; with `loose` it has
+// the elements outside the vectors too.
+struct Share {
+    int first, end, step;
+    bool loose;
+    int vecs;  // of the row
+};
+
 template <typename T, bool TOP, int U>
-__device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, int first, int end, int step, bool loose, int k,
-                                     SoftmaxSums& sums, Best& best) {
+__device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, const Share& sh, SoftmaxSums& sums, Noted& noted) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31;
     const T* const vec0 = row + cut.head;
-    float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
-    // sums' own s and t stay 0 until the end: the pairs hold them
-#pragma unroll 1
-    for (int base = first; base < end; base += U * step) {
-        Vec<T> v[U];
+    SoftmaxPairs acc;
+    acc.clear();
+    auto load = [&](Vec<T>(&v)[U], int base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = base + u * step + lane;
-            v[u].q = i < end && TXL_BOUNDS(i >= 0 && cut.head + (long long)(i + 1) * N <= V, 1101, i)
+            const int i = base + u * sh.step + lane;
+            v[u].q = i < sh.end && TXL_BOUNDS(i >= 0 && cut.head + (long long)(i + 1) * N <= V, 1101, i)
                          ? load_stream(vec0 + (size_t)i * N)
                          : Vec<T>::nothing();
         }
-        float most[U], all = v[0].max();
-        most[0] = all;
+    };
+    auto take = [&](const Vec<T>(&v)[U], int base) {
+        float all = v[0].max();
+        if (TOP) noted.see(all, base + lane);
 #pragma unroll
         for (int u = 1; u < U; ++u) {
-            most[u] = v[u].max();
-            all = sm_max_nan(all, most[u]);
+            const float most = v[u].max();
+            if (TOP) noted.see(most, base + u * sh.step + lane);
+            all = sm_max_nan(all, most);
         }
-        if (all > sums.m) {
-            const float d = fmaxf(sums.m - all, kLowest), f = sm_ex2(d * kLog2e);
-            const float2 ff = make_float2(f, f);
-            t = sm_mul2(ff, sm_fma2(make_float2(d, d), s, t));
-            s = sm_mul2(ff, s);
-            sums.m = all;
-        }
+        acc.raise(all);
+        if (sm_ordinary(acc.m)) {
+            const float r = sm_reference(acc.m);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) sm_add_pair(v[u].pair(i), sums.m, s, t);
-        if (TOP) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!__any_sync(kAll, best.worth(most[u]))) continue;
-                const int i = base + u * step + lane;
+                for (int i = 0; i < N / 2; ++i) acc.add(v[u].pair_from_low(i), r);
+        } else {
 #pragma unroll 1
-                for (int j = 0; j < N; ++j) best.offer(i < end, v[u].at(j), cut.head + i * N + j, k);
+            for (int u = 0; u < U; ++u) {
+                Vec<T> x = v[0];
+#pragma unroll
+                for (int i = 1; i < U; ++i)
+                    if (u == i) x = v[i];
+#pragma unroll 1
+                for (int j = 0; j < N; ++j) acc.add_far(x.at(j));
             }
         }
+    };
+    const int stride = U * sh.step;
+    Vec<T> v[U];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll 1
+        for (int base = sh.first; base < sh.end; base += stride) {
+            load(v, base);
+            take(v, base);
+        }
+    } else {
+        // A batch is on its way while the one before is worked on (1001 x 50021: 37 us, one at
+        // a time 55; in bf16, whose batches have twice the elements and whose CTAs would be
+        // fewer, 11264 x 32768 took 134 us so and takes 112 one at a time).
+        Vec<T> w[U];
+        if (sh.first < sh.end) load(v, sh.first);
+#pragma unroll 1
+        for (int base = sh.first; base < sh.end; base += 2 * stride) {
+            if (base + stride < sh.end) load(w, base + stride);
+            take(v, base);
+            if (base + 2 * stride < sh.end) load(v, base + 2 * stride);
+            if (base + stride < sh.end) take(w, base + stride);
+        }
     }
-    sums.s = s.x + s.y;
-    sums.t = t.x + t.y;
-    if (loose) {
-        const bool mine = lane < cut.loose;
-        const int at = mine ? cut.index<T>(lane) : 0;
-        const float x = mine && TXL_BOUNDS(at < V, 1102, at) ? load_one(row + at) : -INFINITY;
-        sums.raise(x);
-        const float d = sm_max_nan(x - sums.m, kLowest), e = sm_ex2(d * kLog2e);
-        sums.s += e;
-        sums.t = fmaf(e, d, sums.t);
-        if (TOP) best.offer(mine, x, at, k);
+    sums = acc.fold();
+    if (sh.loose && lane < cut.loose) {
+        const int at = cut.index<T>(lane);
+        if (TXL_BOUNDS(at < V, 1102, at)) sums.add(load_one(row + at));
     }
 }
 
-// A row's results from its sums and the best keys (of one warp, all lanes of it here).
-template <typename T, bool TOP>
-__device__ __forceinline__ void finish(const TokenLogprobs& a, long long r, const SoftmaxSums& sums, const Best& best, long long token,
-                                       float given) {
+// The key of a thread's best element in its vectors (0: it has none); `next` becomes the
+// largest order that another of them may have.
+template <typename T>
+__device__ __forceinline__ unsigned long long best_of(const T* row, int V, const RowCut& cut, const Share& sh, const Noted& noted,
+                                                      unsigned& next) {
+    constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31;
-    const SoftmaxRow row(sums);
-    if (lane == 0) {
-        a.lse[r] = row.lse;
-        a.entropy[r] = row.entropy;
-        a.logprob[r] = token < 0 ? 0.f : token < a.V ? row.logprob(given) : __uint_as_float(0x7FFFFFFFu);
+    unsigned long long key = 0;
+    next = noted.next;
+    if (sh.first + lane < sh.end && TXL_BOUNDS(noted.at >= 0 && cut.head + (long long)(noted.at + 1) * N <= V, 1106, noted.at)) {
+        Vec<T> v;
+        v.q = load_stream(row + cut.head + (size_t)noted.at * N);
+        unsigned most = 0;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float2 p = v.pair(j / 2);
+            const unsigned o = order_of(j & 1 ? p.y : p.x);
+            next = ::max(next, ::min(o, most));
+            at = o > most ? j : at;
+            most = ::max(o, most);
+        }
+        key = (unsigned long long)most << 32 | (unsigned)~(cut.head + noted.at * N + at);
     }
-    if (TOP && lane < a.top) {
-        a.top_index[r * a.top + lane] = (unsigned)~(unsigned)best.key;
-        a.top_logprob[r * a.top + lane] = row.logprob(value_of((unsigned)(best.key >> 32)));
+    return key;
+}
+
+// The best keys of a warp as they stand behind best_of: its lanes' best, `mine`, and the
+// elements outside the vectors.
+template <typename T>
+__device__ __forceinline__ unsigned long long first_list(const T* row, int V, const RowCut& cut, const Share& sh, unsigned long long mine,
+                                                         int k) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long list = in_order(mine, k);
+    if (sh.loose && cut.loose) {
+        const int at = lane < cut.loose ? cut.index<T>(lane) : 0;
+        list = merge_all(list, lane < cut.loose && TXL_BOUNDS(at < V, 1107, at) ? key_of(load_one(row + at), at) : 0ull);
     }
+    return list;
+}
+
+// A warp's two best vectors per lane once more, or all of its part, for what else is among
+// its best `k` and not below the order `bar`: its list (a key per lane, falling) with the
+// threads' best, `mine`, in it already.
+template <typename T>
+__device__ __noinline__ unsigned long long look_again(const T* vec0, int head, const Share sh, int at, int at2, bool all,
+                                                      unsigned long long list, unsigned long long mine, unsigned bar, int k) {
+    constexpr int N = Vec<T>::N;
+    const int lane = threadIdx.x & 31;
+    const unsigned long long floor = (unsigned long long)bar << 32;
+    Best best;
+    best.key = list;
+    best.settle(k, floor);
+    auto load = [&](int i) {
+        Vec<T> v;
+        v.q = i >= 0 && i < sh.end && TXL_BOUNDS(i < sh.vecs, 1108, i) ? load_stream(vec0 + (size_t)i * N) : Vec<T>::nothing();
+        return v;
+    };
+    if (all) at = sh.first + lane, at2 = at + sh.step;
+    Vec<T> v = load(at), w = load(at2);
+#pragma unroll 1
+    for (int left = all ? (sh.end - sh.first + sh.step - 1) / sh.step : 2; left > 0; --left) {
+        const Vec<T> x = v;
+        const int i = at;
+        v = w;
+        at = at2;
+        if (all) {
+            at2 += sh.step;
+            w = load(at2);
+        }
+        unsigned bits = 0;  // elements that may count
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float2 p = x.pair(j / 2);
+            bits |= best.worth(j & 1 ? p.y : p.x) ? 1u << j : 0u;
+        }
+        if (i < 0 || i >= sh.end) bits = 0;
+        while (__any_sync(kAll, bits != 0)) {
+            const int j = bits ? __ffs(bits) - 1 : 0;
+            const unsigned long long c = bits ? key_of(x.at(j), head + i * N + j) : 0ull;
+            best.offer(c == mine ? 0ull : c, k, floor);
+            bits &= bits - 1;
+        }
+    }
+    return best.key;
+}
+
+__device__ __forceinline__ void write_statistics(const TokenLogprobs& a, long long r, const SoftmaxRow& row, long long token, float given) {
+    a.lse[r] = row.lse;
+    a.entropy[r] = row.entropy;
+    a.logprob[r] = token < 0 ? 0.f : token < a.V ? row.logprob(given) : __uint_as_float(0x7FFFFFFFu);
+}
+__device__ __forceinline__ void write_best(const TokenLogprobs& a, long long r, const SoftmaxRow& row, int i, unsigned long long key) {
+    a.top_index[r * a.top + i] = (unsigned)~(unsigned)key;
+    a.top_logprob[r * a.top + i] = row.logprob(value_of((unsigned)(key >> 32)));
 }
 
 template <typename T>
@@ -231,24 +423,35 @@ __device__ __forceinline__ float given_logit(const T* row, long long token, int 
     return token >= 0 && token < V ? load_one(row + token) : 0.f;
 }
 
-// One row per warp.
-template <typename T, bool TOP>
+// One row per warp, U vectors per lane at a time.
+template <typename T, bool TOP, int U>
 __global__ void __launch_bounds__(kThreads) logprobs_warp_kernel(const TokenLogprobs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
     const long long r = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (r >= a.rows) return;
     const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
     const long long token = a.tokens[r];
     const float given = given_logit(row, token, a.V);
     const RowCut cut(row, a.V);
+    const Share sh = {0, cut.vecs, 32, true, cut.vecs};
     SoftmaxSums sums;
-    Best best;
-    sums.clear();
-    best.clear();
-    scan<T, TOP, 2>(row, a.V, cut, 0, cut.vecs, 32, true, a.top, sums, best);
+    Noted noted;
+    noted.clear();
+    scan<T, TOP, U>(row, a.V, cut, sh, sums, noted);
     sums.merge_warp();
-    finish<T, TOP>(a, r, sums, best, token, given);
+    const SoftmaxRow out(sums);
+    if (lane == 0) write_statistics(a, r, out, token, given);
+    if (TOP) {
+        unsigned next;
+        const unsigned long long mine = best_of(row, a.V, cut, sh, noted, next);
+        unsigned long long key = first_list(row, a.V, cut, sh, mine, a.top);
+        const unsigned bar = (unsigned)(__shfl_sync(kAll, key, a.top - 1) >> 32);
+        if (__any_sync(kAll, next >= bar))
+            key = look_again(row + cut.head, cut.head, sh, noted.at, noted.at2, __any_sync(kAll, noted.third >= bar), key, mine, bar, a.top);
+        if (lane < a.top) write_best(a, r, out, lane, key);
+    }
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -262,22 +465,37 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
+// Lists of keys, one behind the other without a gap.
 struct RowShared {
+    unsigned bar;  // order of the k-th best of the threads' best
     SoftmaxSums sums[kWarps];
-    unsigned long long best[kWarps][kTopMost];
+    unsigned long long best[kWarps * kTopMost];
     // of the cluster's CTAs, in its first one
     SoftmaxSums part[kMaxCluster];
-    unsigned long long part_best[kMaxCluster][kTopMost];
+    unsigned long long part_best[kMaxCluster * kTopMost];
 };
+static_assert(kMaxCluster <= kWarps, "a CTA's threads hold a key of each of the cluster's lists");
+
+// Of n lists of k keys, this thread's (below n k) and how many of all are above it.
+__device__ __forceinline__ int rank_of(const unsigned long long* lists, int n, int k, unsigned long long& key) {
+    key = lists[threadIdx.x];
+    int above_it = 0;
+#pragma unroll 4
+    for (int l = 0; l < n; ++l) above_it += above(lists + l * k, k, key);
+    return above_it;
+}
 
 // One row per CTA, or per cluster of CTAs.
 template <typename T, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads) logprobs_cta_kernel(const TokenLogprobs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (TOP ? 5 : 6) : (TOP ? 4 : 3)) logprobs_cta_kernel(const TokenLogprobs a) {
     __shared__ RowShared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (CLUSTER) {
+        if (TOP) sh.part_best[threadIdx.x] = 0;  // (lists of less than k keys: 0 in place of the rest)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = a.top;
     const int ctas = CLUSTER ? cluster_size() : 1, rank = CLUSTER ? cluster_rank() : 0;
     const long long r = blockIdx.x / ctas;
     const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
@@ -285,53 +503,79 @@ __global__ void __launch_bounds__(kThreads) logprobs_cta_kernel(const TokenLogpr
     const float given = given_logit(row, token, a.V);
     const RowCut cut(row, a.V);
     const int from = (int)((long long)cut.vecs * rank / ctas), to = (int)((long long)cut.vecs * (rank + 1) / ctas);
+    const Share share = {from + 32 * warp, to, kThreads, rank == 0 && warp == 0, cut.vecs};
     SoftmaxSums sums;
-    Best best;
-    sums.clear();
-    best.clear();
-    scan<T, TOP, 32 / Vec<T>::N>(row, a.V, cut, from + 32 * warp, to, kThreads, rank == 0 && warp == 0, a.top, sums, best);
+    Noted noted;
+    noted.clear();
+    scan<T, TOP, 4>(row, a.V, cut, share, sums, noted);
     sums.merge_warp();
     if (lane == 0) sh.sums[warp] = sums;
-    if (TOP) sh.best[warp][lane] = best.key;
+    unsigned next = 0;
+    unsigned long long mine = 0, list = 0;
+    if (TOP) {
+        mine = best_of(row, a.V, cut, share, noted, next);
+        list = first_list(row, a.V, cut, share, mine, k);
+        if (lane < k) sh.best[warp * k + lane] = list;
+        if (threadIdx.x == 0) sh.bar = 0;
+    }
     // every CTA of the cluster runs by now: its shared memory may be written
-    if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (CLUSTER) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
-    if (warp == 0) {
-        sums = sh.sums[lane & (kWarps - 1)];
-        if (lane >= kWarps) sums.clear();
-        sums.merge_warp();
-        if (TOP)
-#pragma unroll 1
-            for (int w = 1; w < kWarps; ++w) best.offer(lane < a.top ? sh.best[w][lane] : 0ull, a.top);
-        if (CLUSTER) {
-            uint32_t to_sums, to_best;
-            asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_sums) : "r"(smem_u32(&sh.part[rank])));
-            asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_best) : "r"(smem_u32(&sh.part_best[rank][lane])));
-            if (lane == 0) {
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums), "f"(sums.m) : "memory");
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums + 4), "f"(sums.s) : "memory");
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums + 8), "f"(sums.t) : "memory");
+    sums = sh.sums[lane & (kWarps - 1)];  // every warp for itself
+    if (lane >= kWarps) sums.clear();
+    sums.merge_warp();
+    const bool listed = TOP && (int)threadIdx.x < kWarps * k;
+    unsigned long long key = 0;
+    int place = kWarps * kTopMost;
+    if (TOP) {
+        if (listed) {
+            place = rank_of(sh.best, kWarps, k, key);
+            if (place == k - 1) sh.bar = (unsigned)(key >> 32);
+        }
+        __syncthreads();
+        const unsigned bar = sh.bar;
+        const bool again = __any_sync(kAll, next >= bar);
+        if (__syncthreads_or(again)) {
+            if (again) {
+                list = look_again(row + cut.head, cut.head, share, noted.at, noted.at2, __any_sync(kAll, noted.third >= bar), list, mine, bar, k);
+                if (lane < k) sh.best[warp * k + lane] = list;
             }
-            if (TOP) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_best), "l"(best.key) : "memory");
-        } else {
-            finish<T, TOP>(a, r, sums, best, token, given);
+            __syncthreads();
+            if (listed) place = rank_of(sh.best, kWarps, k, key);
         }
     }
-    if (CLUSTER) {
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (rank == 0 && warp == 0) {
-            if (lane < ctas)
-                sums = sh.part[lane];
-            else
-                sums.clear();
-            sums.merge_warp();
-            if (TOP)
-#pragma unroll 1
-                for (int c = 1; c < ctas; ++c) best.offer(lane < a.top ? sh.part_best[c][lane] : 0ull, a.top);
-            finish<T, TOP>(a, r, sums, best, token, given);
-        }
+    if (!CLUSTER) {
+        const SoftmaxRow out(sums);
+        if (threadIdx.x == 0) write_statistics(a, r, out, token, given);
+        if (place < k && key) write_best(a, r, out, place, key);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        uint32_t to_sums;
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_sums) : "r"(smem_u32(&sh.part[rank])));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums), "f"(sums.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums + 4), "f"(sums.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to_sums + 8), "f"(sums.t) : "memory");
+    }
+    if (place < k && key) {
+        uint32_t to_best;
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_best) : "r"(smem_u32(&sh.part_best[rank * k + place])));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_best), "l"(key) : "memory");
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank) return;
+    if (lane < ctas)
+        sums = sh.part[lane];
+    else
+        sums.clear();
+    sums.merge_warp();
+    const SoftmaxRow out(sums);
+    if (threadIdx.x == 0) write_statistics(a, r, out, token, given);
+    if (TOP && (int)threadIdx.x < ctas * k) {
+        const int i = rank_of(sh.part_best, ctas, k, key);
+        if (i < k && key) write_best(a, r, out, i, key);
     }
 }
 
@@ -467,12 +711,14 @@ constexpr int kWarpRowBytes = 4096;  // rows of up to so many bytes go to a warp
 
 template <typename T, bool TOP>
 cudaError_t forward(const TokenLogprobs& a, cudaStream_t stream) {
-    if ((long long)a.V * (long long)sizeof(T) <= kWarpRowBytes)
-        return launch(logprobs_warp_kernel<T, TOP>, (a.rows + kWarps - 1) / kWarps, 1, stream, a);
+    const long long bytes = (long long)a.V * (long long)sizeof(T);
+    if (bytes <= kWarpRowBytes)
+        return launch(bytes <= 512 ? logprobs_warp_kernel<T, TOP, 1> : bytes <= 1024 ? logprobs_warp_kernel<T, TOP, 2> : logprobs_warp_kernel<T, TOP, 4>,
+                      (a.rows + kWarps - 1) / kWarps, 1, stream, a);
     // as many CTAs per row as give every SM two, each with a vector per thread at least
     int ctas = 1;
     while (ctas < kMaxCluster && a.rows * ctas < 2ll * current_sm_count() &&
-           (long long)a.V * (long long)sizeof(T) >= 2ll * ctas * kThreads * 16)
+           bytes >= 2ll * ctas * kThreads * 16)
         ctas *= 2;
     if (ctas == 1) return launch(logprobs_cta_kernel<T, TOP, false>, a.rows, 1, stream, a);
     return launch(logprobs_cta_kernel<T, TOP, true>, a.rows * ctas, ctas, stream, a);
