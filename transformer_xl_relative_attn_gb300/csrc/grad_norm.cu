@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLoads = 8;                          // 16-byte vectors on their way per thread
 constexpr long long kStep = kThreads * 16;         // bytes that a CTA's threads load at once
-constexpr int kSmallTable = 32, kLargeTable = 480;  // tensors per launch
+constexpr int kSmallTable = 32, kMiddleTable = 160, kLargeTable = 480;  // tensors per launch
 constexpr int kNothing = -(1 << 20);               // exponent of a sum that is 0
 
 struct GradEntry {
@@ -245,15 +245,26 @@ __device__ __forceinline__ Total total_by_warp(const Sum* part, unsigned n) {
 }
 
 __device__ __forceinline__ Total total_by_cta(const Sum* part, unsigned n, float (&sh)[kWarps], int (&she)[kWarps]) {
+    constexpr int R = 6;  // kept in registers per thread: the second look at the others is at L2
+    Sum own[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const unsigned i = threadIdx.x + k * kThreads;
+        own[k] = i < n ? part[i] : Sum{0.f, kNothing};
+    }
     int most = kNothing;
-    for (unsigned i = threadIdx.x; i < n; i += kThreads) most = max(most, part[i].e);
+#pragma unroll
+    for (int k = 0; k < R; ++k) most = max(most, own[k].e);
+    for (unsigned i = threadIdx.x + R * kThreads; i < n; i += kThreads) most = max(most, part[i].e);
     most = __reduce_max_sync(0xffffffffu, most);
     if ((threadIdx.x & 31) == 0) she[threadIdx.x >> 5] = most;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) most = max(most, she[w]);
     float x = 0.f;
-    for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) x += ldexpf(own[k].x, max(own[k].e - most, -200));
+    for (unsigned i = threadIdx.x + R * kThreads; i < n; i += kThreads) {
         const Sum s = part[i];
         x += ldexpf(s.x, max(s.e - most, -200));
     }
@@ -411,7 +422,8 @@ long long grad_norm_pieces(const txl_grad_tensor* tensors, int n) {
 size_t grad_norm_workspace_bytes(long long pieces) { return ((size_t)pieces * sizeof(Sum) + 255) / 256 * 256; }
 
 cudaError_t launch_grad_norm(const GradNormArgs& a, cudaStream_t stream) {
-    return a.n_tensors <= kSmallTable ? run<kSmallTable>(a, stream) : run<kLargeTable>(a, stream);
+    if (a.n_tensors <= kSmallTable) return run<kSmallTable>(a, stream);
+    return a.n_tensors <= kMiddleTable ? run<kMiddleTable>(a, stream) : run<kLargeTable>(a, stream);
 }
 
 TXL_BOUNDS_READER(bounds_word_grad_norm)

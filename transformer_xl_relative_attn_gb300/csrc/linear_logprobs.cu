@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     const int src = __ffs(has) - 1, n = __shfl_sync(0xffffffffu, (int)token, src);
                     float g = lp_tmem_column(from + (n - n0));
                     if (BIAS) g += __bfloat162float(p.bias[n]);
-                    if (lane == src && TXL_BOUNDS(row < p.ld, 1301, row)) p.given[row] = g;
+                    if (lane == src && TXL_BOUNDS(row < p.rows, 1301, row)) p.given[row] = g;
                 }
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             }
             if (ok && row < p.rows) {
                 const int slot = 2 * it.run + chalf;
-                if (TXL_BOUNDS(row < p.ld && slot < 2 * p.chunks, 1302, slot))
+                if (TXL_BOUNDS(row < p.rows && slot < 2 * p.chunks, 1302, slot))
                     p.part[(long long)row * (2 * p.chunks) + slot] =
                         make_float4(sums.m, sums.s.x + sums.s.y, sums.t.x + sums.t.y, 0.f);
             }
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256) linear_logprobs_join_kernel(const LpParam
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            v[u] = i + 32 * u < n && TXL_BOUNDS(r < p.ld, 1303, r) ? q[i + 32 * u] : make_float4(-3.402823466e38f, 0.f, 0.f, 0.f);
+            v[u] = i + 32 * u < n && TXL_BOUNDS(r < p.rows && i + 32 * u < n, 1303, r) ? q[i + 32 * u] : make_float4(-3.402823466e38f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const SoftmaxSums b = {v[u].x, v[u].y, v[u].z};
@@ -441,14 +441,13 @@ LpPlan linear_logprobs_plan(int rows, int K, int V) {
                 p.n_vt = vt;
                 p.per = per;
                 p.chunks = chunks;
-                p.ld = (long long)rt * tile;
             }
         }
     }
     return pl;
 }
 
-size_t linear_logprobs_workspace_bytes(const LpPlan& pl) { return ((size_t)pl.p.chunks * 2 * sizeof(float4) + sizeof(float)) * pl.p.ld; }
+size_t linear_logprobs_workspace_bytes(const LpPlan& pl) { return ((size_t)pl.p.chunks * 2 * sizeof(float4) + sizeof(float)) * pl.p.rows; }
 
 namespace {
 
@@ -497,7 +496,7 @@ cudaError_t launch_linear_logprobs(LpPlan pl, const void* x, const void* w, cons
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.wide_bias = (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
     p.part = static_cast<float4*>(workspace);
-    p.given = reinterpret_cast<float*>(p.part + (size_t)p.chunks * 2 * p.ld);
+    p.given = reinterpret_cast<float*>(p.part + (size_t)p.chunks * 2 * p.rows);
     p.status = status;
     LpMaps maps;
     if (!lp_encode(&maps.x, x, p.rows, K, lp::BM) || !lp_encode(&maps.w, w, p.V, K, p.bn / (pl.pair ? 2 : 1))) return cudaErrorInvalidValue;

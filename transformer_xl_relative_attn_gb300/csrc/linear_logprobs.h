@@ -11,12 +11,11 @@ struct LpParams {
     int bn;                // columns of a tile, a multiple of 64 up to 256
     int n_rt, n_vt;        // tiles of rows and of columns
     int per, chunks;       // column tiles of an item; items per row tile
-    long long ld;          // rows of the partial sums, whole tiles
     const long long* tokens;
     const __nv_bfloat16* bias;  // [V] or null
     int wide_bias;         // bias is 16-byte aligned
-    float4* part;          // [ld][2 chunks]: (m, s, t) of each half of an item's columns
-    float* given;          // [ld]: the token's logit
+    float4* part;          // [rows][2 chunks]: (m, s, t) of each half of an item's columns
+    float* given;          // [rows]: the token's logit
     int* status;
 };
 
