@@ -19,7 +19,7 @@
 // time).  Behind it the threads' best elements are put in order, by sorting within warps
 // and by rank among the warps' lists, and the k-th of them is a bar: a second element of a
 // thread can only count where one reaches it.  Then its warp looks at its two vectors each
-// again, and at its whole part where some third vector reaches the bar too.
+// again, and at all vectors of a thread whose third one reaches the bar too.
 //
 // The gradient is a pass of its own, read once and written once, in place where the
 // caller wants it.
@@ -224,19 +224,19 @@ __device__ __forceinline__ int above(const unsigned long long* list, int k, unsi
 }
 
 // ------------------------------------------------------------ one warp's share of a row
-// What a thread notes for the alternatives: the orders of its vectors' three largest
-// values, and the vectors of the first two (of equal ones the first that came).
+// What a thread notes for the alternatives: its vectors' three largest values, and the
+// vectors of the first two (of equal ones the first that came).  A NaN is left out here: the
+// thread's sums show it, and all its vectors are then looked at again.
 struct Noted {
-    unsigned most, next, third;
+    float most, next, third;
     int at, at2;
-    __device__ __forceinline__ void clear() { most = next = third = 0, at = at2 = -1; }
+    __device__ __forceinline__ void clear(int first) { most = next = third = -INFINITY, at = first, at2 = -1; }
     __device__ __forceinline__ void see(float max, int vec) {
-        const unsigned o = order_of(max);
-        third = ::max(third, ::min(o, next));
-        at2 = o > most ? at : o > next ? vec : at2;
-        next = ::max(next, ::min(o, most));
-        at = o > most ? vec : at;
-        most = ::max(o, most);
+        third = fmaxf(third, fminf(max, next));
+        at2 = max > most ? at : max > next ? vec : at2;
+        next = fmaxf(next, fminf(max, most));
+        at = max > most ? vec : at;
+        most = fmaxf(max, most);
     }
 };
 
@@ -255,6 +255,7 @@ __device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, con
     const T* const vec0 = row + cut.head;
     SoftmaxPairs acc;
     acc.clear();
+    if (TOP) noted.clear(sh.first + lane);
     auto load = [&](Vec<T>(&v)[U], int base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -321,31 +322,42 @@ __device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, con
     }
 }
 
-// The key of a thread's best element in its vectors (0: it has none); `next` becomes the
-// largest order that another of them may have.
+// A thread's best vector once more.
 template <typename T>
-__device__ __forceinline__ unsigned long long best_of(const T* row, int V, const RowCut& cut, const Share& sh, const Noted& noted,
-                                                      unsigned& next) {
+__device__ __forceinline__ Vec<T> best_vector(const T* row, int V, const RowCut& cut, const Share& sh, const Noted& noted) {
+    Vec<T> v;
+    v.q = sh.first + (int)(threadIdx.x & 31) < sh.end &&
+                  TXL_BOUNDS(noted.at >= 0 && cut.head + (long long)(noted.at + 1) * Vec<T>::N <= V, 1106, noted.at)
+              ? load_stream(row + cut.head + (size_t)noted.at * Vec<T>::N)
+              : Vec<T>::nothing();
+    return v;
+}
+
+// The key of a thread's best element in its vectors (0: it has none), of whose best vector v is
+// the content; `next` becomes the largest order that another of them may have, and `third` that
+// of one outside the two noted vectors.  (With a NaN, `nan`, both are the highest, and the key
+// is one of the thread's elements all the same.)
+template <typename T>
+__device__ __forceinline__ unsigned long long best_of(const Vec<T>& v, const RowCut& cut, const Share& sh, const Noted& noted, bool nan,
+                                                      unsigned& next, unsigned& third) {
     constexpr int N = Vec<T>::N;
-    const int lane = threadIdx.x & 31;
-    unsigned long long key = 0;
-    next = noted.next;
-    if (sh.first + lane < sh.end && TXL_BOUNDS(noted.at >= 0 && cut.head + (long long)(noted.at + 1) * N <= V, 1106, noted.at)) {
-        Vec<T> v;
-        v.q = load_stream(row + cut.head + (size_t)noted.at * N);
-        unsigned most = 0;
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float2 p = v.pair(j / 2);
-            const unsigned o = order_of(j & 1 ? p.y : p.x);
-            next = ::max(next, ::min(o, most));
-            at = o > most ? j : at;
-            most = ::max(o, most);
-        }
-        key = (unsigned long long)most << 32 | (unsigned)~(cut.head + noted.at * N + at);
+    if (sh.first + (int)(threadIdx.x & 31) >= sh.end) {
+        next = third = 0;
+        return 0;
     }
-    return key;
+    float most = -INFINITY, second = noted.next;
+    int at = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float2 p = v.pair(j / 2);
+        const float x = j & 1 ? p.y : p.x;
+        second = fmaxf(second, fminf(x, most));
+        at = x > most ? j : at;
+        most = fmaxf(x, most);
+    }
+    next = nan ? 0xFFFFFFFFu : order_of(second);
+    third = nan ? 0xFFFFFFFFu : order_of(noted.third);
+    return key_of(v.at(at), cut.head + noted.at * N + at);
 }
 
 // The best keys of a warp as they stand behind best_of: its lanes' best, `mine`, and the
@@ -362,11 +374,12 @@ __device__ __forceinline__ unsigned long long first_list(const T* row, int V, co
     return list;
 }
 
-// A warp's two best vectors per lane once more, or all of its part, for what else is among
-// its best `k` and not below the order `bar`: its list (a key per lane, falling) with the
-// threads' best, `mine`, in it already.
+// A warp's noted vectors once more, two per lane, for what else is among its best `k` and not
+// below the order `bar`; and all vectors of the lanes that `whole` names, each of which the
+// warp shares out.  `list`: its best so far (a key per lane, falling), the threads' best,
+// `mine`, among them.
 template <typename T>
-__device__ __noinline__ unsigned long long look_again(const T* vec0, int head, const Share sh, int at, int at2, bool all,
+__device__ __noinline__ unsigned long long look_again(const T* vec0, int head, const Share sh, int at, int at2, unsigned whole,
                                                       unsigned long long list, unsigned long long mine, unsigned bar, int k) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31;
@@ -379,33 +392,44 @@ __device__ __noinline__ unsigned long long look_again(const T* vec0, int head, c
         v.q = i >= 0 && i < sh.end && TXL_BOUNDS(i < sh.vecs, 1108, i) ? load_stream(vec0 + (size_t)i * N) : Vec<T>::nothing();
         return v;
     };
-    if (all) at = sh.first + lane, at2 = at + sh.step;
-    Vec<T> v = load(at), w = load(at2);
+    if (sh.first + lane >= sh.end) at = -1;
+    if (at2 == at || at2 >= sh.end) at2 = -1;
+    // a vector per lane at a time: first the noted ones, then the shared-out ones
+    int i = at, from = -1, skip = -1, skip2 = -1, round = 0;
+    Vec<T> x = load(at);
+    const Vec<T> second = load(at2);
 #pragma unroll 1
-    for (int left = all ? (sh.end - sh.first + sh.step - 1) / sh.step : 2; left > 0; --left) {
-        const Vec<T> x = v;
-        const int i = at;
-        v = w;
-        at = at2;
-        if (all) {
-            at2 += sh.step;
-            w = load(at2);
-        }
+    for (;;) {
         unsigned bits = 0;  // elements that may count
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float2 p = x.pair(j / 2);
             bits |= best.worth(j & 1 ? p.y : p.x) ? 1u << j : 0u;
         }
-        if (i < 0 || i >= sh.end) bits = 0;
+        if (i < 0) bits = 0;
         while (__any_sync(kAll, bits != 0)) {
             const int j = bits ? __ffs(bits) - 1 : 0;
             const unsigned long long c = bits ? key_of(x.at(j), head + i * N + j) : 0ull;
             best.offer(c == mine ? 0ull : c, k, floor);
             bits &= bits - 1;
         }
+        if (++round == 1) {
+            x = second, i = at2;
+            continue;
+        }
+        if (from < 0 || from + 32 * sh.step >= sh.end) {  // the next lane's
+            if (!whole) return best.key;
+            const int src = __ffs(whole) - 1;
+            whole &= whole - 1;
+            from = sh.first + src;
+            skip = __shfl_sync(kAll, at, src), skip2 = __shfl_sync(kAll, at2, src);
+        } else {
+            from += 32 * sh.step;
+        }
+        i = from + lane * sh.step;
+        if (i >= sh.end || i == skip || i == skip2) i = -1;
+        x = load(i);
     }
-    return best.key;
 }
 
 __device__ __forceinline__ void write_statistics(const TokenLogprobs& a, long long r, const SoftmaxRow& row, long long token, float given) {
@@ -438,18 +462,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_warp_kernel(const TokenLogp
     const Share sh = {0, cut.vecs, 32, true, cut.vecs};
     SoftmaxSums sums;
     Noted noted;
-    noted.clear();
     scan<T, TOP, U>(row, a.V, cut, sh, sums, noted);
+    Vec<T> v;
+    if (TOP) v = best_vector(row, a.V, cut, sh, noted);
+    const bool nan = sums.s != sums.s;
     sums.merge_warp();
     const SoftmaxRow out(sums);
     if (lane == 0) write_statistics(a, r, out, token, given);
     if (TOP) {
-        unsigned next;
-        const unsigned long long mine = best_of(row, a.V, cut, sh, noted, next);
+        unsigned next, third;
+        const unsigned long long mine = best_of(v, cut, sh, noted, nan, next, third);
         unsigned long long key = first_list(row, a.V, cut, sh, mine, a.top);
         const unsigned bar = (unsigned)(__shfl_sync(kAll, key, a.top - 1) >> 32);
         if (__any_sync(kAll, next >= bar))
-            key = look_again(row + cut.head, cut.head, sh, noted.at, noted.at2, __any_sync(kAll, noted.third >= bar), key, mine, bar, a.top);
+            key = look_again(row + cut.head, cut.head, sh, noted.at, noted.at2, __ballot_sync(kAll, third >= bar), key, mine, bar, a.top);
         if (lane < a.top) write_best(a, r, out, lane, key);
     }
 }
@@ -466,15 +492,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 
 // Lists of keys, one behind the other without a gap.
+template <int THREADS>
 struct RowShared {
     unsigned bar;  // order of the k-th best of the threads' best
-    SoftmaxSums sums[kWarps];
-    unsigned long long best[kWarps * kTopMost];
+    SoftmaxSums sums[THREADS / 32];
+    unsigned long long best[THREADS];
     // of the cluster's CTAs, in its first one
     SoftmaxSums part[kMaxCluster];
     unsigned long long part_best[kMaxCluster * kTopMost];
 };
-static_assert(kMaxCluster <= kWarps, "a CTA's threads hold a key of each of the cluster's lists");
+static_assert(kMaxCluster * kTopMost <= kThreads, "a CTA's threads hold a key of each of the cluster's lists");
 
 // Of n lists of k keys, this thread's (below n k) and how many of all are above it.
 __device__ __forceinline__ int rank_of(const unsigned long long* lists, int n, int k, unsigned long long& key) {
@@ -486,9 +513,12 @@ __device__ __forceinline__ int rank_of(const unsigned long long* lists, int n, i
 }
 
 // One row per CTA, or per cluster of CTAs.
-template <typename T, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (TOP ? 5 : 6) : (TOP ? 4 : 3)) logprobs_cta_kernel(const TokenLogprobs a) {
-    __shared__ RowShared sh;
+template <typename T, bool TOP, bool CLUSTER, int THREADS>
+__global__ void __launch_bounds__(THREADS, (sizeof(T) == 2 ? (TOP ? 5 : 6) : (TOP ? 4 : 3)) * (kThreads / THREADS))
+logprobs_cta_kernel(const TokenLogprobs a) {
+    constexpr int WARPS = THREADS / 32;
+    static_assert(!CLUSTER || THREADS == kThreads, "clusters are of the larger CTAs");
+    __shared__ RowShared<THREADS> sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (CLUSTER) {
         if (TOP) sh.part_best[threadIdx.x] = 0;  // (lists of less than k keys: 0 in place of the rest)
@@ -503,17 +533,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (TOP ? 5 : 6) : (TO
     const float given = given_logit(row, token, a.V);
     const RowCut cut(row, a.V);
     const int from = (int)((long long)cut.vecs * rank / ctas), to = (int)((long long)cut.vecs * (rank + 1) / ctas);
-    const Share share = {from + 32 * warp, to, kThreads, rank == 0 && warp == 0, cut.vecs};
+    const Share share = {from + 32 * warp, to, THREADS, rank == 0 && warp == 0, cut.vecs};
     SoftmaxSums sums;
     Noted noted;
-    noted.clear();
     scan<T, TOP, 4>(row, a.V, cut, share, sums, noted);
+    Vec<T> v;
+    if (TOP) v = best_vector(row, a.V, cut, share, noted);
+    const bool nan = sums.s != sums.s;
     sums.merge_warp();
     if (lane == 0) sh.sums[warp] = sums;
-    unsigned next = 0;
+    unsigned next = 0, third = 0;
     unsigned long long mine = 0, list = 0;
     if (TOP) {
-        mine = best_of(row, a.V, cut, share, noted, next);
+        mine = best_of(v, cut, share, noted, nan, next, third);
         list = first_list(row, a.V, cut, share, mine, k);
         if (lane < k) sh.best[warp * k + lane] = list;
         if (threadIdx.x == 0) sh.bar = 0;
@@ -521,15 +553,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (TOP ? 5 : 6) : (TO
     // every CTA of the cluster runs by now: its shared memory may be written
     if (CLUSTER) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
-    sums = sh.sums[lane & (kWarps - 1)];  // every warp for itself
-    if (lane >= kWarps) sums.clear();
+    sums = sh.sums[lane & (WARPS - 1)];  // every warp for itself
+    if (lane >= WARPS) sums.clear();
     sums.merge_warp();
-    const bool listed = TOP && (int)threadIdx.x < kWarps * k;
+    const bool listed = TOP && (int)threadIdx.x < WARPS * k;
     unsigned long long key = 0;
-    int place = kWarps * kTopMost;
+    int place = THREADS;
     if (TOP) {
         if (listed) {
-            place = rank_of(sh.best, kWarps, k, key);
+            place = rank_of(sh.best, WARPS, k, key);
             if (place == k - 1) sh.bar = (unsigned)(key >> 32);
         }
         __syncthreads();
@@ -537,11 +569,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (TOP ? 5 : 6) : (TO
         const bool again = __any_sync(kAll, next >= bar);
         if (__syncthreads_or(again)) {
             if (again) {
-                list = look_again(row + cut.head, cut.head, share, noted.at, noted.at2, __any_sync(kAll, noted.third >= bar), list, mine, bar, k);
+                list = look_again(row + cut.head, cut.head, share, noted.at, noted.at2, __ballot_sync(kAll, third >= bar), list, mine, bar, k);
                 if (lane < k) sh.best[warp * k + lane] = list;
             }
             __syncthreads();
-            if (listed) place = rank_of(sh.best, kWarps, k, key);
+            if (listed) place = rank_of(sh.best, WARPS, k, key);
         }
     }
     if (!CLUSTER) {
@@ -689,11 +721,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const TokenLogpr
 }
 
 // ------------------------------------------------------------ host side
-template <typename... KArgs, typename... Args>
+template <int THREADS = kThreads, typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), long long grid, unsigned cluster, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -707,12 +739,15 @@ cudaError_t launch(void (*kern)(KArgs...), long long grid, unsigned cluster, cud
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-constexpr int kWarpRowBytes = 4096;  // rows of up to so many bytes go to a warp each
+// Rows of up to so many bytes go to a warp each: where rows are many (us, top 8, a warp and a CTA
+// of 128 threads: 10000 x 1024 fp32 17 and 34, 10000 x 4096 bf16 24 and 38), and where they are
+// few and a warp's steps one after the other count (300 x 2048 bf16, top 32: 17 and 6).
+constexpr int kWarpRowBytes = 8192, kWarpFewRowBytes = 1024, kManyRows = 8;  // rows per SM
 
 template <typename T, bool TOP>
 cudaError_t forward(const TokenLogprobs& a, cudaStream_t stream) {
     const long long bytes = (long long)a.V * (long long)sizeof(T);
-    if (bytes <= kWarpRowBytes)
+    if (bytes <= (a.rows >= (long long)kManyRows * current_sm_count() ? kWarpRowBytes : kWarpFewRowBytes))
         return launch(bytes <= 512 ? logprobs_warp_kernel<T, TOP, 1> : bytes <= 1024 ? logprobs_warp_kernel<T, TOP, 2> : logprobs_warp_kernel<T, TOP, 4>,
                       (a.rows + kWarps - 1) / kWarps, 1, stream, a);
     // as many CTAs per row as give every SM two, each with a vector per thread at least
@@ -720,8 +755,15 @@ cudaError_t forward(const TokenLogprobs& a, cudaStream_t stream) {
     while (ctas < kMaxCluster && a.rows * ctas < 2ll * current_sm_count() &&
            bytes >= 2ll * ctas * kThreads * 16)
         ctas *= 2;
-    if (ctas == 1) return launch(logprobs_cta_kernel<T, TOP, false>, a.rows, 1, stream, a);
-    return launch(logprobs_cta_kernel<T, TOP, true>, a.rows * ctas, ctas, stream, a);
+    // CTAs of half the threads, and so twice as many rows at once, with alternatives, whose
+    // search behind the pass leaves other rows' loads to fill the time (us, top 8, 256 and 128
+    // threads: 11264 x 32768 bf16 186 and 133, 1001 x 50021 fp32 45 and 38); without, where
+    // rows are many (11264 x 32768 bf16 108 and 106, but 1001 x 50021 fp32 37 and 40, 2432 x
+    // 50048 bf16 41 and 44).
+    const bool half = TOP || a.rows >= 4096;
+    if (ctas == 1 && half) return launch<kThreads / 2>(logprobs_cta_kernel<T, TOP, false, kThreads / 2>, a.rows, 1, stream, a);
+    if (ctas == 1) return launch(logprobs_cta_kernel<T, TOP, false, kThreads>, a.rows, 1, stream, a);
+    return launch(logprobs_cta_kernel<T, TOP, true, kThreads>, a.rows * ctas, ctas, stream, a);
 }
 
 template <typename T, bool ENT>
