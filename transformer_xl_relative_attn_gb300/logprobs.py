@@ -12,6 +12,7 @@ from ._lib import TXL_BF16, TXL_F32, TxlError, _invoke, _need, _stream
 from .train import _INT_MAX, _on, _ptr, _scratch, _workspace_need
 
 _F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
+_CODES = {_BF16: TXL_BF16, _F32: TXL_F32}
 
 
 def _rows(t, name: str):
@@ -40,11 +41,12 @@ def _rows(t, name: str):
 
 
 def _type_of(t, name: str) -> int:
-    if t.dtype is _BF16:
-        return TXL_BF16
-    if t.dtype is _F32:
-        return TXL_F32
-    raise TypeError(f"unsupported dtype {t.dtype} of {name}: bf16 or fp32 only")
+    """The type of logits, which must be on a GPU."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}: bf16 or fp32 only")
+    _on_gpu(t, name)
+    return code
 
 
 def _on_gpu(t, name: str, device=None) -> None:
@@ -76,7 +78,6 @@ def token_logprobs(logits, tokens, top=0, stream=None, outs=None):
     +inf: NaN."""
     rows, V, ld = _rows(logits, "logits")
     code, dev, shape = _type_of(logits, "logits"), logits.device, logits.shape[:-1]
-    _on_gpu(logits, "logits")
     _need(tokens, "tokens", shape, _I64, dev)
     if not isinstance(top, int) or top < 0:
         raise ValueError("top must be a count")
@@ -114,7 +115,6 @@ def token_logprobs_bwd(logits, tokens, lse, dlogprob=None, dlse=None, dentropy=N
     logits hold."""
     rows, V, ld = _rows(logits, "logits")
     code, dev, shape = _type_of(logits, "logits"), logits.device, logits.shape[:-1]
-    _on_gpu(logits, "logits")
     _need(tokens, "tokens", shape, _I64, dev)
     _need(lse, "lse", shape, _F32, dev)
     if dlogprob is None and dlse is None and dentropy is None:
