@@ -74,6 +74,22 @@ def test_matches_fp64(rows, K, V, bias):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+@pytest.mark.parametrize("rows,V", [(5, 3000), (300, 9000), (40, 70000)])
+def test_rising_and_falling_logits(rows, V):
+    """The sums' reference has to follow the maximum, by steps above and below those it lets pass
+    (whole numbers that bf16 holds: the logits are exact)."""
+    i = torch.arange(V, device="cuda", dtype=torch.float64)
+    for step, every in ((1.0, 32), (4.0, 64), (16.0, 64), (32.0, 100), (64.0, 500), (512.0, 3000)):
+        w = torch.zeros(V, 16, device="cuda", dtype=BF)
+        w[:, 0] = (torch.floor(i / every) * step).to(BF)
+        w[:, 1] = w[:, 0].flip(0)
+        w[:, 2] = -2048.0
+        x = torch.zeros(rows, 16, device="cuda", dtype=BF)
+        x[::2, 0], x[1::2, 1], x[::3, 2] = 1.0, 1.0, 1.0
+        t = torch.arange(rows, device="cuda") * 7919 % V
+        check(x, w, t, None, txl.linear_logprobs(x, w, t))
+
+
 def test_agrees_with_the_logits_in_memory():
     """One and the same logits: whole numbers, exact in bf16 and in every accumulator."""
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -124,6 +124,22 @@ def test_peaked_and_flat_rows():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,V", [(4, 300), (1300, 300), (4, 9000), (500, 9000), (2, 100000)])
+def test_rising_and_falling_logits(dtype, rows, V):
+    """The sums' reference has to follow the maximum, by steps above and below those it lets pass."""
+    i = torch.arange(V, device="cuda", dtype=torch.float64)
+    for step, every in ((1.0, 1), (3.0, 64), (4.0, 64), (8.0, 64), (8.0, 1000), (64.0, 3000)):
+        x = (torch.floor(i / every) * step).to(dtype).repeat(rows, 1)
+        x[1::2] = x[1::2].flip(1)
+        x[2:3] -= 300
+        t = torch.arange(rows, device="cuda") * 7919 % V
+        t[0] = V - 1
+        k = min(V, 5)
+        got = txl.token_logprobs(x, t, top=k)
+        check_top(x, check(x, t, got), got, k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V", [6, 40, 3000, 40000])
 def test_ties_go_to_the_lower_index(dtype, V):
     g = torch.Generator(device="cuda").manual_seed(V)

@@ -239,20 +239,22 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             SoftmaxPairs sums;
             sums.clear();
             auto add = [&](const float (&z)[32]) {
+                const SoftmaxPairs was = sums;
+                if (sm_ordinary(sums.m)) {
+                    const float r = sm_reference(sums.m);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) sums.add(make_float2(z[x], z[x + 1]), r);
+                    if (sums.fine()) return;
+                    sums = was;
+                }
                 float most = fmaxf(z[0], z[1]);
 #pragma unroll
                 for (int x = 2; x < 32; x += 2) most = sm_max3(most, z[x], z[x + 1]);
                 sums.raise(most);
                 if (sm_ordinary(sums.m)) {
                     const float r = sm_reference(sums.m);
-                    const float2 was = sums.t;
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2) sums.add(make_float2(z[x], z[x + 1]), r);
-                    if (sums.lost()) {
-                        sums.t = was;
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2) sums.add_low(make_float2(z[x], z[x + 1]), r);
-                    }
+                    for (int x = 0; x < 32; x += 2) sums.add_low(make_float2(z[x], z[x + 1]), r);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) sums.add_far(z[x]);

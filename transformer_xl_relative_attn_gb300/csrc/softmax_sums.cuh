@@ -3,7 +3,7 @@
 //
 //   m near max x,   r = m L (rounded),   s = sum 2^(x L - r),   t = sum 2^(x L - r) (x L - r)
 //
-// all in fp32, from which log-sum-exp = (r + log2 s) / L and entropy = (log2 s - t / s) ln 2.
+// all in fp32, from which log-sum-exp = m + (log2 s - (m L - r)) / L and entropy = (log2 s - t / s) ln 2.
 // The reference is r itself, so that its rounding is no error, and a term costs one fused
 // product before its power of two; that L is off by 1.3e-8 of itself is a temperature off
 // by as much.  When the reference moves from m to M, with d = r(m) - r(M) <= 0, the sums
@@ -12,11 +12,11 @@
 //
 // What is not ordinary: a value of -inf, or one so low that x L - r is, would make t NaN (0
 // times -inf).  Either nothing below kLow is added, whose power is 0 and whose product with
-// it too, or t is taken once more so for a batch that made it NaN (in linear_logprobs, where
-// an instruction for each logit cost a tenth of the time).  A reference beyond +-kHuge is the
-// maximum: numbers lie 1e28 and more apart there, and s counts those equal to it.  m starts at
-// the lowest finite number, which is beyond -kHuge and equals no -inf.  A NaN or +inf among
-// the values makes s and t NaN.
+// it too; or a batch is added with no look at its values, and once more with it where that
+// was not fine (in linear_logprobs, where two instructions for each logit cost a tenth of the
+// time).  A reference beyond +-kHuge is the maximum: numbers lie 1e28 and more apart there,
+// and s counts those equal to it.  m starts at the lowest finite number, which is beyond
+// -kHuge and equals no -inf.  A NaN or +inf among the values makes s and t NaN.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -25,6 +25,7 @@ namespace txl {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1e38f, kHuge = 1e36f;
 constexpr float kSlack = 4.f;
+constexpr float kMuch = 0x1p30f;  // a sum beyond it has too low a reference: its logarithm's rounding grows with it
 constexpr float kLowest = -1e20f;  // differences of references are held at or above it (times 2^30 terms it is finite)
 
 __device__ __forceinline__ float sm_ex2(float x) {
@@ -139,19 +140,20 @@ struct SoftmaxPairs {
             m = to;
         }
     }
-    // Two values up to m + kSlack, or NaN; m ordinary, r = sm_reference(m).
+    // Two values, m ordinary, r = sm_reference(m).
     __device__ __forceinline__ void add(float2 x, float r) {
         const float2 y = sm_fma2(x, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
         const float2 e = make_float2(sm_ex2(y.x), sm_ex2(y.y));
         s = sm_add2(s, e);
         t = sm_fma2(e, y, t);
     }
-    // Whether t has to be taken again, from what it was, by add_low over the same values.
-    __device__ __forceinline__ bool lost() const { return t.x != t.x || t.y != t.y; }
-    __device__ __forceinline__ void add_low(float2 x, float r) {
-        x = make_float2(sm_max_nan(x.x, kLow), sm_max_nan(x.y, kLow));
-        const float2 y = sm_fma2(x, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
-        t = sm_fma2(make_float2(sm_ex2(y.x), sm_ex2(y.y)), y, t);
+    // The same where values may be below kLow.
+    __device__ __forceinline__ void add_low(float2 x, float r) { add(make_float2(sm_max_nan(x.x, kLow), sm_max_nan(x.y, kLow)), r); }
+    // Whether values that nothing was known of were added as they should: the sum is neither
+    // large, for which the reference has to follow, nor NaN, and t is none either.
+    __device__ __forceinline__ bool fine() const {
+        const float a = s.x + s.y, b = t.x + t.y;
+        return a < kMuch && b == b;
     }
     // One value not above m (or NaN), where m is not ordinary.
     __device__ __forceinline__ void add_far(float x) { s.x += x == m ? (x - x) + 1.f : x != x ? x : 0.f; }
@@ -160,19 +162,23 @@ struct SoftmaxPairs {
 
 // What a row's sums say: log-sum-exp, entropy, and log p of a value of the row.  A row
 // of nothing but -inf has no probabilities: log-sum-exp and log p are -inf, its entropy 0.
+// (log p is x - m, exact or nearly, less ln sum e^(x - m): over x L - r it would carry the
+// roundings of a product of its own size.)
 struct SoftmaxRow {
-    float m, log_s, lse, entropy;  // log_s: log2 s
+    float m, ln_s, lse, entropy;  // ln_s: of the sum against m itself
     __device__ __forceinline__ explicit SoftmaxRow(const SoftmaxSums& a) {
         m = a.m;
-        log_s = log2f(a.s);  // -inf where s is 0
-        lse = sm_ordinary(m) ? (sm_reference(m) + log_s) * (1.f / kLog2e) : m + log_s * kLn2;
+        const float log_s = log2f(a.s);  // -inf where s is 0
+        // the sum is against r, which is m L but for this much
+        const float off = sm_ordinary(m) ? fmaf(m, kLog2e, -sm_reference(m)) : 0.f;
+        ln_s = (log_s - off) * (1.f / kLog2e);
+        lse = m + ln_s;
         const float h = (log_s - a.t / a.s) * kLn2;
         entropy = a.s == 0.f || h < 0.f ? 0.f : h;
     }
     __device__ __forceinline__ float logprob(float x) const {
-        if (log_s == -INFINITY) return -INFINITY;
-        // (x L may leave the range below kLow, where ln s is nothing beside x)
-        return sm_ordinary(m) && !(x < kLow) ? (fmaf(x, kLog2e, -sm_reference(m)) - log_s) * kLn2 : (x - m) - log_s * kLn2;
+        const float l = (x - m) - ln_s;
+        return ln_s == -INFINITY ? -INFINITY : l > 0.f ? 0.f : l;  // (a rounding above it where p is 1)
     }
 };
 
