@@ -411,13 +411,13 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
  * each may be null: zeros, but not all three),
  *   dx_j = dlogprob (delta_j,token - p_j) + dlse p_j - dentropy p_j ((x_j - lse) + entropy),
  * dlogprob taken as 0 where there is no token.  lse and entropy (null without dentropy)
- * as the forward call gave them.  dlogits (rows ldd elements apart) may be logits with
+ * as the forward call gave them (p carries lse's rounding, 2^-24 of it).  dlogits (rows ldd elements apart) may be logits with
  * the same distance of rows: the gradient then takes their place.  A row whose gradients
  * are all 0 gets zeros whatever its logits hold, as does a row of nothing but -inf;
  * dlogprob other than 0 at a token >= V makes the row NaN.  What lies between the rows
  * is left as it was.
  *
- * 0 <= rows < 2^31, 1 <= V <= 2^30, rows * max(ld, ldd) <= 2^40 (TXL_ERR_UNSUPPORTED
+ * 0 <= rows < 2^31, 1 <= V <= 2^24, rows * max(ld, ldd) <= 2^40 (TXL_ERR_UNSUPPORTED
  * beyond, as for top > 32; top > V is TXL_ERR_INVALID_ARG).  Pointers need the alignment
  * of their elements (TXL_ERR_MISALIGNED).  What is written overlaps nothing else
  * (TXL_ERR_ALIAS), but for dlogits as said.
@@ -432,12 +432,13 @@ int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* to
 /*
  * txl_linear_logprobs: txl_token_logprobs of the logits z = x W^T + bias without the
  * logits: x [rows, K], w [V, K] and bias [V] (may be null) bf16, products on the tensor
- * cores with fp32 accumulation, z never rounded to fewer bits; the row statistics lse,
+ * cores with fp32 accumulation (which cuts off some 2^-26 of the sum per 16 elements of K), z
+ * never rounded to fewer bits; the row statistics lse,
  * logprob and entropy (fp32 [rows]) and their special cases are those of
  * txl_token_logprobs (a bias of -inf masks a column).  For scoring; the gradient goes over
  * txl_linear's logits and txl_token_logprobs_bwd.  The same inputs give the same bits.
  *
- * 0 <= rows <= 2^28, K a multiple of 8 up to 2^20, 1 <= V <= 2^30, rows * V <= 2^40
+ * 0 <= rows <= 2^28, K a multiple of 8 up to 2^20, 1 <= V <= 2^24, rows * V <= 2^40
  * (TXL_ERR_UNSUPPORTED beyond).  x and w 16-byte aligned, the others to their elements
  * (TXL_ERR_MISALIGNED); outputs overlap neither inputs nor each other (TXL_ERR_ALIAS).
  * workspace as for txl_layer_norm_bwd, of txl_linear_logprobs_workspace_bytes(...) bytes.

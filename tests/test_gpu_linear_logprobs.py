@@ -90,6 +90,26 @@ def test_rising_and_falling_logits(rows, V):
         check(x, w, t, None, txl.linear_logprobs(x, w, t))
 
 
+@pytest.mark.parametrize("base", [2.0 ** 10, 2.0 ** 16, 2.0 ** 21, -2.0 ** 21, 2.0 ** 27, 2.0 ** 33, -2.0 ** 90])
+def test_logits_far_from_zero(base):
+    """One column of x and w makes the offset; the rest are whole numbers, which fp32 still holds
+    beside it up to 2^21 (beyond, what is left of them)."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for rows, V in ((5, 300), (300, 5000)):
+        w = torch.randint(-1, 2, (V, 32), device="cuda", generator=g).to(BF)
+        x = torch.randint(-1, 2, (rows, 32), device="cuda", generator=g).to(BF)
+        w[:, 0], x[:, 0] = 1.0, base
+        t = torch.arange(rows, device="cuda") % V
+        got = txl.linear_logprobs(x, w, t)
+        if abs(base) <= 2.0 ** 21:
+            check(x, w, t, None, got)
+            want = txl.linear_logprobs(torch.cat((torch.zeros_like(x[:, :1]), x[:, 1:]), 1), w, t)
+            assert bool(((got["logprob"] - want["logprob"]).abs() <= 1e-5 * (1 + want["logprob"].abs())).all())
+        else:
+            assert bool(((got["lse"] / base - 1).abs() <= 1e-5).all()) and bool((got["logprob"] <= 0).all())
+            assert bool((got["entropy"] >= 0).all()) and bool((got["entropy"] <= math.log(V) + 1e-4).all())
+
+
 def test_agrees_with_the_logits_in_memory():
     """One and the same logits: whole numbers, exact in bf16 and in every accumulator."""
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -51,10 +51,12 @@ def formula(x, t):
 
 def check(x, t, got):
     f, K = formula(x, t), terms(x.shape[-1], x.dtype)
-    sums = U * (3 * f["A"] + K + 4) + 2 * U * f["ls"]
+    # (the reference m log2 e is off by 1.45 U |m| <= 47, which each sum carries through 8 roundings)
+    off = 8 * U * (1.45 * U * f["m"].abs()).clamp(max=47.0)
+    sums = U * (3 * f["A"] + K + 4) + 2 * U * f["ls"] + off
     tol = {"lse": sums + U * (f["m"].abs() + f["lse"].abs()),
            "logprob": torch.where(t < 0, 0.0, sums + U * torch.where(f["xt"] > -INF, f["xt"].abs(), 0.0) + U * f["ls"]),
-           "entropy": sums + U * (3 * f["B"] + (K + 4) * f["A"]) + f["A"] * U * (3 * f["A"] + K + 4) + U * f["entropy"]}
+           "entropy": sums + off + U * (3 * f["B"] + (K + 4) * f["A"]) + f["A"] * U * (3 * f["A"] + K + 4) + U * f["entropy"]}
     for n in tol:
         assert got[n].dtype is F32 and got[n].shape == t.shape, n
         ref = f[n]
@@ -202,6 +204,35 @@ def test_rows_that_are_not_finite_stay_alone(dtype, V):
             else:
                 assert torch.equal(got[k][r], ref[k][r]), (k, r)
     assert [int(got["top_index"][r, 0]) for r in (2, 4, 6)] == [7, V - 1, 0]
+
+
+@pytest.mark.parametrize("base", [1e5, 1e6, 1.6e7, 1e8, 3e8, 2.0 ** 29 - 32, 2.0 ** 29, 1e9, 1e10, 1e12, 1e30])
+@pytest.mark.parametrize("V", [40, 5000])
+def test_logits_far_from_zero(base, V):
+    """Differences that fp32 still holds there, or none."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for sign in (1, -1):
+        x = torch.randint(0, 6, (20, V), device="cuda", generator=g).double()
+        x = (sign * (base + x * max(1.0, base * 2.0 ** -23))).float()
+        x[3, 1:] = -INF
+        t = torch.arange(20, device="cuda")
+        got = txl.token_logprobs(x, t, top=3)
+        check(x, t, got)
+        assert torch.equal(got["top_index"], best(x, 3))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,V", [(6, 40), (1300, 200), (6, 3001), (6, 40000), (700, 5000)])
+def test_order_with_many_values_that_are_not_finite(dtype, rows, V):
+    x, t = make(rows, V, dtype, seed=11)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    kind = torch.randint(0, 40, (rows, V), device="cuda", generator=g)
+    x = torch.where(kind == 0, NAN, torch.where(kind == 1, INF, torch.where(kind < 5, -INF, x.float()))).to(dtype)
+    x[1] = NAN
+    x[2, ::2] = INF
+    x[3] = -INF
+    for k in (1, 4, 9, 32):
+        assert torch.equal(txl.token_logprobs(x, t, top=k)["top_index"], best(x, k))
 
 
 def test_extreme_magnitudes():

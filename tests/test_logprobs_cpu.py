@@ -32,7 +32,7 @@ def test_token_logprobs_rejects_bad_arguments(lib):
     assert call(top=0) == -1                                             # alternatives that are not asked for
     assert call(rows=-1) == -1 and call(V=0) == -1 and call(dtype=2) == -1 and call(top=-1) == -1
     assert call(ld=499) == -1 and call(V=3, top=4) == -1
-    assert call(top=33) == -2 and call(V=(1 << 30) + 1, ld=1 << 31) == -2
+    assert call(top=33) == -2 and call(V=(1 << 24) + 1, ld=1 << 31) == -2
     assert call(rows=1 << 31, ld=512) == -2 and call(rows=1 << 20, ld=(1 << 20) + 1) == -2
     assert call(lp=addr(3)) == -4 and call(lse=addr(1) + 8) == -4 and call(ent=addr(0) + 64) == -4
     assert call(ti=addr(6)) == -4 and call(tl=addr(0) + 63 * 1000) == -4
@@ -111,7 +111,7 @@ def test_linear_logprobs_rejects_bad_arguments(lib):
     for name in ("b", "t", "lp", "lse", "ent"):
         assert call(**{name: addr(8) + 1}) == -3, name
     assert call(rows=-1) == -1 and call(K=0) == -1 and call(V=0) == -1
-    assert call(K=60) == -2 and call(K=(1 << 20) + 8) == -2 and call(V=(1 << 30) + 1) == -2
+    assert call(K=60) == -2 and call(K=(1 << 20) + 8) == -2 and call(V=(1 << 24) + 1) == -2
     assert call(rows=(1 << 28) + 1) == -2 and call(rows=1 << 27, V=1 << 14) == -2
     assert call(ws=None) == -7 and call(ws=addr(7) + 128) == -7 and call(ws_bytes=need - 1) == -7
     assert call(lp=addr(5)) == -4 and call(lse=addr(1) + 64) == -4 and call(ws=addr(0)) == -4 and call(ent=addr(7) + 16) == -4

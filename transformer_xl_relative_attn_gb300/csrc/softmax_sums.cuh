@@ -14,16 +14,18 @@
 // times -inf).  Either nothing below kLow is added, whose power is 0 and whose product with
 // it too; or a batch is added with no look at its values, and once more with it where that
 // was not fine (in linear_logprobs, where two instructions for each logit cost a tenth of the
-// time).  A reference beyond +-kHuge is the maximum: numbers lie 1e28 and more apart there,
-// and s counts those equal to it.  m starts at the lowest finite number, which is beyond
-// -kHuge and equals no -inf.  A NaN or +inf among the values makes s and t NaN.
+// time).  A reference from +-kHuge on is the maximum: numbers lie 64 and more apart there, where
+// r's rounding would leave the powers' range, and s counts those equal to it.  m starts at the
+// lowest finite number, which is beyond -kHuge and equals no -inf.  A NaN or +inf among the
+// values makes s and t NaN.
 #pragma once
 #include <cuda_bf16.h>
 
 namespace txl {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLow = -1e38f, kHuge = 1e36f;
+constexpr float kLow = -1e38f;    // (bf16 and fp32 hold it, and x L - r of it is finite)
+constexpr float kHuge = 0x1p29f;  // r is off by 32 at most below it
 constexpr float kSlack = 4.f;
 constexpr float kMuch = 0x1p30f;  // a sum beyond it has too low a reference: its logarithm's rounding grows with it
 constexpr float kLowest = -1e20f;  // differences of references are held at or above it (times 2^30 terms it is finite)

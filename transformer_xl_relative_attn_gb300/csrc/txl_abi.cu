@@ -690,9 +690,11 @@ int linear_bwd_sizes(int x_layout, int B, int T, int K, int N) {
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Logits: 2^31 - 1 rows, 2^30 columns and 2^40 elements at most.
+// Logits: 2^31 - 1 rows, 2^24 columns (a thread's chain of additions stays below 2^13) and 2^40
+// elements at most.
+constexpr int kMostColumns = 1 << 24;
 bool logit_rows_too_large(long long rows, int V, long long ld) {
-    return V > (1 << 30) || rows > 0x7FFFFFFFll || ld > (1ll << 40) || rows > (1ll << 40) / ld;
+    return V > kMostColumns || rows > 0x7FFFFFFFll || ld > (1ll << 40) || rows > (1ll << 40) / ld;
 }
 
 // Bytes from the first row's begin to the last one's end.
@@ -700,7 +702,7 @@ size_t row_span(long long rows, int V, long long ld, int es) { return ((size_t)(
 
 int linear_logprobs_sizes(long long rows, int K, int V) {
     if (rows < 0 || K <= 0 || V <= 0) return TXL_ERR_INVALID_ARG;
-    if (K % 8 != 0 || K > (1 << 20) || V > (1 << 30) || rows > (1ll << 28) || rows > (1ll << 40) / V) return TXL_ERR_UNSUPPORTED;
+    if (K % 8 != 0 || K > (1 << 20) || V > kMostColumns || rows > (1ll << 28) || rows > (1ll << 40) / V) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
 }
 

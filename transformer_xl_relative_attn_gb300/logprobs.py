@@ -141,7 +141,7 @@ def token_logprobs_bwd(logits, tokens, lse, dlogprob=None, dlse=None, dentropy=N
                  out.data_ptr(), ldd, code, _stream(stream, dev))
     if rc != 0:
         raise TxlError(rc, "txl_token_logprobs_bwd")
-    if out.data_ptr() == logits.data_ptr():
+    if out.data_ptr() == logits.data_ptr() and not out.is_inference():
         increment_version([out])  # what was computed from the logits is not differentiated any more
     return out
 
