@@ -55,7 +55,8 @@ struct Cfg {
     static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
     static constexpr uint32_t OFF_B = STAGES * SZ_A;
     static constexpr uint32_t OFF_BAR = OFF_B + STAGES * SZ_B;
-    static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
+    static constexpr uint32_t OFF_BIAS = OFF_BAR + 512;       // of each epilogue warp's columns, fp32
+    static constexpr uint32_t SMEM_BYTES = OFF_BIAS + 8 * (BN / 2) * 4 + 1024;
     static constexpr uint32_t IDESC = idesc_bf16_f32(TM, BN, 0, 0);
     static_assert(SMEM_BYTES <= 232448, "shared memory budget of one sm_103a CTA");
 };
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
         constexpr int chunks = BN / 64, half = 32 * chunks;  // 32-column chunks per warp; its columns
         const uint32_t t_row = tmem + ((uint32_t)(wq * 32) << 16) + half * chalf;
         const uint32_t acc_empty0 = PAIR ? lb_mapa(&sh->acc_empty[0], 0) : 0;
+        float4* const my_bias = reinterpret_cast<float4*>(smem + C::OFF_BIAS) + (warp - 4) * (half / 4);
         bool ok = true;
         int j = 0;
         for (int i = unit; ok && i < items; i += units) {
@@ -260,9 +262,9 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     for (int x = 0; x < 32; ++x) sums.add_far(z[x]);
                 }
             };
-            // A chunk of the accumulator, columns n .. n + 31 of the logits.  (Two copies of the
-            // sums: with what the bias and the end of V change in the first, it took 2 % longer.)
-            auto take = [&](const uint32_t (&q)[32], int n) {
+            // A chunk of the accumulator, columns n .. n + 31 of the logits, c of this warp's.  (Two
+            // copies of the sums: with what the end of V changes in the first, it took 2 % longer.)
+            auto take = [&](const uint32_t (&q)[32], int n, int c) {
                 float z[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x) z[x] = __uint_as_float(q[x]);
@@ -271,31 +273,50 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     return;
                 }
                 float w[32];
-                if (BIAS && p.wide_bias && n + 32 <= p.V) {
-                    const uint4* const b4 = reinterpret_cast<const uint4*>(p.bias + n);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const uint4 b = __ldg(b4 + h);
-                        const uint32_t e[4] = {b.x, b.y, b.z, b.w};
+                for (int x = 0; x < 32; x += 4) {
+                    if (BIAS) {
+                        const float4 b = my_bias[8 * c + x / 4];
+                        const float2 lo = sm_add2(make_float2(z[x], z[x + 1]), make_float2(b.x, b.y));
+                        const float2 hi = sm_add2(make_float2(z[x + 2], z[x + 3]), make_float2(b.z, b.w));
+                        w[x] = lo.x, w[x + 1] = lo.y, w[x + 2] = hi.x, w[x + 3] = hi.y;
+                    } else {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            w[8 * h + 2 * x] = z[8 * h + 2 * x] + __uint_as_float(e[x] << 16);
-                            w[8 * h + 2 * x + 1] = z[8 * h + 2 * x + 1] + __uint_as_float(e[x] & 0xFFFF0000u);
-                        }
+                        for (int k = 0; k < 4; ++k) w[x + k] = n + x + k < p.V ? z[x + k] : -INFINITY;
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        w[x] = n + x < p.V ? z[x] + (BIAS ? __bfloat162float(p.bias[n + x]) : 0.f) : -INFINITY;
                 }
                 add(w);
             };
+            // The bias of this warp's columns from n on, four per lane; -inf behind V, which masks them.
+            auto load_bias = [&](int n) {
+                float4 b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                n += 4 * lane;
+                if (4 * lane >= half || n >= p.V) return b;
+                if (p.wide_bias && n + 4 <= p.V) {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+                    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+                }
+                b.x = __bfloat162float(p.bias[n]);
+                if (n + 1 < p.V) b.y = __bfloat162float(p.bias[n + 1]);
+                if (n + 2 < p.V) b.z = __bfloat162float(p.bias[n + 2]);
+                if (n + 3 < p.V) b.w = __bfloat162float(p.bias[n + 3]);
+                return b;
+            };
+            float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);  // the next tile's
+            if (BIAS) ahead = load_bias(it.v0 * BN + half * chalf);
             for (int v = it.v0; v < it.v1; ++v, ++j) {
                 const int acc = j & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh->acc_full[acc], (j >> 1) & 1, kDevTimeoutSoftmax, abort, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 const int n0 = v * BN + half * chalf;
+                if (BIAS) {
+                    __syncwarp();  // the last tile's has been read
+                    if (4 * lane < half) my_bias[lane] = ahead;
+                    __syncwarp();
+                    if (v + 1 < it.v1) ahead = load_bias((v + 1) * BN + half * chalf);
+                }
                 const uint32_t from = t_row + acc * MAX_BN;
                 // the logits of the tokens that lie in these columns, row by row (few do)
                 for (unsigned has = __ballot_sync(0xffffffffu, token >= n0 && token < n0 + half && token < p.V); has; has &= has - 1) {
@@ -319,7 +340,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                                 mbar_arrive(&sh->acc_empty[acc]);
                         }
                     }
-                    take(q, n0 + 32 * c);
+                    take(q, n0 + 32 * c, c);
                 }
             }
             if (ok && row < p.rows) {
@@ -496,7 +517,7 @@ cudaError_t launch_linear_logprobs(LpPlan pl, const void* x, const void* w, cons
     LpParams& p = pl.p;
     p.tokens = tokens;
     p.bias = static_cast<const __nv_bfloat16*>(bias);
-    p.wide_bias = (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
+    p.wide_bias = (reinterpret_cast<uintptr_t>(bias) & 7u) == 0;
     p.part = static_cast<float4*>(workspace);
     p.given = reinterpret_cast<float*>(p.part + (size_t)p.chunks * 2 * p.rows);
     p.status = status;

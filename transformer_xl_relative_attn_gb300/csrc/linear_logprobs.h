@@ -13,7 +13,7 @@ struct LpParams {
     int per, chunks;       // column tiles of an item; items per row tile
     const long long* tokens;
     const __nv_bfloat16* bias;  // [V] or null
-    int wide_bias;         // bias is 16-byte aligned
+    int wide_bias;         // bias is 8-byte aligned
     float4* part;          // [rows][2 chunks]: (m, s, t) of each half of an item's columns
     float* given;          // [rows]: the token's logit
     int* status;
