@@ -14,7 +14,7 @@
 //
 // Alternatives are ordered as 64-bit keys: the value's order, then the complement of the
 // index, so that no two are alike.  In the pass over the row a thread only notes which two
-// of its 16-byte vectors have the largest values, and the largest of the others (14
+// of its 16-byte vectors have the largest values, and the largest of the others (10
 // instructions a vector; keeping the best in order as they come took the kernel twice its
 // time).  Behind it the threads' best elements are put in order, by sorting within warps
 // and by rank among the warps' lists, and the k-th of them is a bar: a second element of a
@@ -310,7 +310,7 @@ __device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, con
     } else {
         // A batch is on its way while the one before is worked on (1001 x 50021: 37 us, one at
         // a time 55; in bf16, whose batches have twice the elements and whose CTAs would be
-        // fewer, 11264 x 32768 took 134 us so and takes 112 one at a time).
+        // fewer, 11264 x 32768 took 134 us so and 112 one at a time).
         Vec<T> w[U];
         if (sh.first < sh.end) load(v, sh.first);
 #pragma unroll 1
