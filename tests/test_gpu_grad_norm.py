@@ -179,6 +179,40 @@ def test_the_memory_lives_as_long_as_the_object():
     assert torch.equal(n.norm, want)
 
 
+def test_more_than_2_to_32_elements():
+    x = torch.full((2 ** 32 + 5,), 0.5, device="cuda", dtype=BF)
+    x[-3:] = 4096.0
+    n = txl.GradNorm([x, x[:8].clone()])
+    n.clip(256.0)
+    want = math.sqrt((2 ** 32 + 2) * 0.25 + 3 * 4096.0 ** 2)
+    assert abs(float(n.norms[0]) / want - 1) <= relative(n.grads)
+    factor = 256.0 / math.sqrt(want ** 2 + 8 * 0.25)
+    half = 2.0 ** -8 + 1e-5
+    assert abs(float(x[0]) / (0.5 * factor) - 1) <= half and abs(float(x[-1]) / (4096 * factor) - 1) <= half
+    assert bool((x[: -3] == x[0]).all()) and bool((x[-3:] == x[-1]).all())
+
+
+def test_the_library_call_alone():
+    """Without norms; a workspace of the size asked for, and nothing written behind it."""
+    from transformer_xl_relative_attn_gb300 import _lib
+
+    lib = txl.load()
+    grads = make([70000, 0, 33], (BF, F32), seed=12)
+    table = (_lib.GradTensor * 3)()
+    for i, g in enumerate(grads):
+        table[i] = _lib.GradTensor(g.data_ptr(), g.numel(), txl.TXL_BF16 if g.dtype is BF else txl.TXL_F32, 0)
+    need = lib.txl_grad_norm_workspace_bytes(table, 3)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    norm = torch.zeros(2, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.txl_grad_norm(table, 3, 0.0, norm.data_ptr(), None, ws.data_ptr(), need, stream) == 0
+    want = float(reference(grads)[1])
+    assert abs(float(norm[0]) / want - 1) <= relative(grads) and float(norm[1]) == 0.0
+    assert bool((ws[need:] == 255).all())
+    assert lib.txl_grad_norm(table, 3, want / 2, norm.data_ptr(), None, ws.data_ptr(), need, stream) == 0
+    assert abs(float(reference(grads)[1]) / want * 2 - 1) <= 1e-2
+
+
 def test_bad_tensors_are_refused():
     x = torch.zeros(64, 64, device="cuda")
     for bad, error in (([x.t()[:, :5]], ValueError), ([x, x.cpu()], ValueError), ([x.double()], TypeError), ([x.half()], TypeError),
