@@ -357,6 +357,10 @@ long long piece_bytes_of(const txl_grad_tensor* tensors, int n) {
     const long long most = 8ll * current_sm_count();
     return std::max(4ll, (total + most * kStep - 1) / (most * kStep)) * kStep;
 }
+long long pieces_of(const txl_grad_tensor& t, long long piece_bytes) {
+    const long long n = bytes_of(t);
+    return n <= piece_bytes ? n > 0 : (n + piece_bytes - 1) / piece_bytes;
+}
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, cudaStream_t stream, Args... args) {
@@ -384,7 +388,7 @@ cudaError_t each_group(const GradNormArgs& a, long long piece_bytes, F f) {
         for (; i < a.n_tensors && t.n < CAP; ++i) {
             const txl_grad_tensor& x = a.tensors[i];
             t.e[t.n++] = {x.grad, x.n, (unsigned)at, x.dtype == TXL_BF16};
-            at += (bytes_of(x) + piece_bytes - 1) / piece_bytes;
+            at += pieces_of(x, piece_bytes);
         }
         t.pieces = (unsigned)at;
         const cudaError_t e = f(t, first, i0);
@@ -396,7 +400,7 @@ cudaError_t each_group(const GradNormArgs& a, long long piece_bytes, F f) {
 
 template <int CAP>
 cudaError_t run(const GradNormArgs& a, cudaStream_t stream) {
-    const long long piece = piece_bytes_of(a.tensors, a.n_tensors), pieces = grad_norm_pieces(a.tensors, a.n_tensors);
+    const long long piece = a.plan.piece_bytes, pieces = a.plan.pieces;
     Sum* const part = static_cast<Sum*>(a.workspace);
     cudaError_t e = each_group<CAP>(a, piece, [&](const GradTable<CAP>& t, long long first, int) {
         return t.pieces ? launch_pdl(grad_sums_kernel<CAP>, t.pieces, stream, t, piece, part + first, (unsigned)(pieces - first))
@@ -417,14 +421,13 @@ cudaError_t run(const GradNormArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-long long grad_norm_pieces(const txl_grad_tensor* tensors, int n) {
-    const long long piece = piece_bytes_of(tensors, n);
-    long long pieces = 0;
-    for (int i = 0; i < n; ++i) pieces += (bytes_of(tensors[i]) + piece - 1) / piece;
-    return pieces;
+GradNormPlan grad_norm_plan(const txl_grad_tensor* tensors, int n) {
+    GradNormPlan p = {piece_bytes_of(tensors, n), 0};
+    for (int i = 0; i < n; ++i) p.pieces += pieces_of(tensors[i], p.piece_bytes);
+    return p;
 }
 
-size_t grad_norm_workspace_bytes(long long pieces) { return ((size_t)pieces * sizeof(Sum) + 255) / 256 * 256; }
+size_t grad_norm_workspace_bytes(const GradNormPlan& plan) { return ((size_t)plan.pieces * sizeof(Sum) + 255) / 256 * 256; }
 
 cudaError_t launch_grad_norm(const GradNormArgs& a, cudaStream_t stream) {
     if (a.n_tensors <= kSmallTable) return run<kSmallTable>(a, stream);

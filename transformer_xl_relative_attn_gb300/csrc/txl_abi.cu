@@ -959,7 +959,7 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
 
 size_t txl_grad_norm_workspace_bytes(const txl_grad_tensor* tensors, int n_tensors) {
     return grad_tensors_status(tensors, n_tensors) == TXL_OK
-               ? txl::grad_norm_workspace_bytes(txl::grad_norm_pieces(tensors, n_tensors))
+               ? txl::grad_norm_workspace_bytes(txl::grad_norm_plan(tensors, n_tensors))
                : 0;
 }
 
@@ -971,26 +971,39 @@ int txl_grad_norm(const txl_grad_tensor* tensors, int n_tensors, double max_norm
     const int rc = grad_tensors_status(tensors, n_tensors);
     if (rc != TXL_OK) return rc;
     if (!aligned_to(norm, 4) || !aligned_to(norms, 4)) return TXL_ERR_MISALIGNED;
-    const size_t need = txl_grad_norm_workspace_bytes(tensors, n_tensors);
+    const txl::GradNormPlan plan = txl::grad_norm_plan(tensors, n_tensors);
+    const size_t need = txl::grad_norm_workspace_bytes(plan);
     if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
-    std::vector<Range> r;
-    try {
-        r.reserve((size_t)n_tensors + 3);
-    } catch (const std::bad_alloc&) {
-        return TXL_ERR_UNSUPPORTED;
-    }
+    const Range own[] = {range_of(norm, sizeof(float), true), range_of(norms, (size_t)n_tensors * sizeof(float), true),
+                         range_of(workspace, need, true)};
+    bool rising = true;  // each tensor behind the one before: none overlaps another
+    uintptr_t end = 0;
     for (int i = 0; i < n_tensors; ++i) {
         const txl_grad_tensor& t = tensors[i];
         if (t.n == 0) continue;
         if (!t.grad) return TXL_ERR_INVALID_ARG;
         if (!aligned16(t.grad)) return TXL_ERR_MISALIGNED;
-        r.push_back(range_of(t.grad, (size_t)t.n * elem_size(t.dtype), max_norm > 0.0));
+        const Range g = range_of(t.grad, (size_t)t.n * elem_size(t.dtype), false);
+        rising = rising && g.at >= end;
+        end = g.end;
+        for (const Range& o : own)
+            if (o.at && o.at < g.end && g.at < o.end) return TXL_ERR_ALIAS;
     }
-    r.push_back(range_of(norm, sizeof(float), true));
-    r.push_back(range_of(norms, (size_t)n_tensors * sizeof(float), true));
-    r.push_back(range_of(workspace, need, true));
-    if (any_written_overlap(r.data(), r.size())) return TXL_ERR_ALIAS;
-    const txl::GradNormArgs a = {tensors, n_tensors, max_norm, norm, norms, workspace};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (own[i].at && own[j].at && own[i].at < own[j].end && own[j].at < own[i].end) return TXL_ERR_ALIAS;
+    if (max_norm > 0.0 && !rising) {
+        std::vector<Range> r;
+        try {
+            r.reserve((size_t)n_tensors);
+        } catch (const std::bad_alloc&) {
+            return TXL_ERR_UNSUPPORTED;
+        }
+        for (int i = 0; i < n_tensors; ++i)
+            if (tensors[i].n) r.push_back(range_of(tensors[i].grad, (size_t)tensors[i].n * elem_size(tensors[i].dtype), true));
+        if (any_written_overlap(r.data(), r.size())) return TXL_ERR_ALIAS;
+    }
+    const txl::GradNormArgs a = {tensors, n_tensors, plan, max_norm, norm, norms, workspace};
     return cuda_status(txl::launch_grad_norm(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -458,6 +458,8 @@ class GradNorm(_Bound):
         self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         with torch.cuda.device(dev):
             self._made()
+        # (views of one tensor share its version counter)
+        self._versions = list({id(t if t._base is None else t._base): t for t in self.grads}.values())
         types = _lib.load().txl_grad_norm.argtypes
         args = (self.norm.data_ptr(), self.norms.data_ptr(), self._workspace.data_ptr(), need)
         self._args = tuple(of(a) for of, a in zip(types[3:], args))
@@ -484,4 +486,4 @@ class GradNorm(_Bound):
         if not max_norm > 0:
             raise ValueError("max_norm must be positive")
         self._call(float(max_norm), stream)
-        increment_version(self.grads)
+        increment_version(self._versions)
