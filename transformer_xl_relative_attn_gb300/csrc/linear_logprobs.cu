@@ -426,12 +426,23 @@ bool lp_encode(CUtensorMap* map, const void* base, long long rows, int K, int hi
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Microseconds that a stage takes at 256 columns and at least, and that an item's end adds.
-constexpr double kStepPair = 0.36, kStepOne = 0.36, kStepLeast = 0.15, kItem = 1.0;
+// Microseconds that a tile takes, as measured over K of 64 to 1024 and tiles of 64 to 256
+// columns: its stages, or, where those are few, what lies between two of its accumulators (a
+// pair's hand-over goes through both CTAs) and the epilogue.  A single CTA's stages take longer, as
+// it loads as many rows of W for half the rows of x, its hand-over half the time: 11264 rows to
+// 32768 columns take pairs and single CTAs 156 and 111 us with K of 256, 199 and 219 with 512.
+double lp_tile_us(bool pair, int bn, int ksteps, bool lines, bool bias) {
+    const double w = (double)bn / lp::MAX_BN;
+    // (rows of W that do not begin on 128-byte lines take longer to load)
+    const double step = pair ? (0.10 + 0.23 * w) * (lines ? 1.0 : 1.3) : (0.16 + 0.20 * w) * (lines ? 1.0 : 1.5);
+    const double apart = (pair ? 0.9 + (0.75 + 0.14 * ksteps) * w : 0.25 + w) + (bias ? 0.4 * w : 0.0);
+    return std::max(step * ksteps, apart);
+}
+constexpr double kItem = 1.0;  // that an item's end adds
 
 }  // namespace
 
-LpPlan linear_logprobs_plan(int rows, int K, int V) {
+LpPlan linear_logprobs_plan(int rows, int K, int V, bool bias) {
     LpPlan pl = {};
     LpParams& p = pl.p;
     p.rows = rows;
@@ -449,12 +460,12 @@ LpPlan linear_logprobs_plan(int rows, int K, int V) {
         const bool few = (double)rt * ((double)V / lp::MAX_BN) < 16.0 * most;
         for (int bn = lp::MAX_BN; bn >= (few ? 64 : lp::MAX_BN); bn -= 64) {
             const int vt = (int)(((long long)V + bn - 1) / bn);
-            const double step = std::max(kStepLeast, (ctas == 2 ? kStepPair : kStepOne) * bn / lp::MAX_BN);
+            const double us = lp_tile_us(ctas == 2, bn, p.ksteps, K % lp::BK == 0, bias);
             for (int rounds = 1; rounds <= (few ? 4 : 24); ++rounds) {
                 const int runs = (int)std::max(1ll, std::min<long long>(vt, (long long)most * rounds / rt));
                 const int per = (vt + runs - 1) / runs, chunks = (vt + per - 1) / per;
                 const long long items = (long long)rt * chunks, units = std::min<long long>(items, most);
-                const double cost = (double)((items + units - 1) / units) * (per * p.ksteps * step + kItem);
+                const double cost = (double)((items + units - 1) / units) * (per * us + kItem);
                 if (best >= 0 && cost >= best) continue;
                 best = cost;
                 pl.pair = ctas == 2;

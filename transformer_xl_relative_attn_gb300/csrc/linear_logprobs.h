@@ -25,7 +25,7 @@ struct LpPlan {
     LpParams p;
 };
 
-LpPlan linear_logprobs_plan(int rows, int K, int V);
+LpPlan linear_logprobs_plan(int rows, int K, int V, bool bias);
 size_t linear_logprobs_workspace_bytes(const LpPlan& plan);
 // Of x [rows, K], w [V, K] and bias [V] (may be null), bf16, K a multiple of 8.
 // cudaErrorInvalidValue: a tensor map could not be encoded.

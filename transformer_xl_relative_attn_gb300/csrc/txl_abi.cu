@@ -853,7 +853,8 @@ int txl_token_logprobs_bwd(const void* logits, long long ld, const long long* to
 
 size_t txl_linear_logprobs_workspace_bytes(long long rows, int K, int V) {
     if (linear_logprobs_sizes(rows, K, V) != TXL_OK || rows == 0) return 0;
-    return txl::linear_logprobs_workspace_bytes(txl::linear_logprobs_plan((int)rows, K, V));
+    return std::max(txl::linear_logprobs_workspace_bytes(txl::linear_logprobs_plan((int)rows, K, V, false)),
+                    txl::linear_logprobs_workspace_bytes(txl::linear_logprobs_plan((int)rows, K, V, true)));
 }
 
 int txl_linear_logprobs(const void* x, const void* w, const void* bias, const long long* tokens, long long rows, int K,
@@ -866,8 +867,8 @@ int txl_linear_logprobs(const void* x, const void* w, const void* bias, const lo
     if (!aligned16(x) || !aligned16(w) || !aligned_to(bias, 2) || !aligned_to(tokens, 8) || !aligned_to(logprob, 4) ||
         !aligned_to(lse, 4) || !aligned_to(entropy, 4))
         return TXL_ERR_MISALIGNED;
-    const txl::LpPlan plan = txl::linear_logprobs_plan((int)rows, K, V);
-    const size_t need = txl::linear_logprobs_workspace_bytes(plan);
+    const txl::LpPlan plan = txl::linear_logprobs_plan((int)rows, K, V, bias != nullptr);
+    const size_t need = txl_linear_logprobs_workspace_bytes(rows, K, V);
     if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
     const size_t nr = (size_t)rows * sizeof(float);
     Range r[] = {range_of(x, (size_t)rows * K * 2, false), range_of(w, (size_t)V * K * 2, false),
