@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
     const uint32_t s_base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lb_cta_rank() : 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 1) lb_tmem_alloc<PAIR>(&sh->tmem_base, TMEM_COLS);
     if (threadIdx.x == 0) {
@@ -132,6 +131,8 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
     if (PAIR) __syncthreads();
     lb_sync<PAIR>();
     tc_fence_after();
+    // (not before the CTA has its tensor memory: a kernel that got ahead would hold it and wait for this one)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = sh->tmem_base;
     volatile int* abort = &sh->abort;
@@ -238,8 +239,11 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             const LpItem it = lp_item(p, i);
             const int row = it.r * TM + BM * rank + 32 * wq + lane;
             const long long token = row < p.rows ? p.tokens[row] : -1;
-            SoftmaxPairs sums;
+            // a tile's sums, and those of the tiles before it: one chain of additions through all of
+            // a run would round each way as often as it has columns
+            SoftmaxPairs sums, before;
             sums.clear();
+            before.clear();
             auto add = [&](const float (&z)[32]) {
                 const SoftmaxPairs was = sums;
                 if (sm_ordinary(sums.m)) {
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
 #pragma unroll
                 for (int x = 2; x < 32; x += 2) most = sm_max3(most, z[x], z[x + 1]);
                 sums.raise(most);
+                if (sums.m != before.m) before.follow(sums.m);
                 if (sm_ordinary(sums.m)) {
                     const float r = sm_reference(sums.m);
 #pragma unroll
@@ -342,12 +347,13 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     }
                     take(q, n0 + 32 * c, c);
                 }
+                before.take(sums);
             }
             if (ok && row < p.rows) {
                 const int slot = 2 * it.run + chalf;
                 if (TXL_BOUNDS(row < p.rows && slot < 2 * p.chunks, 1302, slot))
                     p.part[(long long)row * (2 * p.chunks) + slot] =
-                        make_float4(sums.m, sums.s.x + sums.s.y, sums.t.x + sums.t.y, 0.f);
+                        make_float4(before.m, before.s.x + before.s.y, before.t.x + before.t.y, 0.f);
             }
         }
     }
@@ -439,6 +445,7 @@ double lp_tile_us(bool pair, int bn, int ksteps, bool lines, bool bias) {
     return std::max(step * ksteps, apart);
 }
 constexpr double kItem = 1.0;  // that an item's end adds
+constexpr int kMostTiles = 2048;  // of an item, whose sums are added one after the other
 
 }  // namespace
 
@@ -463,7 +470,7 @@ LpPlan linear_logprobs_plan(int rows, int K, int V, bool bias) {
             const double us = lp_tile_us(ctas == 2, bn, p.ksteps, K % lp::BK == 0, bias);
             for (int rounds = 1; rounds <= (few ? 4 : 24); ++rounds) {
                 const int runs = (int)std::max(1ll, std::min<long long>(vt, (long long)most * rounds / rt));
-                const int per = (vt + runs - 1) / runs, chunks = (vt + per - 1) / per;
+                const int per = std::min((vt + runs - 1) / runs, kMostTiles), chunks = (vt + per - 1) / per;
                 const long long items = (long long)rt * chunks, units = std::min<long long>(items, most);
                 const double cost = (double)((items + units - 1) / units) * (per * us + kItem);
                 if (best >= 0 && cost >= best) continue;

@@ -133,14 +133,21 @@ struct SoftmaxPairs {
     __device__ __forceinline__ void clear() { m = -3.402823466e38f, s = t = make_float2(0.f, 0.f); }
     // Ahead of values of which `to` is the largest.
     __device__ __forceinline__ void raise(float to) {
-        if (to > m + kSlack) {
-            float d;
-            const float f = sm_factor(m, to, d);
-            const float2 ff = make_float2(f, f);
-            t = sm_mul2(ff, sm_fma2(make_float2(d, d), s, t));
-            s = sm_mul2(ff, s);
-            m = to;
-        }
+        if (to > m + kSlack) follow(to);
+    }
+    // The same sums against another reference, to >= m.
+    __device__ __forceinline__ void follow(float to) {
+        float d;
+        const float f = sm_factor(m, to, d);
+        const float2 ff = make_float2(f, f);
+        t = sm_mul2(ff, sm_fma2(make_float2(d, d), s, t));
+        s = sm_mul2(ff, s);
+        m = to;
+    }
+    // Takes over the other's sums, whose reference is the same one.
+    __device__ __forceinline__ void take(SoftmaxPairs& o) {
+        s = sm_add2(s, o.s), t = sm_add2(t, o.t);
+        o.s = o.t = make_float2(0.f, 0.f);
     }
     // Two values, m ordinary, r = sm_reference(m).
     __device__ __forceinline__ void add(float2 x, float r) {

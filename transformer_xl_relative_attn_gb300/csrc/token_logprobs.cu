@@ -246,6 +246,8 @@ struct Noted {
     }
 };
 
+constexpr int kBatches = 64;  // even, as they are taken two by two
+
 // A warp's vectors are first + lane + i step, i = 0, 1, .., below `end`; with `loose` it has
 // the elements outside the vectors too.
 struct Share {
@@ -301,27 +303,37 @@ __device__ __forceinline__ void scan(const T* row, int V, const RowCut& cut, con
     };
     const int stride = U * sh.step;
     Vec<T> v[U];
-    if constexpr (sizeof(T) == 2) {
+    // A chain of additions has kBatches batches at most; the chains are added one by one.
+    int base = sh.first;
+    do {
+        const int end = sh.end - base > kBatches * stride ? base + kBatches * stride : sh.end;
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll 1
-        for (int base = sh.first; base < sh.end; base += stride) {
-            load(v, base);
-            take(v, base);
-        }
-    } else {
-        // A batch is on its way while the one before is worked on (1001 x 50021: 37 us, one at
-        // a time 55; in bf16, whose batches have twice the elements and whose CTAs would be
-        // fewer, 11264 x 32768 took 134 us so and 112 one at a time).
-        Vec<T> w[U];
-        if (sh.first < sh.end) load(v, sh.first);
+            for (; base < end; base += stride) {
+                load(v, base);
+                take(v, base);
+            }
+        } else {
+            // A batch is on its way while the one before is worked on (1001 x 50021: 37 us, one at
+            // a time 55; in bf16, whose batches have twice the elements and whose CTAs would be
+            // fewer, 11264 x 32768 took 134 us so and 112 one at a time).
+            Vec<T> w[U];
+            if (base < end) load(v, base);
 #pragma unroll 1
-        for (int base = sh.first; base < sh.end; base += 2 * stride) {
-            if (base + stride < sh.end) load(w, base + stride);
-            take(v, base);
-            if (base + 2 * stride < sh.end) load(v, base + 2 * stride);
-            if (base + stride < sh.end) take(w, base + stride);
+            for (; base < end; base += 2 * stride) {
+                if (base + stride < end) load(w, base + stride);
+                take(v, base);
+                if (base + 2 * stride < end) load(v, base + 2 * stride);
+                if (base + stride < end) take(w, base + stride);
+            }
         }
-    }
-    sums = acc.fold();
+        if (end <= sh.first + kBatches * stride) {
+            sums = acc.fold();
+        } else {
+            sums.merge(acc.fold());
+        }
+        acc.clear();
+    } while (base < sh.end);
     if (sh.loose && lane < cut.loose) {
         const int at = cut.index<T>(lane);
         if (TXL_BOUNDS(at < V, 1102, at)) sums.add(load_one(row + at));

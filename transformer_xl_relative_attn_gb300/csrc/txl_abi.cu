@@ -690,7 +690,7 @@ int linear_bwd_sizes(int x_layout, int B, int T, int K, int N) {
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Logits: 2^31 - 1 rows, 2^24 columns (a thread's chain of additions stays below 2^13) and 2^40
+// Logits: 2^31 - 1 rows, 2^24 columns (a thread's chains of additions stay below 2^11) and 2^40
 // elements at most.
 constexpr int kMostColumns = 1 << 24;
 bool logit_rows_too_large(long long rows, int V, long long ld) {
@@ -868,7 +868,9 @@ int txl_linear_logprobs(const void* x, const void* w, const void* bias, const lo
         !aligned_to(lse, 4) || !aligned_to(entropy, 4))
         return TXL_ERR_MISALIGNED;
     const txl::LpPlan plan = txl::linear_logprobs_plan((int)rows, K, V, bias != nullptr);
-    const size_t need = txl_linear_logprobs_workspace_bytes(rows, K, V);
+    // (a workspace serves calls with a bias and without)
+    const size_t need = std::max(txl::linear_logprobs_workspace_bytes(plan),
+                                 txl::linear_logprobs_workspace_bytes(txl::linear_logprobs_plan((int)rows, K, V, bias == nullptr)));
     if (bad_workspace(workspace, ws_bytes, need)) return TXL_ERR_WORKSPACE;
     const size_t nr = (size_t)rows * sizeof(float);
     Range r[] = {range_of(x, (size_t)rows * K * 2, false), range_of(w, (size_t)V * K * 2, false),
