@@ -490,3 +490,12 @@ def test_bad_tensors_are_refused():
     with pytest.raises(txl.TxlError) as e:
         txl.token_logprobs(x, t, outs=outs)
     assert e.value.code == -4
+
+
+@pytest.mark.parametrize("top,V,code", [(2 ** 30, 64, -1), (2 ** 40, 64, -1), (40, 64, -2), (33, 32, -1)])
+def test_counts_beyond_the_limit_are_refused_ahead_of_buffers_for_them(top, V, code):
+    x, t = make(1000, V, BF)
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    with pytest.raises(txl.TxlError) as e:
+        txl.token_logprobs(x, t, top=top)
+    assert e.value.code == code and torch.cuda.memory_stats()["allocation.all.allocated"] == before

@@ -12,6 +12,7 @@ from ._lib import TXL_BF16, TXL_F32, TxlError, _invoke, _need, _stream
 from .train import _INT_MAX, _on, _ptr, _scratch, _workspace_need
 
 _F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
+_TOP_MOST = 32
 _CODES = {_BF16: TXL_BF16, _F32: TXL_F32}
 
 
@@ -56,15 +57,32 @@ def _on_gpu(t, name: str, device=None) -> None:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
 
 
-def _statistics(shape, dev, outs):
-    """logprob, lse, entropy: the caller's, or new ones (three allocations take 6 us, parts
-    of one buffer 12)."""
+def _new(shape, top: int, dev):
+    """New outputs: logprob, lse, entropy, and with top its two (an allocation each; parts of one
+    buffer take twice the time)."""
+    logprob = torch.empty(shape, dtype=_F32, device=dev)
+    lse = torch.empty(shape, dtype=_F32, device=dev)
+    entropy = torch.empty(shape, dtype=_F32, device=dev)
+    if not top:
+        return logprob, lse, entropy, None, None
+    shape = (*shape, top)
+    return logprob, lse, entropy, torch.empty(shape, dtype=_I64, device=dev), torch.empty(shape, dtype=_F32, device=dev)
+
+
+def _outputs(shape, top: int, dev, stream, outs):
+    """logprob, lse, entropy, top_index, top_logprob: the caller's, or new ones."""
     if outs is None:
-        return (torch.empty(shape, dtype=_F32, device=dev), torch.empty(shape, dtype=_F32, device=dev),
-                torch.empty(shape, dtype=_F32, device=dev))
+        if stream is None:
+            return _new(shape, top, dev)
+        with _on(stream, dev):
+            return _new(shape, top, dev)
     for n in ("logprob", "lse", "entropy"):
         _need(outs[n], n, shape, _F32, dev)
-    return outs["logprob"], outs["lse"], outs["entropy"]
+    if not top:
+        return outs["logprob"], outs["lse"], outs["entropy"], None, None
+    _need(outs["top_index"], "top_index", (*shape, top), _I64, dev)
+    _need(outs["top_logprob"], "top_logprob", (*shape, top), _F32, dev)
+    return outs["logprob"], outs["lse"], outs["entropy"], outs["top_index"], outs["top_logprob"]
 
 
 def token_logprobs(logits, tokens, top=0, stream=None, outs=None):
@@ -81,19 +99,9 @@ def token_logprobs(logits, tokens, top=0, stream=None, outs=None):
     _need(tokens, "tokens", shape, _I64, dev)
     if not isinstance(top, int) or top < 0:
         raise ValueError("top must be a count")
-    if max(V, rows, top) > _INT_MAX:
-        raise TxlError(-2, "txl_token_logprobs")
-    index = value = None
-    with _on(stream, dev):
-        logprob, lse, entropy = _statistics(shape, dev, outs)
-        if top:
-            if outs is None:
-                index = torch.empty((*shape, top), dtype=_I64, device=dev)
-                value = torch.empty((*shape, top), dtype=_F32, device=dev)
-            else:
-                index, value = outs["top_index"], outs["top_logprob"]
-                _need(index, "top_index", (*shape, top), _I64, dev)
-                _need(value, "top_logprob", (*shape, top), _F32, dev)
+    if V > _INT_MAX or rows > _INT_MAX or top > _TOP_MOST:  # (ahead of buffers for so many)
+        raise TxlError(-1 if top > V else -2, "txl_token_logprobs")
+    logprob, lse, entropy, index, value = _outputs(shape, top, dev, stream, outs)
     rc = _invoke(dev, "txl_token_logprobs", logits.data_ptr(), ld, tokens.data_ptr(), rows, V, top, logprob.data_ptr(),
                  lse.data_ptr(), entropy.data_ptr(), _ptr(index), _ptr(value), code, _stream(stream, dev))
     if rc != 0:
@@ -126,11 +134,15 @@ def token_logprobs_bwd(logits, tokens, lse, dlogprob=None, dlse=None, dentropy=N
     if dentropy is not None:
         _need(dentropy, "dentropy", shape, _F32, dev)
         _need(entropy, "entropy", shape, _F32, dev)
-    if max(V, rows) > _INT_MAX:
+    if V > _INT_MAX or rows > _INT_MAX:
         raise TxlError(-2, "txl_token_logprobs_bwd")
     if out is None:
-        with _on(stream, dev):
-            out, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=dev), V
+        if stream is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        else:
+            with _on(stream, dev):
+                out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        ldd = V
     else:
         if not isinstance(out, torch.Tensor) or out.shape != logits.shape or out.dtype is not logits.dtype:
             raise ValueError(f"out must be a tensor {tuple(logits.shape)} of {logits.dtype}")
@@ -175,15 +187,16 @@ def linear_logprobs(x, w, tokens, bias=None, stream=None, workspace=None, outs=N
     _need(tokens, "tokens", shape, _I64, dev)
     rows = x.numel() // K
     need = _workspace_need(dev.index, "txl_linear_logprobs_workspace_bytes", rows, K, V)
-    with _on(stream, dev):
-        logprob, lse, entropy = _statistics(shape, dev, outs)
-        if workspace is not None:
-            at = _scratch(workspace, need, dev)
-        elif need:
+    logprob, lse, entropy, _, _ = _outputs(shape, 0, dev, stream, outs)
+    if workspace is not None:
+        at = _scratch(workspace, need, dev)
+    elif stream is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        at = workspace.data_ptr()
+    else:
+        with _on(stream, dev):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            at = workspace.data_ptr()
-        else:
-            at = 0
+        at = workspace.data_ptr()
     rc = _invoke(dev, "txl_linear_logprobs", x.data_ptr(), w.data_ptr(), _ptr(bias), tokens.data_ptr(), rows, K, V,
                  logprob.data_ptr(), lse.data_ptr(), entropy.data_ptr(), at, need, _stream(stream, dev))
     if rc != 0:
