@@ -110,13 +110,16 @@ def test_logits_far_from_zero(base):
             assert bool((got["entropy"] >= 0).all()) and bool((got["entropy"] <= math.log(V) + 1e-4).all())
 
 
-def test_long_runs_of_alike_logits():
+# of 152 SMs each has 128 rows, or two of them 256, and all columns; more tiles than an item takes;
+# the most columns there may be, nearly
+@pytest.mark.parametrize("rows,V", [(19456, 262144), (19456, 600001), (130, (1 << 24) - 3)])
+def test_long_runs_of_alike_logits(rows, V):
     """One logit of 0 and V - 1 at one distance c below it: every addition of a thread rounds the same
     way, so that one chain through a run's columns (65536 of them) is off by up to 9e-4.  A term is off
-    by U (3 |c| + 4), a tile's sums are 64 additions at most, a run's V / 256 tiles, and 6 U go to
-    each merge of a few parts; logarithm and results round by U (2 ls + lse).  In the entropy, ls - t / s,
-    t / s is -A, and off by twice as much as s."""
-    rows, V = 19456, 262144  # of 152 SMs each has 128 rows, or two of them 256, and all columns
+    by U (3 |c| + 4), a tile's sums are 64 additions at most, a run's one for each of its tiles (2048 at
+    most), and 6 U go to each merge: a lane's, of two parts for each of an item's runs (24 rounds of 152
+    SMs at most), and a few more; logarithm and results round by U (2 ls + lse).  In the entropy,
+    ls - t / s, t / s is -A, and off by twice as much as s."""
     x, w = torch.zeros(rows, 8, device="cuda", dtype=BF), torch.zeros(V, 8, device="cuda", dtype=BF)
     c = -(torch.arange(rows, device="cuda") % 190 + 2).double() / 64
     x[:, 0], w[1:, 0] = c.to(BF), 1.0
@@ -124,7 +127,8 @@ def test_long_runs_of_alike_logits():
     got = txl.linear_logprobs(x, w, t)
     s = 1 + (V - 1) * c.exp()
     ls, A = s.log(), -(V - 1) * c.exp() * c / s
-    sums = U * (3 * c.abs() + 4 + 64 + V / 256 + 60) + 2 * U * ls
+    merges = 2 * min(V / 256, 24 * 152) / 32 + 10
+    sums = U * (3 * c.abs() + 4 + 64 + min(V / 256, 2048) + 6 * merges) + 2 * U * ls
     tol = {"lse": sums + U * ls, "entropy": sums + A * (2 * sums + 4 * U) + U * (ls + A), "logprob": sums + U * (c.abs() + ls)}
     ref = {"lse": ls, "entropy": ls + A, "logprob": torch.where(t == 0, 0.0, c) - ls}
     for k in ref:
