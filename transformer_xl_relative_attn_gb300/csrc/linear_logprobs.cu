@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             SoftmaxPairs sums, before;
             sums.clear();
             before.clear();
-            auto add = [&](const float (&z)[32]) {
+            auto add = [&](float (&z)[32], int n) {
                 const SoftmaxPairs was = sums;
                 if (sm_ordinary(sums.m)) {
                     const float r = sm_reference(sums.m);
@@ -252,6 +252,11 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     for (int x = 0; x < 32; x += 2) sums.add(make_float2(z[x], z[x + 1]), r);
                     if (sums.fine()) return;
                     sums = was;
+                }
+                if (BIAS && n + 32 > p.V) {  // the sum with a bias of -inf is NaN where 0 met an infinite x
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (n + x >= p.V) z[x] = -INFINITY;
                 }
                 float most = fmaxf(z[0], z[1]);
 #pragma unroll
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
 #pragma unroll
                 for (int x = 0; x < 32; ++x) z[x] = __uint_as_float(q[x]);
                 if (!BIAS && n + 32 <= p.V) {
-                    add(z);
+                    add(z, n);
                     return;
                 }
                 float w[32];
@@ -290,9 +295,10 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                         for (int k = 0; k < 4; ++k) w[x + k] = n + x + k < p.V ? z[x + k] : -INFINITY;
                     }
                 }
-                add(w);
+                add(w, n);
             };
-            // The bias of this warp's columns from n on, four per lane; -inf behind V, which masks them.
+            // The bias of this warp's columns from n on, four per lane; -inf behind V, by which no chunk with
+            // such columns is fine.
             auto load_bias = [&](int n) {
                 float4 b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
                 n += 4 * lane;
