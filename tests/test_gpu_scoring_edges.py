@@ -35,3 +35,29 @@ def test_an_infinite_hidden_state_leaves_nothing(rows, K, V):
         assert bool((got["lse"][hit] == -INF).all()) and bool((got["entropy"][hit] == 0).all())
         assert bool((got["logprob"][hit] == torch.where(t < 0, 0.0, -INF)[hit]).all())
         assert all(torch.equal(got[key][~hit], want[key][~hit]) for key in want)
+
+
+@pytest.mark.parametrize("rows,V", [(19456, 256), (19456, 2048), (300, 2048), (19456, 262144)])
+def test_a_run_that_begins_far_below_what_counts(rows, V):
+    """The first 32 columns of each half of a tile lie L below all others, whose logits are 0.  Once a
+    thread's reference is at those, their terms are 1 and their sums whole numbers, which fp32 holds:
+    what is left are the low columns' part q e^-L of S, off by U (3 L / ln 2 + 64 + 60) of itself and
+    times L + 1 in the entropy, and the logarithm, quotient and products of the results (6 U ls + 4 U).
+    For L from 3 on, as 32 columns of e^3 weigh more than four times the columns of a half tile."""
+    low = torch.zeros(V, dtype=torch.bool, device="cuda")
+    low[:32] = low[128:160] = True
+    L = (3.0 + torch.arange(rows, device="cuda") % 35 * 0.5).double()
+    x, w = torch.zeros(rows, 8, device="cuda", dtype=BF), torch.zeros(V, 8, device="cuda", dtype=BF)
+    x[:, 0], w[low, 0] = L.to(BF), -1.0
+    t = torch.arange(rows, device="cuda") % 100
+    got = txl.linear_logprobs(x, w, t)
+    q = 64 * (-L).exp()
+    s = V - 64 + q
+    ls, part = s.log(), q / s * U * (3 * L / math.log(2) + 124)
+    given = torch.where(low[t], -L, 0.0)
+    ref = {"lse": ls, "entropy": ls + q * L / s, "logprob": given - ls}
+    tol = {"lse": part + 6 * U * ls + 4 * U, "entropy": part * (L + 1) + (6 * ls + 4 + q * L / s) * U,
+           "logprob": part + U * (L + 7 * ls + 4)}
+    for k in ref:
+        off = (got[k].double() - ref[k]).abs()
+        assert bool((off <= tol[k]).all()), (k, float(off.max()), float((off / tol[k]).max()))

@@ -240,7 +240,13 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             const int row = it.r * TM + BM * rank + 32 * wq + lane;
             const long long token = row < p.rows ? p.tokens[row] : -1;
             // a tile's sums, and those of the tiles before it: one chain of additions through all of
-            // a run would round each way as often as it has columns
+            // a run would round each way as often as it has columns.  Both against one reference, which
+            // follows the maximum of a chunk with which a tile's terms are `much` (262144 logits in one
+            // run, alike but for the first 32, which lie 15.5 lower: their entropy was off by 3.3e-4 with
+            // 2^30 as much, and is by 1.4e-6; by 3.6e-5 at most where they lie 1.25 lower, which makes the
+            // others' terms just less than much.  A look at the sums behind each tile too would make that
+            // 1e-5, for a 140th of the time)
+            constexpr float much = 4.f * half;
             SoftmaxPairs sums, before;
             sums.clear();
             before.clear();
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                     const float r = sm_reference(sums.m);
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) sums.add(make_float2(z[x], z[x + 1]), r);
-                    if (sums.fine()) return;
+                    if (sums.fine(much)) return;
                     sums = was;
                 }
                 if (BIAS && n + 32 > p.V) {  // the sum with a bias of -inf is NaN where 0 met an infinite x
@@ -261,8 +267,7 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                 float most = fmaxf(z[0], z[1]);
 #pragma unroll
                 for (int x = 2; x < 32; x += 2) most = sm_max3(most, z[x], z[x + 1]);
-                sums.raise(most);
-                if (sums.m != before.m) before.follow(sums.m);
+                if (most > sums.m) sums.follow(most), before.follow(most);
                 if (sm_ordinary(sums.m)) {
                     const float r = sm_reference(sums.m);
 #pragma unroll
@@ -270,6 +275,11 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                 } else {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) sums.add_far(z[x]);
+                }
+                const float terms = sums.s.x + sums.s.y;
+                if (terms > 2.f * half) {  // made much by the chunks before: on to where all are on average
+                    const float to = sums.m + __logf(terms / half);
+                    if (sm_ordinary(to)) sums.follow(to), before.follow(to);
                 }
             };
             // A chunk of the accumulator, columns n .. n + 31 of the logits, c of this warp's.  (Two

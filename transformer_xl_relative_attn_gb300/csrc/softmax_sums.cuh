@@ -7,8 +7,11 @@
 // The reference is r itself, so that its rounding is no error, and a term costs one fused
 // product before its power of two; that L is off by 1.3e-8 of itself is a temperature off
 // by as much.  When the reference moves from m to M, with d = r(m) - r(M) <= 0, the sums
-// become s 2^d and 2^d (t + d s).  m need not be the maximum itself: it follows once a value
-// is kSlack above it (moved each time, some lane of a warp had to in most of the steps).
+// become s 2^d and 2^d (t + d s).  m need not be the maximum itself (moved each time, some lane of a
+// warp had to in most of the steps), but log2 s and t / s then carry its distance, which cancels
+// between them but for their roundings.  Where the values' maximum is at hand (token_logprobs) m
+// follows it once it is kSlack above; where it is not (linear_logprobs) once the terms of a tile
+// are four times as much as the columns they may be of.
 //
 // What is not ordinary: a value of -inf, or one so low that x L - r is, would make t NaN (0
 // times -inf).  Either nothing below kLow is added, whose power is 0 and whose product with
@@ -27,7 +30,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1e38f;    // (bf16 and fp32 hold it, and x L - r of it is finite)
 constexpr float kHuge = 0x1p29f;  // r is off by 32 at most below it
 constexpr float kSlack = 4.f;
-constexpr float kMuch = 0x1p30f;  // a sum beyond it has too low a reference: its logarithm's rounding grows with it
 constexpr float kLowest = -1e20f;  // differences of references are held at or above it (times 2^30 terms it is finite)
 
 __device__ __forceinline__ float sm_ex2(float x) {
@@ -159,10 +161,10 @@ struct SoftmaxPairs {
     // The same where values may be below kLow.
     __device__ __forceinline__ void add_low(float2 x, float r) { add(make_float2(sm_max_nan(x.x, kLow), sm_max_nan(x.y, kLow)), r); }
     // Whether values that nothing was known of were added as they should: the sum is neither
-    // large, for which the reference has to follow, nor NaN, and t is none either.
-    __device__ __forceinline__ bool fine() const {
+    // `much`, for which the reference has to follow, nor NaN, and t is none either.
+    __device__ __forceinline__ bool fine(float much) const {
         const float a = s.x + s.y, b = t.x + t.y;
-        return a < kMuch && b == b;
+        return a < much && b == b;
     }
     // One value not above m (or NaN), where m is not ordinary.
     __device__ __forceinline__ void add_far(float x) { s.x += x == m ? (x - x) + 1.f : x != x ? x : 0.f; }
