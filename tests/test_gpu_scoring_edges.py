@@ -61,3 +61,26 @@ def test_a_run_that_begins_far_below_what_counts(rows, V):
     for k in ref:
         off = (got[k].double() - ref[k]).abs()
         assert bool((off <= tol[k]).all()), (k, float(off.max()), float((off / tol[k]).max()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("limit,norm", [(1e-3, 1e38), (1e-6, 2e38), (1e-8, 2e38), (2.0 ** -126, 3e38), (2.0 ** -100, 2.0 ** 27), (1e-30, 1e9)])
+def test_clipping_by_a_factor_below_the_range(dtype, limit, norm):
+    """max_norm / norm is below 2^-126, the clipped gradients mostly are not: norm and limit are off by
+    24 U (as a root half of 4 additions of a thread's, 21 in a CTA, 14 for the pieces, and a square's
+    rounding), a quotient and two products by 4 U, besides the type's rounding and that to the type's
+    smallest step."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    unit = torch.empty(9000, device="cuda", dtype=torch.float64).normal_(generator=g)
+    unit[:5] = torch.tensor([0.0, 1e-20, -30.0, 50.0, 1e-3], device="cuda")
+    grads = [(p * (norm / unit.norm()).item()).to(dtype) for p in (unit[:4001], unit[4001:])]
+    was = [p.double() for p in grads]
+    length = torch.cat(was).norm()
+    n = txl.GradNorm(grads)
+    n.clip(limit)
+    assert abs(float(n.norm) / float(length) - 1) <= 24 * U
+    half, tiny = torch.finfo(dtype).eps / 2, 2.0 ** -149 if dtype is F32 else 2.0 ** -133
+    for p, q in zip(grads, was):
+        ref = q * (limit / length)
+        e = 28 * U
+        assert bool(((p.double() - ref).abs() <= ref.abs() * (e + half * (1 + e)) + tiny).all())

@@ -110,6 +110,21 @@ __device__ __forceinline__ float over_cta(float a, float (&sh)[kWarps]) {
     return a;
 }
 
+// max_norm / norm as a factor, and a power of two (1 as a rule) that a value is multiplied by behind
+// it: a quotient below 2^-126 would lose its bits, where the product need not.
+struct Factor {
+    float f, down;
+    __device__ __forceinline__ Factor(float max_norm, float norm) : f(max_norm / norm), down(1.f) {
+        if (f < 0x1p-126f) {
+            const int m = ilogbf(max_norm), n = ilogbf(norm), a = (n - m) / 2 - 1;
+            f = ldexpf(ldexpf(max_norm, -m) / ldexpf(norm, -n), -a);
+            down = ldexpf(1.f, a - (n - m));
+        }
+    }
+    // (rounded by the first product alone, unless the result is below 2^-126)
+    __device__ __forceinline__ float operator()(float x) const { return x * f * down; }
+};
+
 // A piece of a tensor: elements [at, at + n) of `of`.
 struct Piece {
     char* p;  // of the first element
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     const float length = s.norm();
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = length;
     if (!CLIP || !(length > max_norm && length < INFINITY) || blockIdx.x >= t.pieces) return;
-    const float factor = max_norm / length;
+    const Factor scaled(max_norm, length);
     const unsigned b = t.pieces - 1 - blockIdx.x;
     const int e = find_entry(t, b);
     const Piece c = piece_of(t, e, b, piece_bytes);
@@ -323,12 +338,12 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 f = bf16_pair(w[k]);
-                    w[k] = pack_bf16x2(f.x * factor, f.y * factor);
+                    w[k] = pack_bf16x2(scaled(f.x), scaled(f.y));
                 }
                 o = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
-                o = make_uint4(__float_as_uint(__uint_as_float(v[u].x) * factor), __float_as_uint(__uint_as_float(v[u].y) * factor),
-                               __float_as_uint(__uint_as_float(v[u].z) * factor), __float_as_uint(__uint_as_float(v[u].w) * factor));
+                o = make_uint4(__float_as_uint(scaled(__uint_as_float(v[u].x))), __float_as_uint(scaled(__uint_as_float(v[u].y))),
+                               __float_as_uint(scaled(__uint_as_float(v[u].z))), __float_as_uint(scaled(__uint_as_float(v[u].w))));
             }
             if (i < vecs && TXL_BOUNDS(c.at >= 0 && c.at + (i + 1) * n <= c.of, 1205, c.at + i * n))
                 store16(c.p + i * 16, o);
@@ -338,9 +353,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     if ((int)threadIdx.x < left && TXL_BOUNDS(c.at + vecs * n + threadIdx.x < c.of, 1206, threadIdx.x)) {
         if (bf16) {
             __nv_bfloat16* const p = reinterpret_cast<__nv_bfloat16*>(c.p + vecs * 16) + threadIdx.x;
-            *p = __float2bfloat16_rn(__bfloat162float(*p) * factor);
+            *p = __float2bfloat16_rn(scaled(__bfloat162float(*p)));
         } else {
-            reinterpret_cast<float*>(c.p + vecs * 16)[threadIdx.x] *= factor;
+            float* const p = reinterpret_cast<float*>(c.p + vecs * 16) + threadIdx.x;
+            *p = scaled(*p);
         }
     }
 }
