@@ -84,3 +84,15 @@ def test_clipping_by_a_factor_below_the_range(dtype, limit, norm):
         ref = q * (limit / length)
         e = 28 * U
         assert bool(((p.double() - ref).abs() <= ref.abs() * (e + half * (1 + e)) + tiny).all())
+
+
+@pytest.mark.parametrize("dtype,value", [(BF, 1.546875), (BF, 1.515625), (F32, 1.406510353088379)])
+def test_long_sums_of_alike_gradients(dtype, value):
+    """16 GB of one value: the chains of additions do not grow with the gradients (128 of a thread's,
+    one for each 16 rounds of its piece, 21 in a CTA, 18 for the pieces; half of it in the norm)."""
+    x = torch.full((2 ** 33 if dtype is BF else 2 ** 32,), value, device="cuda", dtype=dtype)
+    n = txl.GradNorm([x])
+    n.measure()
+    want = float(x[0].double()) * math.sqrt(x.numel())
+    assert abs(float(n.norm) / want - 1) <= U * ((128 + 27 + 21 + 18) / 2 + 2)
+    assert abs(float(n.norms[0]) / want - 1) <= U * ((128 + 27 + 21 + 1216 / 32 + 5) / 2 + 2)
