@@ -96,3 +96,25 @@ def test_long_sums_of_alike_gradients(dtype, value):
     want = float(x[0].double()) * math.sqrt(x.numel())
     assert abs(float(n.norm) / want - 1) <= U * ((128 + 27 + 21 + 18) / 2 + 2)
     assert abs(float(n.norms[0]) / want - 1) <= U * ((128 + 27 + 21 + 1216 / 32 + 5) / 2 + 2)
+
+
+@pytest.mark.parametrize("count", [3000, 5000, 300_000])
+def test_many_small_tensors(count):
+    """Alike ones: the additions of all tensors' sums do not grow with their number (a thread's chains
+    of 64, then one for each chain, 13 in a CTA, 6 of a piece's own)."""
+    flat = torch.full((count, 4), 1.406510353088379, device="cuda")
+    flat[:, 3] = 0.0
+    n = txl.GradNorm(list(flat.unbind(0)))
+    n.measure()
+    want = float(flat[0, 0].double()) * math.sqrt(3 * count)
+    tol = U * ((64 + count / 256 / 64 + 13 + 6) / 2 + 2)
+    assert abs(float(n.norm) / want - 1) <= tol
+    each = float(flat[0, 0].double()) * math.sqrt(3)
+    assert bool(((n.norms.double() / each - 1).abs() <= 8 * U).all())
+    first = n.norm.clone(), flat.clone()
+    n.clip(want * 2)
+    assert torch.equal(n.norm, first[0]) and torch.equal(flat, first[1])
+    n.clip(want / 3)
+    assert torch.equal(n.norm, first[0])
+    assert bool(((flat.double() / (first[1][0, 0].double() / 3) - (flat != 0).double()).abs() <= tol + 4 * U).all())
+    assert bool((flat[:, 3] == 0).all()) and bool((flat[:, :3] == flat[0, 0]).all())

@@ -3,8 +3,8 @@
 //
 // Two launches.  The first cuts the tensors into pieces, one per CTA, and leaves the sum
 // of squares of each; in the second every CTA adds all pieces' sums, in the same order,
-// so that each has the norm without a launch in between that finds it, and scales a piece
-// of its own.  The pieces come in the opposite order then: the last ones read are still in
+// so that each has the norm without a launch in between that finds it (but where tensors
+// are many), and scales a piece of its own.  The pieces come in the opposite order then: the last ones read are still in
 // L2.  Both are bound by memory; nothing is written where nothing is clipped.
 //
 // Sums are fp32 throughout, in chains of 128 additions and then of those, for a piece whose
@@ -34,6 +34,10 @@ constexpr long long kStep = kThreads * 16;         // bytes that a CTA's threads
 // takes less time (37.8 M bf16 gradients: 10.5 us, with it 11.2).
 constexpr int kRounds = 16;
 constexpr long long kShort = kRounds * kLoads * kStep;
+// Up to so many pieces each CTA that scales adds all their sums itself; more, as many small tensors
+// have, are added once in a launch of their own (clipped, us, without and with it: 1000 small tensors
+// 20 and 22, 2000 39 and 37, 5000 112 and 85, 100000 16000 and 1700).
+constexpr long long kFewPieces = 1800;
 constexpr int kSmallTable = 32, kMiddleTable = 160, kLargeTable = 480;  // tensors per launch
 constexpr int kNothing = -(1 << 20);               // exponent of a sum that is 0
 
@@ -297,15 +301,30 @@ __device__ __forceinline__ Total total_by_cta(const Sum* part, unsigned n, float
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < R; ++k) x += ldexpf(own[k].x, max(own[k].e - most, -200));
-    for (unsigned i = threadIdx.x + R * kThreads; i < n; i += kThreads) {
-        const Sum s = part[i];
-        x += ldexpf(s.x, max(s.e - most, -200));
+    for (unsigned i = threadIdx.x + R * kThreads; i < n;) {  // (in chains of 64, as many tensors are many sums)
+        const unsigned end = n - i > 64 * kThreads ? i + 64 * kThreads : n;
+        float chain = 0.f;
+        for (; i < end; i += kThreads) {
+            const Sum s = part[i];
+            chain += ldexpf(s.x, max(s.e - most, -200));
+        }
+        x += chain;
     }
     return {over_cta<false>(x, sh), most};
 }
 
-// Norms from the sums, and a piece's scaling.  `all`, `n_all`: the sums of every launch's pieces;
-// `part`: this one's.
+// The total of n sums, which stands in their place for the scaling where they are many.
+__global__ void __launch_bounds__(kThreads) grad_total_kernel(const Sum* __restrict__ part, unsigned n, Sum* __restrict__ total) {
+    __shared__ float sh[kWarps];
+    __shared__ int she[kWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Total t = total_by_cta(part, n, sh, she);
+    if (threadIdx.x == 0) *total = {t.x, t.e};
+}
+
+// Norms from the sums, and a piece's scaling.  `all`, `n_all`: the sums of every launch's pieces, or
+// their total; `part`: this one's.
 template <int CAP, bool CLIP>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, long long piece_bytes,
                                                              const Sum* __restrict__ all, unsigned n_all,
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
             if (lane == 0) norms[e] = s.norm();
         }
     }
-    if (!CLIP && blockIdx.x) return;
+    if (!CLIP && (blockIdx.x || !norm)) return;
     const Total s = total_by_cta(all, n_all, sh, she);
     const float length = s.norm();
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = length;
@@ -438,14 +457,21 @@ cudaError_t run(const GradNormArgs& a, cudaStream_t stream) {
                         : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
+    const Sum* all = part;
+    unsigned n_all = (unsigned)pieces;
+    if (a.max_norm > 0 && pieces > kFewPieces) {
+        e = launch_pdl(grad_total_kernel, 1, stream, (const Sum*)part, n_all, part + pieces);
+        if (e != cudaSuccess) return e;
+        all = part + pieces, n_all = 1;
+    }
     return each_group<CAP>(a, piece, [&](const GradTable<CAP>& t, long long first, int i0) {
         float* const norm = i0 ? nullptr : a.norm;
         float* const norms = a.norms ? a.norms + i0 : nullptr;
         const unsigned by_norms = (unsigned)(t.n + kWarps - 1) / kWarps;
         if (a.max_norm > 0)
-            return launch_pdl(grad_norm_kernel<CAP, true>, std::max(1u, t.pieces), stream, t, piece, (const Sum*)part,
-                              (unsigned)pieces, (const Sum*)(part + first), (float)a.max_norm, norm, norms);
-        return launch_pdl(grad_norm_kernel<CAP, false>, norms ? by_norms : 1u, stream, t, piece, (const Sum*)part, (unsigned)pieces,
+            return launch_pdl(grad_norm_kernel<CAP, true>, std::max(1u, t.pieces), stream, t, piece, all, n_all,
+                              (const Sum*)(part + first), (float)a.max_norm, norm, norms);
+        return launch_pdl(grad_norm_kernel<CAP, false>, norms ? by_norms : 1u, stream, t, piece, all, n_all,
                           (const Sum*)(part + first), 0.f, norm, norms);
     });
 }
@@ -458,7 +484,10 @@ GradNormPlan grad_norm_plan(const txl_grad_tensor* tensors, int n) {
     return p;
 }
 
-size_t grad_norm_workspace_bytes(const GradNormPlan& plan) { return ((size_t)plan.pieces * sizeof(Sum) + 255) / 256 * 256; }
+size_t grad_norm_workspace_bytes(const GradNormPlan& plan) {
+    const long long sums = plan.pieces + (plan.pieces > kFewPieces);  // (the total)
+    return ((size_t)sums * sizeof(Sum) + 255) / 256 * 256;
+}
 
 cudaError_t launch_grad_norm(const GradNormArgs& a, cudaStream_t stream) {
     if (a.n_tensors <= kSmallTable) return run<kSmallTable>(a, stream);
