@@ -118,3 +118,15 @@ def test_many_small_tensors(count):
     assert torch.equal(n.norm, first[0])
     assert bool(((flat.double() / (first[1][0, 0].double() / 3) - (flat != 0).double()).abs() <= tol + 4 * U).all())
     assert bool((flat[:, 3] == 0).all()) and bool((flat[:, :3] == flat[0, 0]).all())
+
+
+def test_alternatives_counted_by_a_numpy_integer():
+    np = pytest.importorskip("numpy")
+    x, t = torch.randn(5, 300, device="cuda"), torch.zeros(5, dtype=torch.int64, device="cuda")
+    want = txl.token_logprobs(x, t, top=3)
+    for count in (np.int64(3), np.int32(3)):
+        got = txl.token_logprobs(x, t, top=count)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    for count in (3.0, "3", None, -1, np.int64(-1)):
+        with pytest.raises(ValueError, match="count"):
+            txl.token_logprobs(x, t, top=count)

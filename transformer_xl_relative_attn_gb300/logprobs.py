@@ -5,6 +5,8 @@ Argument marshalling and buffers only: every step of the computation runs in
 libtxl.so's CUDA kernels."""
 from __future__ import annotations
 
+import operator
+
 import torch
 from torch.autograd.graph import increment_version
 
@@ -97,7 +99,12 @@ def token_logprobs(logits, tokens, top=0, stream=None, outs=None):
     rows, V, ld = _rows(logits, "logits")
     code, dev, shape = _type_of(logits, "logits"), logits.device, logits.shape[:-1]
     _need(tokens, "tokens", shape, _I64, dev)
-    if not isinstance(top, int) or top < 0:
+    if type(top) is not int:  # an integer of another type, as NumPy's are
+        try:
+            top = int(operator.index(top))
+        except TypeError:
+            raise ValueError("top must be a count") from None
+    if top < 0:
         raise ValueError("top must be a count")
     if V > _INT_MAX or rows > _INT_MAX or top > _TOP_MOST:  # (ahead of buffers for so many)
         raise TxlError(-1 if top > V else -2, "txl_token_logprobs")
