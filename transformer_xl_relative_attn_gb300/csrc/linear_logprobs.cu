@@ -90,6 +90,13 @@ __device__ __forceinline__ LpItem lp_item(const LpParams& p, int i) {
     return it;
 }
 
+// Whether a part or a token's logit lies in the workspace.
+template <typename T>
+__device__ __forceinline__ bool lp_in_workspace(const LpParams& p, const T* at) {
+    return reinterpret_cast<const char*>(at) >= reinterpret_cast<const char*>(p.part) &&
+           reinterpret_cast<const char*>(at + 1) <= p.ws_end;
+}
+
 // One column of an accumulator, a row per lane.
 __device__ __forceinline__ float lp_tmem_column(uint32_t taddr) {
     uint32_t r;
@@ -332,7 +339,9 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                 const int n0 = v * BN + half * chalf;
                 if (BIAS) {
                     __syncwarp();  // the last tile's has been read
-                    if (4 * lane < half) my_bias[lane] = ahead;
+                    if (4 * lane < half &&
+                        TXL_BOUNDS(smem_u32(my_bias + lane + 1) <= smem_u32(smem_raw) + C::SMEM_BYTES, 1304, lane))
+                        my_bias[lane] = ahead;
                     __syncwarp();
                     if (v + 1 < it.v1) ahead = load_bias((v + 1) * BN + half * chalf);
                 }
@@ -340,9 +349,10 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
                 // the logits of the tokens that lie in these columns, row by row (few do)
                 for (unsigned has = __ballot_sync(0xffffffffu, token >= n0 && token < n0 + half && token < p.V); has; has &= has - 1) {
                     const int src = __ffs(has) - 1, n = __shfl_sync(0xffffffffu, (int)token, src);
+                    if (!TXL_BOUNDS(n - v * BN >= 0 && n - v * BN < BN && acc * MAX_BN + n - v * BN < (int)TMEM_COLS, 1306, n)) continue;
                     float g = lp_tmem_column(from + (n - n0));
                     if (BIAS) g += __bfloat162float(p.bias[n]);
-                    if (lane == src && TXL_BOUNDS(row < p.rows, 1301, row)) p.given[row] = g;
+                    if (lane == src && TXL_BOUNDS(lp_in_workspace(p, p.given + row), 1301, row)) p.given[row] = g;
                 }
                 // Columns behind V hold 0 times x, which is NaN where x is not finite, and that with the bias
                 // of -inf too.  (Selected in the sums instead, wherever in them, 4 % more time with K of 256.)
@@ -372,9 +382,9 @@ __global__ void __launch_bounds__(lp::NTHREADS, 1) linear_logprobs_kernel(const 
             }
             if (ok && row < p.rows) {
                 const int slot = 2 * it.run + chalf;
-                if (TXL_BOUNDS(row < p.rows && slot < 2 * p.chunks, 1302, slot))
-                    p.part[(long long)row * (2 * p.chunks) + slot] =
-                        make_float4(before.m, before.s.x + before.s.y, before.t.x + before.t.y, 0.f);
+                float4* const to = p.part + ((long long)row * (2 * p.chunks) + slot);
+                if (TXL_BOUNDS(slot < 2 * p.chunks && lp_in_workspace(p, to) && to < reinterpret_cast<const float4*>(p.given), 1302, slot))
+                    *to = make_float4(before.m, before.s.x + before.s.y, before.t.x + before.t.y, 0.f);
             }
         }
     }
@@ -399,14 +409,16 @@ __global__ void __launch_bounds__(256) linear_logprobs_join_kernel(const LpParam
     if (r >= p.rows) return;
     const long long token = p.tokens[r];
     const float4* const q = p.part + (long long)r * n;
-    const float given = token >= 0 && token < p.V ? p.given[r] : 0.f;
+    const float given = token >= 0 && token < p.V && TXL_BOUNDS(lp_in_workspace(p, p.given + r), 1305, r) ? p.given[r] : 0.f;
     SoftmaxSums a;
     a.clear();
     for (int i = lane; i < n; i += 32 * 8) {  // 8 on their way at a time
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            v[u] = i + 32 * u < n && TXL_BOUNDS(r < p.rows && i + 32 * u < n, 1303, r) ? q[i + 32 * u] : make_float4(-3.402823466e38f, 0.f, 0.f, 0.f);
+            v[u] = i + 32 * u < n && TXL_BOUNDS(lp_in_workspace(p, q + i + 32 * u), 1303, r)
+                       ? q[i + 32 * u]
+                       : make_float4(-3.402823466e38f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const SoftmaxSums b = {v[u].x, v[u].y, v[u].z};
@@ -551,7 +563,7 @@ cudaError_t lp_launch(const LpMaps& maps, const LpPlan& pl, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_linear_logprobs(LpPlan pl, const void* x, const void* w, const void* bias, int K, const long long* tokens,
-                                   float* logprob, float* lse, float* entropy, void* workspace, int* status,
+                                   float* logprob, float* lse, float* entropy, void* workspace, size_t ws_bytes, int* status,
                                    cudaStream_t stream) {
     LpParams& p = pl.p;
     p.tokens = tokens;
@@ -559,6 +571,7 @@ cudaError_t launch_linear_logprobs(LpPlan pl, const void* x, const void* w, cons
     p.wide_bias = (reinterpret_cast<uintptr_t>(bias) & 7u) == 0;
     p.part = static_cast<float4*>(workspace);
     p.given = reinterpret_cast<float*>(p.part + (size_t)p.chunks * 2 * p.rows);
+    p.ws_end = static_cast<const char*>(workspace) + ws_bytes;
     p.status = status;
     LpMaps maps;
     if (!lp_encode(&maps.x, x, p.rows, K, lp::BM) || !lp_encode(&maps.w, w, p.V, K, p.bn / (pl.pair ? 2 : 1))) return cudaErrorInvalidValue;

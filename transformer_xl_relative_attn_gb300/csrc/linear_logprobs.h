@@ -16,6 +16,7 @@ struct LpParams {
     int wide_bias;         // bias is 8-byte aligned
     float4* part;          // [rows][2 chunks]: (m, s, t) of each half of an item's columns
     float* given;          // [rows]: the token's logit
+    const char* ws_end;    // of the workspace, both buffers in it
     int* status;
 };
 
@@ -30,7 +31,7 @@ size_t linear_logprobs_workspace_bytes(const LpPlan& plan);
 // Of x [rows, K], w [V, K] and bias [V] (may be null), bf16, K a multiple of 8.
 // cudaErrorInvalidValue: a tensor map could not be encoded.
 cudaError_t launch_linear_logprobs(LpPlan plan, const void* x, const void* w, const void* bias, int K, const long long* tokens,
-                                   float* logprob, float* lse, float* entropy, void* workspace, int* status,
+                                   float* logprob, float* lse, float* entropy, void* workspace, size_t ws_bytes, int* status,
                                    cudaStream_t stream);
 
 }  // namespace txl

@@ -880,7 +880,7 @@ int txl_linear_logprobs(const void* x, const void* w, const void* bias, const lo
     if (any_written_overlap(r, sizeof(r) / sizeof(r[0]))) return TXL_ERR_ALIAS;
     int* status = dev_status_ptr();
     if (!status) return TXL_ERR_CUDA;
-    return launch_status(txl::launch_linear_logprobs(plan, x, w, bias, K, tokens, logprob, lse, entropy, workspace, status,
+    return launch_status(txl::launch_linear_logprobs(plan, x, w, bias, K, tokens, logprob, lse, entropy, workspace, need, status,
                                                      static_cast<cudaStream_t>(stream)));
 }
 
