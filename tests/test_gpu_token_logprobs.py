@@ -499,3 +499,13 @@ def test_counts_beyond_the_limit_are_refused_ahead_of_buffers_for_them(top, V, c
     with pytest.raises(txl.TxlError) as e:
         txl.token_logprobs(x, t, top=top)
     assert e.value.code == code and torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,V", [(1500, 5003), (1521, 5003), (1530, 12288), (1530, 12289), (1530, 24577), (4110, 9000), (4110, 20001)])
+def test_many_rows_on_both_sides_of_the_choice_of_threads(rows, V, dtype):
+    x, t = make(rows, V, dtype, seed=rows + V)
+    got = txl.token_logprobs(x, t)
+    check(x, t, got)
+    again = txl.token_logprobs(x, t)
+    assert all(torch.equal(got[k], again[k]) for k in got)

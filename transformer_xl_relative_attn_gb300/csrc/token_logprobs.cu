@@ -775,10 +775,14 @@ cudaError_t forward(const TokenLogprobs& a, cudaStream_t stream) {
         ctas *= 2;
     // CTAs of half the threads, and so twice as many rows at once, with alternatives, whose
     // search behind the pass leaves other rows' loads to fill the time (us, top 8, 256 and 128
-    // threads: 11264 x 32768 bf16 186 and 133, 1001 x 50021 fp32 45 and 38); without, where
-    // rows are many (11264 x 32768 bf16 108 and 106, but 1001 x 50021 fp32 37 and 40, 2432 x
-    // 50048 bf16 41 and 44).
-    const bool half = TOP || a.rows >= 4096;
+    // threads: 11264 x 32768 bf16 186 and 133, 1001 x 50021 fp32 45 and 38).  Without, where
+    // rows are many: short ones, where a CTA's begin and end weigh (1520 x 4200 bf16 6.3 and 4.9,
+    // 1824 x 24576 bf16 16 and 14, 1520 x 8200 fp32 9.5 and 7.3, 8000 x 12288 fp32 68 and 59; with
+    // 1300 x 16384 bf16 8.8 and 10, 1520 about even), and by a little others (8000 x 32768 bf16
+    // 79 and 77, fp32 146 and 143; 2432 x 32768 bf16 27.7 and 28.8).  The longest take as long or
+    // less with all threads (8000 x 65536 bf16 149 and 150, 4100 124 and 130 with 100000).
+    const long long per_sm = a.rows / current_sm_count();
+    const bool half = TOP || (bytes <= 48 * 1024 ? per_sm >= 10 : bytes <= 128 * 1024 && per_sm >= 27);
     if (ctas == 1 && half) return launch<kThreads / 2>(logprobs_cta_kernel<T, TOP, false, kThreads / 2>, a.rows, 1, stream, a);
     if (ctas == 1) return launch(logprobs_cta_kernel<T, TOP, false, kThreads>, a.rows, 1, stream, a);
     return launch(logprobs_cta_kernel<T, TOP, true, kThreads>, a.rows * ctas, ctas, stream, a);
