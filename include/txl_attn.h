@@ -413,8 +413,8 @@ int txl_linear_bwd(const void* dy, const void* x, int x_layout, int B, int T, in
  * dlogprob taken as 0 where there is no token.  lse and entropy (null without dentropy)
  * as the forward call gave them (p carries lse's rounding, 2^-24 of it).  dlogits (rows ldd elements apart) may be logits with
  * the same distance of rows: the gradient then takes their place.  A row whose gradients
- * are all 0 gets zeros whatever its logits hold, as does a row of nothing but -inf;
- * dlogprob other than 0 at a token >= V makes the row NaN.  What lies between the rows
+ * are all 0 gets zeros whatever its logits hold, as does a row of nothing but -inf (lse
+ * -inf); dlogprob other than 0 at a token >= V makes any other row NaN.  What lies between the rows
  * is left as it was.
  *
  * 0 <= rows < 2^31, 1 <= V <= 2^24, rows * max(ld, ldd) <= 2^40 (TXL_ERR_UNSUPPORTED
@@ -507,7 +507,8 @@ int txl_adamw_step(const txl_adamw_tensor* tensors, int n_tensors, int param_dty
  * read during the call; tensor i has n elements (0: its norm is 0) of type dtype (TXL_F32
  * or TXL_BF16, which may differ from tensor to tensor).  Products and sums in fp32 over
  * values scaled by powers of two where their squares would leave its range, added in a
- * fixed order (the same inputs give the same bits); a scaled value is rounded once.
+ * fixed order (the same inputs give the same bits).  A scaled value is its product with
+ * max_norm / norm in fp32, whatever the quotient's size, rounded to its type.
  * norm and norms are those before the scaling.  A norm that is not finite in fp32 leaves
  * the tensors as they were, as does one of at most max_norm.  max_norm = 0: nothing is
  * scaled, and tensors may overlap each other.
